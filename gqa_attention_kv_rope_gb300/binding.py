@@ -31,6 +31,7 @@ ERRBIT_ATTN_POS = 0x4
 ERRBIT_TIMEOUT = 0x8
 ERRBIT_BLOCK = 0x10
 ERRBIT_WORKSPACE = 0x20
+ERRBIT_CHUNK = 0x40
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -105,7 +106,23 @@ _SIGS = {
                                     _I, _F, _F, _I, _P, _P, _SZ, _P, _P], _I),
     "minf_layer_attn_step_paged_f16": ([_P, _P, _P, _F, _I, _P, _P, _P, _P, _I, _P, _P, _I64, _P, _I, _I, _I, _I,
                                         _I, _I, _F, _F, _I, _P, _P, _SZ, _P, _P], _I),
+    # chunks of new tokens: several-axis RoPE, RoPE + store into paged regions, read back, attention
+    "minf_rope_axes": ([_P, _P, _P, _I, _I, _P, _I, _I, _F, _F, _I, _P, _P], _I),
+    "minf_attn_chunk_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _SZ),
 }
+for _end in ("", "_f16", "_q8"):
+    _SIGS["minf_rope_kv_append_chunk_paged" + _end] = (
+        [_P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _I, _P, _P, _I64, _P, _I, _I, _P, _P],
+        _I)
+    _SIGS["minf_kv_read_chunk_paged" + _end] = (
+        [_P, _P, _I, _P, _P, _I64, _I, _P, _I, _I, _P, _P, _I, _I, _P, _P], _I)
+    _SIGS["minf_gqa_attn_chunk_paged" + _end] = (
+        [_P, _P, _P, _P, _I64, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _SZ, _P, _P], _I)
+    _SIGS["minf_gqa_attn_window" + _end] = (
+        [_P, _P, _P, _P, _P, _P, _I, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P, _SZ, _P, _P], _I)
+    _SIGS["minf_layer_attn_step_chunk_paged" + _end] = (
+        [_P, _P, _P, _F, _I, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _I64, _P, _I, _I, _I, _I, _I, _I, _F,
+         _F, _I, _I, _I, _P, _P, _SZ, _P, _P], _I)
 
 
 class MinfError(RuntimeError):
@@ -559,3 +576,285 @@ def minf_layer_attn_step_qkv(xn, h, gain, eps, w_qkv, b_qkv, pos, q, k, v, k_reg
         _dev(v, name="v"), _dev(k_reg, name="k_reg"), _dev(v_reg, name="v_reg"), k_reg.shape[0], n_head, n_kv_head,
         hd, hd_kv, theta, freq_scale, style, _dev(out, name="out"), _dev(ws, torch.uint8, "ws"), ws.numel(),
         _dev(err, torch.int32, "err"), _stream(stream)), "minf_layer_attn_step_qkv")
+
+
+# ----------------------------------------------------------------------------- chunks of new tokens
+# chunk_off: int32 [n_seq + 1] on the device (None: one token a sequence); n_past: int32 [n_seq];
+# pair_axis: the axis of each of the hd/2 pairs, as bytes or a sequence of ints (None: one axis).
+# These check sizes too (the library sees only pointers), and that every tensor is on the current
+# device, whose stream the call goes to.
+_CHUNK_DTYPE = {"": torch.float32, "_f16": torch.float16, "_q8": torch.uint8}
+
+
+def _on_current_device(*tensors):
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"every tensor must be on the current device (cuda:{here}), got one on {t.device}")
+
+
+def _size(name, t, n):
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _axis_bytes(pair_axis, hd):
+    if pair_axis is None:
+        return None
+    pair_axis = bytes(pair_axis)
+    if len(pair_axis) != hd // 2:
+        raise ValueError(f"pair_axis must have hd/2 = {hd // 2} entries, got {len(pair_axis)}")
+    return pair_axis
+
+
+def _chunk_seqs(chunk_off, n_past, nt):
+    n_seq = n_past.numel()
+    if chunk_off is not None:
+        _size("chunk_off", chunk_off, n_seq + 1)
+    elif nt != n_seq:
+        raise ValueError(f"without chunk_off there is one token a sequence: {nt} tokens for {n_seq} sequences")
+    return n_seq
+
+
+def _chunk_pool(end, k_pool, v_pool, block_table, n_seq, row_width):
+    cols = row_width
+    if end == "_q8":
+        if row_width % 32:
+            raise ValueError("Q8_0 rows hold whole 32-value blocks")
+        cols = row_width + ((row_width // 32) * 2 + 15) // 16 * 16
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] != k_pool.shape[0]:
+            raise ValueError(f"{name} must be [pool_rows, {cols}], the same rows for both, got {tuple(t.shape)}")
+    if block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != n_seq):
+        raise ValueError(f"block_table must be [{n_seq}, max_blocks], got {tuple(block_table.shape)}")
+
+
+def minf_rope_axes(y, x, pos, pair_axis, n_head, hd, theta, freq_scale, style, err, stream=None):
+    """pos: int32 [n_axis, nt] (or [nt] for one axis); y may be x."""
+    n_axis, nt = pos.shape if pos.dim() == 2 else (1, pos.numel())
+    _on_current_device(y, x, pos, err)
+    _size("x", x, nt * n_head * hd)
+    _size("y", y, nt * n_head * hd)
+    _check(lib().minf_rope_axes(_dev(y, name="y"), _dev(x, name="x"), _dev(pos, torch.int32, "pos"), nt, n_axis,
+                                _axis_bytes(pair_axis, hd), n_head, hd, theta, freq_scale, style,
+                                _dev(err, torch.int32, "err"), _stream(stream)), "minf_rope_axes")
+
+
+def _rope_kv_append_chunk_paged(end, q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head,
+                                hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table, block_rows, err,
+                                stream):
+    dt, w = _CHUNK_DTYPE[end], n_kv_head * hd_kv
+    nt = v.numel() // w
+    n_axis = 1 if rope_pos is None or rope_pos.dim() == 1 else rope_pos.shape[0]
+    _on_current_device(q_out, k_out, q, k, v, rope_pos, chunk_off, n_past, k_pool, v_pool, block_table, err)
+    n_seq = _chunk_seqs(chunk_off, n_past, nt)
+    _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
+    for name, t, n in (("q", q, n_head * hd), ("q_out", q_out, n_head * hd), ("k", k, w), ("k_out", k_out, w),
+                       ("v", v, w), ("rope_pos", rope_pos, n_axis)):
+        if t is not None:
+            _size(name, t, nt * n)
+    axes = _axis_bytes(pair_axis, hd)
+    if rope_pos is None and axes is not None:  # one position for every axis
+        axes = None
+    name = "minf_rope_kv_append_chunk_paged" + end
+    _check(getattr(lib(), name)(
+        _dev(q_out, name="q_out"), _dev(k_out, name="k_out"), _dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"),
+        _dev(rope_pos, torch.int32, "rope_pos"), n_axis, axes, _dev(chunk_off, torch.int32, "chunk_off"),
+        _dev(n_past, torch.int32, "n_past"), nt, n_seq, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
+        _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"), k_pool.shape[0],
+        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows, _dev(err, torch.int32, "err"),
+        _stream(stream)), name)
+
+
+def minf_rope_kv_append_chunk_paged(q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head, hd,
+                                    hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table, block_rows, err,
+                                    stream=None):
+    _rope_kv_append_chunk_paged("", q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head,
+                                hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table, block_rows, err,
+                                stream)
+
+
+def minf_rope_kv_append_chunk_paged_f16(q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head,
+                                        hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table, block_rows,
+                                        err, stream=None):
+    _rope_kv_append_chunk_paged("_f16", q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head,
+                                n_kv_head, hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table,
+                                block_rows, err, stream)
+
+
+def minf_rope_kv_append_chunk_paged_q8(q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head,
+                                       hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table, block_rows,
+                                       err, stream=None):
+    _rope_kv_append_chunk_paged("_q8", q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head,
+                                n_kv_head, hd, hd_kv, theta, freq_scale, style, k_pool, v_pool, block_table,
+                                block_rows, err, stream)
+
+
+def _kv_read_chunk_paged(end, k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err, stream):
+    dt, w = _CHUNK_DTYPE[end], k_rows.shape[-1]
+    nt = k_rows.numel() // w
+    _on_current_device(k_rows, v_rows, k_pool, v_pool, block_table, chunk_off, n_past, err)
+    n_seq = _chunk_seqs(chunk_off, n_past, nt)
+    _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
+    _size("v_rows", v_rows, nt * w)
+    rows = torch.float16 if k_rows.dtype == torch.float16 else torch.float32
+    name = "minf_kv_read_chunk_paged" + end
+    _check(getattr(lib(), name)(
+        _dev(k_rows, rows, "k_rows"), _dev(v_rows, rows, "v_rows"), rows == torch.float16, _dev(k_pool, dt, "k_pool"),
+        _dev(v_pool, dt, "v_pool"), k_pool.shape[0], w, _dev(block_table, torch.int32, "block_table"),
+        block_table.shape[1], block_rows, _dev(chunk_off, torch.int32, "chunk_off"),
+        _dev(n_past, torch.int32, "n_past"), nt, n_seq, _dev(err, torch.int32, "err"), _stream(stream)), name)
+
+
+def minf_kv_read_chunk_paged(k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
+                             stream=None):
+    """k_rows, v_rows: [nt, W] float32 or float16 (both the same)."""
+    _kv_read_chunk_paged("", k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err, stream)
+
+
+def minf_kv_read_chunk_paged_f16(k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
+                                 stream=None):
+    _kv_read_chunk_paged("_f16", k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
+                         stream)
+
+
+def minf_kv_read_chunk_paged_q8(k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
+                                stream=None):
+    _kv_read_chunk_paged("_q8", k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
+                         stream)
+
+
+def minf_attn_chunk_workspace_bytes(nt, n_seq, n_head, n_kv_head, hd_kv, max_chunk) -> int:
+    return int(lib().minf_attn_chunk_workspace_bytes(nt, n_seq, n_head, n_kv_head, hd_kv, max_chunk))
+
+
+def _attn_rows(out, q, n_head, hd, hd_kv):
+    nt = out.numel() // (n_head * hd_kv)
+    _size("q", q, nt * n_head * hd)
+    _size("out", out, nt * n_head * hd_kv)
+    return nt
+
+
+def _gqa_attn_chunk_paged(end, out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                          n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream):
+    dt = _CHUNK_DTYPE[end]
+    nt = _attn_rows(out, q, n_head, hd, hd_kv)
+    _on_current_device(out, q, k_pool, v_pool, block_table, chunk_off, n_past, ws, err)
+    n_seq = _chunk_seqs(chunk_off, n_past, nt)
+    _chunk_pool(end, k_pool, v_pool, block_table, n_seq, n_kv_head * hd_kv)
+    name = "minf_gqa_attn_chunk_paged" + end
+    _check(getattr(lib(), name)(
+        _dev(out, name="out"), _dev(q, name="q"), _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"),
+        k_pool.shape[0], _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows,
+        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk, n_head,
+        n_kv_head, hd, hd_kv, scale, window, n_sink, _dev(ws, torch.uint8, "ws"), _nbytes(ws),
+        _dev(err, torch.int32, "err"), _stream(stream)), name)
+
+
+def minf_gqa_attn_chunk_paged(out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                              n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    _gqa_attn_chunk_paged("", out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                          n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def minf_gqa_attn_chunk_paged_f16(out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                                  n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    _gqa_attn_chunk_paged("_f16", out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                          n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def minf_gqa_attn_chunk_paged_q8(out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                                 n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    _gqa_attn_chunk_paged("_q8", out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
+                          n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def _gqa_attn_window(end, out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                     n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream):
+    dt = _CHUNK_DTYPE[end]
+    nt = _attn_rows(out, q, n_head, hd, hd_kv)
+    _on_current_device(out, q, k_reg, v_reg, seq_row_off, seq_cap, chunk_off, n_past, ws, err)
+    n_seq = _chunk_seqs(chunk_off, n_past, nt)
+    _chunk_pool(end, k_reg, v_reg, None, n_seq, n_kv_head * hd_kv)
+    for name, t in (("seq_row_off", seq_row_off), ("seq_cap", seq_cap)):
+        if t is not None:
+            _size(name, t, n_seq)
+    if seq_row_off is None and k_reg.shape[0] < max_cap:
+        raise ValueError(f"the regions have {k_reg.shape[0]} rows, max_cap is {max_cap}")
+    name = "minf_gqa_attn_window" + end
+    _check(getattr(lib(), name)(
+        _dev(out, name="out"), _dev(q, name="q"), _dev(k_reg, dt, "k_reg"), _dev(v_reg, dt, "v_reg"),
+        _dev(seq_row_off, torch.int64, "seq_row_off"), _dev(seq_cap, torch.int32, "seq_cap"), max_cap, k_reg.shape[0],
+        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk, n_head,
+        n_kv_head, hd, hd_kv, scale, window, n_sink, _dev(ws, torch.uint8, "ws"), _nbytes(ws),
+        _dev(err, torch.int32, "err"), _stream(stream)), name)
+
+
+def minf_gqa_attn_window(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                         n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    """k_reg/v_reg: the [rows, W] arena (or one sequence's [cap, W] regions, with seq_row_off None)."""
+    _gqa_attn_window("", out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                     n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def minf_gqa_attn_window_f16(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                             n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    _gqa_attn_window("_f16", out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                     n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def minf_gqa_attn_window_q8(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                            n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream=None):
+    _gqa_attn_window("_q8", out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
+                     n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream)
+
+
+def _layer_step_chunk_paged(end, xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk, k_pool,
+                            v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
+                            window, n_sink, out, ws, err, stream):
+    dt, w = _CHUNK_DTYPE[end], n_kv_head * hd_kv
+    nt, n_embd = h.shape
+    n_axis = 1 if rope_pos is None or rope_pos.dim() == 1 else rope_pos.shape[0]
+    _on_current_device(xn, h, gain, q, k, v, rope_pos, chunk_off, n_past, k_pool, v_pool, block_table, out, ws, err)
+    n_seq = _chunk_seqs(chunk_off, n_past, nt)
+    _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
+    for name, t, n in (("xn", xn, nt * n_embd), ("gain", gain, n_embd), ("q", q, nt * n_head * hd), ("k", k, nt * w),
+                       ("v", v, nt * w), ("rope_pos", rope_pos, nt * n_axis), ("out", out, nt * n_head * hd_kv)):
+        if t is not None:
+            _size(name, t, n)
+    axes = _axis_bytes(pair_axis, hd)
+    if rope_pos is None:
+        axes = None
+    name = "minf_layer_attn_step_chunk_paged" + end
+    _check(getattr(lib(), name)(
+        _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd, _dev(q, name="q"),
+        _dev(k, name="k"), _dev(v, name="v"), _dev(rope_pos, torch.int32, "rope_pos"), n_axis, axes,
+        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk,
+        _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"), k_pool.shape[0],
+        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows, n_head, n_kv_head, hd, hd_kv,
+        theta, freq_scale, style, window, n_sink, _dev(out, name="out"), _dev(ws, torch.uint8, "ws"), _nbytes(ws),
+        _dev(err, torch.int32, "err"), _stream(stream)), name)
+
+
+def minf_layer_attn_step_chunk_paged(xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,
+                                     k_pool, v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta,
+                                     freq_scale, style, window, n_sink, out, ws, err, stream=None):
+    _layer_step_chunk_paged("", xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk, k_pool,
+                            v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
+                            window, n_sink, out, ws, err, stream)
+
+
+def minf_layer_attn_step_chunk_paged_f16(xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,
+                                         k_pool, v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta,
+                                         freq_scale, style, window, n_sink, out, ws, err, stream=None):
+    _layer_step_chunk_paged("_f16", xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,
+                            k_pool, v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta, freq_scale,
+                            style, window, n_sink, out, ws, err, stream)
+
+
+def minf_layer_attn_step_chunk_paged_q8(xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,
+                                        k_pool, v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta,
+                                        freq_scale, style, window, n_sink, out, ws, err, stream=None):
+    _layer_step_chunk_paged("_q8", xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,
+                            k_pool, v_pool, block_table, block_rows, n_head, n_kv_head, hd, hd_kv, theta, freq_scale,
+                            style, window, n_sink, out, ws, err, stream)

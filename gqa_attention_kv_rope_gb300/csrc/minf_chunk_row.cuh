@@ -1,0 +1,98 @@
+// minf_chunk_row.cuh -- one output row (a token and a head) of the chunk attention by one warp.
+//
+// The definition, as directly as a warp can compute it: the visible keys in groups of 32, a key a
+// lane, with the running maximum and sum of an online softmax in fp32; then every lane adds the
+// group's weighted V rows for its own dimensions, leaving out the hidden ones, so that nothing a
+// hidden row holds (infinities, NaN, whatever an unwritten row has) reaches the result.
+#pragma once
+
+#include "minf_chunk.cuh"
+
+namespace minf {
+
+struct RowJob {
+    const float *q;  // hd_kv values
+    float *out;      // hd_kv values
+    SeqRows rows;
+    long long p;     // the query's position
+    int hk;          // kv head
+};
+
+// Returns (in every lane) whether a block the row sees is missing; its rows count as zeros.
+template <typename T, int HD>
+__device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float scale_log2, int window, int n_sink) {
+    constexpr int D4 = HD / 4, PER = HD / 32;  // values a lane owns
+    const int lane = threadIdx.x & 31;
+    const long long last = job.p < job.rows.cap - 1 ? job.p : job.rows.cap - 1;  // last visible key
+    float m = -INFINITY, l = 0.0f, acc[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+    bool missing = false;
+    // key groups: from 0 while sinks are left, then from the window's first key
+    const long long first = window == 0 ? 0 : (job.p - window + 1 > 0 ? job.p - window + 1 : 0);
+    for (long long j0 = n_sink > 0 ? 0 : (first & ~31LL); j0 <= last; j0 += 32) {
+        if (window && j0 >= n_sink && j0 + 31 < first) j0 = first & ~31LL;
+        if (j0 > last) break;
+        const int j = static_cast<int>(j0) + lane;
+        const bool see = j <= last && chunk_sees(job.p, j, window, n_sink);
+        long long row = -1;
+        if (see) {
+            row = seq_row(job.rows, j);
+            if (row < 0) missing = true;
+        }
+        float s = 0.0f;
+        if (row >= 0) {
+            const float4 *q4 = reinterpret_cast<const float4 *>(job.q);
+#pragma unroll 4
+            for (int d = 0; d < D4; ++d) {
+                const float4 k = row_ld4<T>(c.k, row, c.W, c.row_bytes, job.hk * D4 + d), q = __ldg(q4 + d);
+                s = fmaf(q.x, k.x, s);
+                s = fmaf(q.y, k.y, s);
+                s = fmaf(q.z, k.z, s);
+                s = fmaf(q.w, k.w, s);
+            }
+        }
+        s = see ? s * scale_log2 : -INFINITY;
+        float mx = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float t = __shfl_xor_sync(0xffffffffu, mx, o);
+            mx = mx > t || mx != mx ? mx : t;  // a NaN score stays
+        }
+        const float mn = m > mx || m != m ? m : mx;
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        const float corr = exp2f(m - base), pr = see ? exp2f(s - base) : 0.0f;
+        m = mn;
+        float sum = pr;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l = l * corr + sum;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] *= corr;
+        for (unsigned left = __ballot_sync(0xffffffffu, row >= 0); left; left &= left - 1) {
+            const int b = __ffs(left) - 1;
+            const float pb = __shfl_sync(0xffffffffu, pr, b);
+            const long long rb = __shfl_sync(0xffffffffu, row, b);
+            if (lane < D4) {
+                if constexpr (PER == 4) {
+                    const float4 v = row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + lane);
+                    acc[0] = fmaf(pb, v.x, acc[0]);
+                    acc[1] = fmaf(pb, v.y, acc[1]);
+                    acc[2] = fmaf(pb, v.z, acc[2]);
+                    acc[3] = fmaf(pb, v.w, acc[3]);
+                }
+            }
+            if constexpr (PER == 2) {
+                const float4 v = row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + (lane >> 1));
+                acc[0] = fmaf(pb, lane & 1 ? v.z : v.x, acc[0]);
+                acc[1] = fmaf(pb, lane & 1 ? v.w : v.y, acc[1]);
+            }
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing visible: zeros
+#pragma unroll
+    for (int i = 0; i < PER; ++i) job.out[lane * PER + i] = l == 0.0f ? 0.0f : acc[i] * inv;
+    return __any_sync(0xffffffffu, missing);
+}
+
+}  // namespace minf

@@ -155,4 +155,80 @@ bool fused_step_supported(int nh, int nk, int hd, int hd_kv, int n_embd);
 int launch_decode(const DecodeArgs &a, cudaStream_t s);
 int launch_decode_step(const DecodeArgs &a, const DecodeStepExtra &x, cudaStream_t s);
 
+// ----------------------------------------------------------------------------- chunks
+// Cached sequences as the chunk operators see them (minf_chunk.cuh): paged (table non-null) or
+// contiguous rows of W values held as `kv`.
+struct ChunkKv {
+    const void *k, *v;       // pools, regions or arenas
+    int kv, W;
+    long long row_bytes;     // bytes of a row
+    long long rows;          // rows of the pool or arena
+    const int32_t *table;    // [n_seq, max_blocks] block ids
+    int max_blocks, block_shift, pool_blocks;
+    const int64_t *row_off;  // contiguous: per sequence first row (nullable: 0)
+    const int32_t *caps;     // contiguous: per sequence rows (nullable: cap)
+    int cap;                 // rows of a sequence (paged: max_blocks << block_shift), or their bound
+};
+struct ChunkSeqs {
+    const int32_t *off;      // [n_seq + 1] packed rows of each sequence (null: one each)
+    const int32_t *n_past;   // [n_seq]
+    int nt, n_seq;
+};
+
+// Several-axis RoPE: pair i turns by pos[axis[i]][t] * f_i, with f_i / 2 pi held as a 64-bit
+// fraction of a turn, so that whole turns drop out of the product exactly.
+struct AxisTable {
+    unsigned long long turn[128];  // kMaxHalf
+    unsigned char axis[128];
+};
+void axis_table(AxisTable *t, int hd, float theta, float freq_scale, const unsigned char *pair_axis);
+
+struct RopeAxesArgs {
+    float *y;
+    const float *x;
+    const int32_t *pos;  // [n_axis, nt]
+    int32_t *err;
+    int nt, n_axis, nh, hd, style;
+};
+int launch_rope_axes(const RopeAxesArgs &a, float theta, float freq_scale, const unsigned char *pair_axis,
+                     cudaStream_t s);
+
+struct ChunkStoreArgs {
+    float *q_out, *k_out;        // rotated rows (may be q and k; k_out may be null)
+    const float *q, *k, *v;      // [nt, nh, hd], [nt, nk, hd_kv], [nt, W]
+    const int32_t *rope_pos;     // [n_axis, nt], or null: the cache position on every axis
+    int n_axis;
+    ChunkSeqs sq;
+    ChunkKv c;
+    int nh, nk, hd, hd_kv, style;
+    int32_t *err;
+};
+int launch_chunk_store(const ChunkStoreArgs &a, float theta, float freq_scale, const unsigned char *pair_axis,
+                       cudaStream_t s);
+
+struct ChunkReadArgs {
+    void *k_rows, *v_rows;       // [nt, W] fp32, or binary16 with f16 set
+    int f16;
+    ChunkSeqs sq;
+    ChunkKv c;
+    int32_t *err;
+};
+int launch_chunk_read(const ChunkReadArgs &a, cudaStream_t s);
+
+struct ChunkAttnArgs {
+    float *out;                  // [nt, nh*hd_kv]
+    const float *q;              // [nt, nh, hd]
+    ChunkSeqs sq;
+    ChunkKv c;
+    int max_chunk;               // host bound of the chunk lengths (which kernel runs)
+    int nh, nk, hd, hd_kv;
+    float scale;
+    int window, n_sink;
+    int32_t *err;
+    void *ws;
+    size_t ws_bytes;
+};
+size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk);
+int launch_chunk_attn(const ChunkAttnArgs &a, cudaStream_t s);
+
 }  // namespace minf

@@ -104,3 +104,11 @@ def prefill_workspace(nt: int, n_head: int, n_kv_head: int, hd_kv: int, cap: int
                       device="cuda") -> torch.Tensor:
     n = binding.minf_attn_prefill_workspace_bytes(nt, n_head, n_kv_head, hd_kv, cap)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def chunk_workspace(nt: int, n_seq: int, n_head: int, n_kv_head: int, hd_kv: int, max_chunk: int,
+                    device="cuda") -> torch.Tensor:
+    """Workspace of the chunk attention (its contents need no preparation); calls of any shape whose
+    minf_attn_chunk_workspace_bytes it covers may share it one after the other."""
+    n = binding.minf_attn_chunk_workspace_bytes(nt, n_seq, n_head, n_kv_head, hd_kv, max_chunk)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

@@ -79,6 +79,9 @@ enum {
                                       tag in the workspace's first 256 bytes (its control block:
                                       the counters every call leaves at zero, and the layout of
                                       the last call that used it). */
+#define MINF_ERRBIT_CHUNK 0x40 /* chunk operators: chunk_off is not nondecreasing within [0, nt].
+                                  The attention wrote nothing; the rows that the store and the
+                                  read back wrote are not to be used. */
 
 /* Human-readable name of a status code (static storage). */
 MINF_API const char *minf_status_string(int status);
@@ -511,6 +514,176 @@ MINF_API int minf_layer_attn_step_qkv(float *xn, const float *h, const float *ga
                                       float *k, float *v, float *k_reg, float *v_reg, int cap, int n_head,
                                       int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
                                       float *out, void *ws, size_t ws_bytes, int32_t *err, minf_stream_t stream);
+
+/*
+ * Rotary position embedding with a position per axis (time, height and width of image and
+ * video rows; one axis is plain text).  As minf_rope, but pair i of token t turns by
+ * pos[pair_axis[i] * nt + t] * freq_i, and y may differ from x (or equal it).
+ * pos: int32 [n_axis, nt] (device); pair_axis: HOST array of hd/2 axis numbers below n_axis
+ * (sections in a row, interleaved, any order), NULL for one axis.  freq_i is as in
+ * minf_rope_freqs but kept to 53 bits, and whole turns drop out of the angle exactly: far
+ * positions lose nothing (minf_rope's fp32 product is off by 2^-24 of the angle).
+ * Device errors: a negative position on an axis that a pair uses -> MINF_ERRBIT_ROPE_POS,
+ * that token copied unrotated.
+ * Errors: MINF_ERR_ARG for null pointers, nt < 0, n_head <= 0, odd hd, hd > 256, a style
+ * not in {0, 1}, n_axis outside [1, 255], pair_axis NULL with n_axis > 1 or naming an axis
+ * that is not there; MINF_ERR_UNSUPPORTED for n_head * hd above 2^20.
+ */
+MINF_API int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt, int n_axis, const uint8_t *pair_axis,
+                            int n_head, int hd, float theta, float freq_scale, int style, int32_t *err,
+                            minf_stream_t stream);
+
+/*
+ * Chunks of new tokens ([P1] §3.2.4 and [P3] §2.2, for several sequences and several tokens of
+ * each in one call: prompts, parts of prompts, drafted tokens and single decode tokens mixed).
+ * The nt rows of q, k, v and out are packed by sequence: rows chunk_off[s] .. chunk_off[s+1]-1
+ * belong to sequence s, and its i-th new token is at cache position p = n_past[s] + i.
+ * chunk_off: int32[n_seq + 1], nondecreasing within [0, nt]; n_past: int32[n_seq]; both on the
+ * device, so a captured call replays with other lengths.  chunk_off NULL: one token a sequence
+ * (nt == n_seq).  A sequence may have no token.  Rows outside every chunk (padding before the
+ * first or behind the last) are neither read into a result nor written.
+ * Pools, block_table, max_blocks, block_rows and pool_rows are as for the paged forms above;
+ * blocks that no token needs (behind the last token, or outside its window and sinks) may be
+ * missing from the table.
+ *
+ * minf_rope_kv_append_chunk_paged: rotates q [nt, n_head, hd] into q_out and k [nt, n_kv_head,
+ * hd_kv] into k_out (each may be its input; k_out may be NULL: only stored), as minf_rope_axes
+ * with rope_pos [n_axis, nt] (NULL: the cache position on every axis), and writes the rotated k
+ * rows and the v rows to the pool rows of their positions: a copy, rounded to binary16 (_f16) or
+ * quantized (_q8) exactly as minf_kv_append_f16 and minf_kv_append_q8 do.
+ * Two tokens at one position of one sequence cannot be: each row has one writer, as long as no
+ * block id is used twice.
+ * Device errors: MINF_ERRBIT_ROPE_POS (token left unrotated, still stored), _STORE_POS (position
+ * outside [0, max_blocks * block_rows): rotated, not stored), _BLOCK (not stored), _CHUNK.
+ * Errors: as minf_rope_axes and minf_gqa_attn_decode_paged; MINF_ERR_UNSUPPORTED also for
+ * hd not a multiple of 8.
+ *
+ * minf_kv_read_chunk_paged: the rows of the chunks back from the pools, as values: row t of
+ * k_rows and v_rows [nt, row_width] is the cached row of token t, in fp32 or (rows_f16) rounded
+ * to binary16.  Rows of missing blocks or past the capacity come back as zeros, with
+ * MINF_ERRBIT_BLOCK or MINF_ERRBIT_STORE_POS.
+ * Errors: as minf_kv_append_paged; MINF_ERR_ARG also for rows_f16 with row_width not a
+ * multiple of 8.
+ */
+MINF_API int minf_rope_kv_append_chunk_paged(float *q_out, float *k_out, const float *q, const float *k, const float *v,
+                                             const int32_t *rope_pos, int n_axis, const uint8_t *pair_axis,
+                                             const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq, int n_head,
+                                             int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                             float *k_pool, float *v_pool, int64_t pool_rows, const int32_t *block_table,
+                                             int max_blocks, int block_rows, int32_t *err, minf_stream_t stream);
+MINF_API int minf_rope_kv_append_chunk_paged_f16(float *q_out, float *k_out, const float *q, const float *k, const float *v,
+                                             const int32_t *rope_pos, int n_axis, const uint8_t *pair_axis,
+                                             const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq, int n_head,
+                                             int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                             uint16_t *k_pool, uint16_t *v_pool, int64_t pool_rows, const int32_t *block_table,
+                                             int max_blocks, int block_rows, int32_t *err, minf_stream_t stream);
+MINF_API int minf_rope_kv_append_chunk_paged_q8(float *q_out, float *k_out, const float *q, const float *k, const float *v,
+                                             const int32_t *rope_pos, int n_axis, const uint8_t *pair_axis,
+                                             const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq, int n_head,
+                                             int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                             uint8_t *k_pool, uint8_t *v_pool, int64_t pool_rows, const int32_t *block_table,
+                                             int max_blocks, int block_rows, int32_t *err, minf_stream_t stream);
+MINF_API int minf_kv_read_chunk_paged(void *k_rows, void *v_rows, int rows_f16, const float *k_pool, const float *v_pool,
+                                      int64_t pool_rows, int row_width, const int32_t *block_table, int max_blocks,
+                                      int block_rows, const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq,
+                                      int32_t *err, minf_stream_t stream);
+MINF_API int minf_kv_read_chunk_paged_f16(void *k_rows, void *v_rows, int rows_f16, const uint16_t *k_pool, const uint16_t *v_pool,
+                                      int64_t pool_rows, int row_width, const int32_t *block_table, int max_blocks,
+                                      int block_rows, const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq,
+                                      int32_t *err, minf_stream_t stream);
+MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f16, const uint8_t *k_pool, const uint8_t *v_pool,
+                                      int64_t pool_rows, int row_width, const int32_t *block_table, int max_blocks,
+                                      int block_rows, const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq,
+                                      int32_t *err, minf_stream_t stream);
+
+/*
+ * Attention of the chunks ([P1] §3.2.4): for token t of sequence s at position p and query head h,
+ *   out[t, h] = sum_{j visible} softmax_j(scale * q[t,h][0:hd_kv] . K[j, hk]) V[j, hk],
+ *   j visible: 0 <= j <= min(p, cap - 1), and window == 0 or j > p - window or j < n_sink.
+ * window: positions each token sees back, itself included (0: no limit); n_sink: first rows of
+ * the sequence that stay visible beside the window (n_sink 0: none; without a window it changes
+ * nothing).  A token that sees nothing (p < 0) gets zeros.  Values in rows that a token does not
+ * see, infinities and NaN among them, do not reach its result.  The new tokens' own rows must
+ * have been stored.  q [nt, n_head, hd] is rotated; out [nt, n_head*hd_kv].
+ * minf_gqa_attn_chunk_paged reads paged pools; minf_gqa_attn_window reads contiguous regions:
+ * sequence s has rows seq_row_off[s] .. + seq_cap[s] of the arena [arena_rows, W], as for
+ * minf_gqa_attn_decode (seq_row_off NULL: one sequence, the regions' max_cap rows; seq_cap NULL:
+ * max_cap each; a sequence's rows past the arena's end do not exist).
+ * max_chunk: host bound of the chunk lengths.  It only chooses the kernel (few rows a sequence:
+ * a split-KV stream; many: tensor-core tiles); longer chunks are computed correctly, only slower.
+ * ws: minf_attn_chunk_workspace_bytes(nt, n_seq, n_head, n_kv_head, hd_kv, max_chunk) bytes,
+ * 16-byte aligned.  Its contents need no preparation and no call leaves anything in it for the
+ * next, so calls of any shape may share it one after the other; two calls that run concurrently
+ * must not.
+ * Sums and softmax statistics are fp32; products run on the tensor cores with operands split
+ * into halves whose sum carries 22 bits or more.
+ * Device errors: MINF_ERRBIT_ATTN_POS (p < 0, or p >= cap: the window is clamped to cap), _BLOCK
+ * (a visible row's block is missing: read as zeros), _CHUNK (nothing written), _TIMEOUT.
+ * Errors: as minf_gqa_attn_decode; MINF_ERR_ARG for window < 0, n_sink < 0, max_chunk <= 0,
+ * chunk_off NULL with nt != n_seq, seq_row_off NULL with n_seq > 1; MINF_ERR_WORKSPACE.
+ */
+MINF_API size_t minf_attn_chunk_workspace_bytes(int nt, int n_seq, int n_head, int n_kv_head, int hd_kv, int max_chunk);
+MINF_API int minf_gqa_attn_chunk_paged(float *out, const float *q, const float *k_pool, const float *v_pool, int64_t pool_rows,
+                                       const int32_t *block_table, int max_blocks, int block_rows, const int32_t *chunk_off,
+                                       const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                       int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                       minf_stream_t stream);
+MINF_API int minf_gqa_attn_chunk_paged_f16(float *out, const float *q, const uint16_t *k_pool, const uint16_t *v_pool, int64_t pool_rows,
+                                       const int32_t *block_table, int max_blocks, int block_rows, const int32_t *chunk_off,
+                                       const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                       int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                       minf_stream_t stream);
+MINF_API int minf_gqa_attn_chunk_paged_q8(float *out, const float *q, const uint8_t *k_pool, const uint8_t *v_pool, int64_t pool_rows,
+                                       const int32_t *block_table, int max_blocks, int block_rows, const int32_t *chunk_off,
+                                       const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                       int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                       minf_stream_t stream);
+MINF_API int minf_gqa_attn_window(float *out, const float *q, const float *k_reg, const float *v_reg, const int64_t *seq_row_off,
+                                  const int32_t *seq_cap, int max_cap, int64_t arena_rows, const int32_t *chunk_off,
+                                  const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                  int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                  minf_stream_t stream);
+MINF_API int minf_gqa_attn_window_f16(float *out, const float *q, const uint16_t *k_reg, const uint16_t *v_reg, const int64_t *seq_row_off,
+                                  const int32_t *seq_cap, int max_cap, int64_t arena_rows, const int32_t *chunk_off,
+                                  const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                  int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                  minf_stream_t stream);
+MINF_API int minf_gqa_attn_window_q8(float *out, const float *q, const uint8_t *k_reg, const uint8_t *v_reg, const int64_t *seq_row_off,
+                                  const int32_t *seq_cap, int max_cap, int64_t arena_rows, const int32_t *chunk_off,
+                                  const int32_t *n_past, int nt, int n_seq, int max_chunk, int n_head, int n_kv_head, int hd,
+                                  int hd_kv, float scale, int window, int n_sink, void *ws, size_t ws_bytes, int32_t *err,
+                                  minf_stream_t stream);
+
+/*
+ * One layer's attention stage for chunks over paged regions: xn = RMSNorm(h) * gain over all nt
+ * rows ([P1] §3.2.1); minf_rope_kv_append_chunk_paged with q and k in place; then
+ * minf_gqa_attn_chunk_paged with scale 1/sqrt(hd) ([P1] §2.4).  Arguments, errors and device
+ * errors as those three.
+ */
+MINF_API int minf_layer_attn_step_chunk_paged(float *xn, const float *h, const float *gain, float eps, int n_embd, float *q,
+                                              float *k, const float *v, const int32_t *rope_pos, int n_axis,
+                                              const uint8_t *pair_axis, const int32_t *chunk_off, const int32_t *n_past, int nt,
+                                              int n_seq, int max_chunk, float *k_pool, float *v_pool, int64_t pool_rows,
+                                              const int32_t *block_table, int max_blocks, int block_rows, int n_head,
+                                              int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                              int window, int n_sink, float *out, void *ws, size_t ws_bytes, int32_t *err,
+                                              minf_stream_t stream);
+MINF_API int minf_layer_attn_step_chunk_paged_f16(float *xn, const float *h, const float *gain, float eps, int n_embd, float *q,
+                                              float *k, const float *v, const int32_t *rope_pos, int n_axis,
+                                              const uint8_t *pair_axis, const int32_t *chunk_off, const int32_t *n_past, int nt,
+                                              int n_seq, int max_chunk, uint16_t *k_pool, uint16_t *v_pool, int64_t pool_rows,
+                                              const int32_t *block_table, int max_blocks, int block_rows, int n_head,
+                                              int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                              int window, int n_sink, float *out, void *ws, size_t ws_bytes, int32_t *err,
+                                              minf_stream_t stream);
+MINF_API int minf_layer_attn_step_chunk_paged_q8(float *xn, const float *h, const float *gain, float eps, int n_embd, float *q,
+                                              float *k, const float *v, const int32_t *rope_pos, int n_axis,
+                                              const uint8_t *pair_axis, const int32_t *chunk_off, const int32_t *n_past, int nt,
+                                              int n_seq, int max_chunk, uint8_t *k_pool, uint8_t *v_pool, int64_t pool_rows,
+                                              const int32_t *block_table, int max_blocks, int block_rows, int n_head,
+                                              int n_kv_head, int hd, int hd_kv, float theta, float freq_scale, int style,
+                                              int window, int n_sink, float *out, void *ws, size_t ws_bytes, int32_t *err,
+                                              minf_stream_t stream);
 
 /*
  * SiLU times up ([P1] §3.2.5): y = gate / (1 + e^-gate) * up over n elements.

@@ -1,0 +1,122 @@
+"""The chunk operators' refusals, before anything is launched (no GPU needed)."""
+import ctypes
+
+import pytest
+
+P = ctypes.c_void_p
+FAKE = P(0x1000)  # never dereferenced: validation rejects before any launch
+ODD = P(0x1004)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gqa_attention_kv_rope_gb300 import binding, build
+
+    build.build()
+    return binding.lib()
+
+
+def attn_args(**kw):
+    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, pool_rows=256, table=FAKE, max_blocks=4, block_rows=16, off=FAKE,
+             past=FAKE, nt=8, n_seq=2, max_chunk=4, nh=14, nk=2, hd=64, hd_kv=64, scale=0.125, window=0, n_sink=0,
+             ws=FAKE, ws_bytes=1 << 40, err=FAKE, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+def window_args(**kw):
+    a = dict(out=FAKE, q=FAKE, k=FAKE, v=FAKE, row_off=FAKE, cap=None, max_cap=100, arena_rows=500, off=FAKE, past=FAKE,
+             nt=8, n_seq=2, max_chunk=4, nh=14, nk=2, hd=64, hd_kv=64, scale=0.125, window=0, n_sink=0, ws=FAKE,
+             ws_bytes=1 << 40, err=FAKE, stream=None)
+    a.update(kw)
+    return list(a.values())
+
+
+SHARED = [(dict(out=None), 1), (dict(q=None), 1), (dict(q=ODD), 1), (dict(k=ODD), 1), (dict(v=None), 1),
+          (dict(past=None), 1), (dict(err=None), 1), (dict(off=None), 1), (dict(nt=-1), 1), (dict(n_seq=-1), 1),
+          (dict(max_chunk=0), 1), (dict(window=-1), 1), (dict(n_sink=-1), 1), (dict(nh=15), 2), (dict(hd_kv=128), 2),
+          (dict(hd=96, hd_kv=96), 3), (dict(nh=18), 3), (dict(nh=0), 1), (dict(hd=260), 3), (dict(ws=None), 5),
+          (dict(ws=ODD), 5), (dict(ws_bytes=0), 5)]
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad,status", SHARED + [
+    (dict(table=None), 1), (dict(pool_rows=0), 1), (dict(max_blocks=0), 1), (dict(block_rows=8), 3),
+    (dict(block_rows=48), 3), (dict(block_rows=8192), 3), (dict(pool_rows=250), 3),
+    (dict(max_blocks=1 << 30), 3), (dict(pool_rows=1 << 32), 3)])
+def test_chunk_attention_refuses(lib, end, bad, status):
+    assert getattr(lib, "minf_gqa_attn_chunk_paged" + end)(*attn_args(**bad)) == status
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad,status", SHARED + [(dict(row_off=None), 1), (dict(max_cap=0), 1), (dict(arena_rows=0), 1),
+                                                 (dict(arena_rows=1 << 31), 3), (dict(max_cap=(1 << 31) - 1), 3)])
+def test_window_attention_refuses(lib, end, bad, status):
+    assert getattr(lib, "minf_gqa_attn_window" + end)(*window_args(**bad)) == status
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+def test_empty_calls_launch_nothing(lib, end):
+    assert getattr(lib, "minf_gqa_attn_chunk_paged" + end)(*attn_args(nt=0)) == 0
+    assert getattr(lib, "minf_gqa_attn_chunk_paged" + end)(*attn_args(n_seq=0)) == 0
+    assert getattr(lib, "minf_gqa_attn_window" + end)(*window_args(nt=0, ws=None, ws_bytes=0)) == 0
+
+
+def axes(*values):
+    return (ctypes.c_uint8 * len(values))(*values)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(y=None), 1), (dict(x=None), 1), (dict(pos=None), 1), (dict(err=None), 1), (dict(nt=-1), 1), (dict(n_axis=0), 1),
+    (dict(n_axis=256), 1), (dict(pair_axis=None), 1), (dict(pair_axis=axes(0, 1, 2, 0)), 1), (dict(nh=0), 1),
+    (dict(hd=7), 1), (dict(hd=258, pair_axis=axes(*[0] * 129)), 1), (dict(style=2), 1), (dict(nh=1 << 20), 3)])
+def test_rope_axes_refuses(lib, bad, status):
+    a = dict(y=FAKE, x=FAKE, pos=FAKE, nt=4, n_axis=2, pair_axis=axes(0, 1, 1, 0), nh=2, hd=8, theta=1e4, fs=1.0, style=0,
+             err=FAKE, stream=None)
+    a.update(bad)
+    assert lib.minf_rope_axes(*a.values()) == status
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad,status", [
+    (dict(q_out=None), 1), (dict(k_out=ODD), 1), (dict(q=ODD), 1), (dict(k=None), 1), (dict(v=None), 1),
+    (dict(off=None), 1), (dict(past=None), 1), (dict(n_axis=2), 1), (dict(style=3), 1), (dict(nh=15), 2),
+    (dict(hd=68), 3), (dict(hd_kv=32), 3), (dict(kp=ODD), 1), (dict(table=None), 1), (dict(block_rows=24), 3),
+    (dict(err=None), 1)])
+def test_store_refuses(lib, end, bad, status):
+    a = dict(q_out=FAKE, k_out=None, q=FAKE, k=FAKE, v=FAKE, pos=None, n_axis=1, pair_axis=None, off=FAKE, past=FAKE,
+             nt=4, n_seq=2, nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, kp=FAKE, vp=FAKE, rows=256,
+             table=FAKE, max_blocks=4, block_rows=16, err=FAKE, stream=None)
+    a.update(bad)
+    assert getattr(lib, "minf_rope_kv_append_chunk_paged" + end)(*a.values()) == status
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad,status", [
+    (dict(k_rows=None), 1), (dict(v_rows=ODD), 1), (dict(w=0), 1), (dict(w=2), 1), (dict(f16=1, w=36), 1),
+    (dict(table=None), 1), (dict(rows=100), 3), (dict(off=None), 1), (dict(err=None), 1)])
+def test_read_refuses(lib, end, bad, status):
+    a = dict(k_rows=FAKE, v_rows=FAKE, f16=0, kp=FAKE, vp=FAKE, rows=256, w=128, table=FAKE, max_blocks=4, block_rows=16,
+             off=FAKE, past=FAKE, nt=4, n_seq=2, err=FAKE, stream=None)
+    a.update(bad)
+    assert getattr(lib, "minf_kv_read_chunk_paged" + end)(*a.values()) == status
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad,status", [
+    (dict(xn=None), 1), (dict(h=None), 1), (dict(n_embd=0), 1), (dict(q=ODD), 1), (dict(n_axis=3), 1), (dict(off=None), 1),
+    (dict(max_chunk=0), 1), (dict(hd=68), 3), (dict(hd_kv=128), 2), (dict(window=-2), 1), (dict(out=None), 1),
+    (dict(ws=None), 5), (dict(ws_bytes=8), 5)])
+def test_layer_step_refuses_before_its_first_launch(lib, end, bad, status):
+    a = dict(xn=FAKE, h=FAKE, gain=None, eps=1e-6, n_embd=896, q=FAKE, k=FAKE, v=FAKE, pos=None, n_axis=1, pair_axis=None,
+             off=FAKE, past=FAKE, nt=4, n_seq=2, max_chunk=4, kp=FAKE, vp=FAKE, rows=256, table=FAKE, max_blocks=4,
+             block_rows=16, nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, window=0, n_sink=0, out=FAKE,
+             ws=FAKE, ws_bytes=1 << 40, err=FAKE, stream=None)
+    a.update(bad)
+    assert getattr(lib, "minf_layer_attn_step_chunk_paged" + end)(*a.values()) == status
+
+
+def test_workspace_sizes(lib):
+    f = lib.minf_attn_chunk_workspace_bytes
+    assert f(0, 1, 14, 2, 64, 1) == 0 and f(4, 1, 15, 2, 64, 1) == 0 and f(4, 1, 14, 2, 96, 1) == 0
+    assert f(1, 1, 14, 2, 64, 1) >= 256 and f(5000, 64, 16, 8, 128, 4096) >= 256
