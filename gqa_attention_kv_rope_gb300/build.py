@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libminf.so")
 SOURCES = ["minf_api.cu", "minf_elementwise.cu", "minf_decode.cu", "minf_decode_f16.cu", "minf_decode_q8.cu",
            "minf_prefill.cu", "minf_noalloc.cu", "minf_qkv.cu", "minf_chunk_api.cu", "minf_chunk_rows.cu",
-           "minf_chunk_attn.cu", "minf_chunk_plan.cu", "minf_chunk_tiles.cu"]
+           "minf_chunk_attn.cu", "minf_chunk_plan.cu", "minf_chunk_tiles.cu",
+           "minf_chunk_stream.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", f"-I{os.path.join(ROOT, 'include')}"]

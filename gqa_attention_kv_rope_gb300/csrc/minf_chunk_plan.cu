@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         int lo, hi;
         chunk_rows(a.sq.off, a.sq.nt, s, lo, hi);
         const long long past = __ldg(a.sq.n_past + s), base = tile_base(lo, s, a.tt);
-        const int cap = seq_rows(a.c, s).cap, n = hi - lo, tiles = (n + a.tt - 1) / a.tt;
+        const int cap = seq_rows(a.c, s).cap, n = hi - lo, tiles = n < a.least || n > a.most ? 0 : (n + a.tt - 1) / a.tt;
         long long run = 0;
         int reported = 0;
         for (int t0 = 0; t0 < tiles; t0 += 32) {

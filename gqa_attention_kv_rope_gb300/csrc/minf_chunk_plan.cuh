@@ -67,6 +67,7 @@ struct PlanArgs {
     ChunkSeqs sq;
     int nk, tt, kt, window, n_sink;
     int max_ctas, min_units;  // stretches at most; units a stretch should have at least
+    int least, most;          // chunk lengths that this plan takes (the others have no units)
     PlanHead *head;
     PlanStart *starts;        // [max_ctas]
     int *tickets;             // [max_ctas]

@@ -89,6 +89,7 @@ struct TileParams {
     float scale_log2;
     int tt;        // tokens of a tile
     int box_rows;  // rows of a TMA copy
+    int least;     // sequences with shorter chunks are not this kernel's (see launch_chunk_attn)
 };
 
 // ----------------------------------------------------------------------------- tensor-core wrappers
@@ -238,7 +239,7 @@ __device__ __forceinline__ bool walk_next(Walk &w, const TileParams &p) {
             do {
                 ++w.seq;
                 walk_seq(w, p);
-            } while (w.hi == w.lo);
+            } while (w.hi - w.lo < p.least);
         }
     }
     walk_item(w, p);
@@ -604,7 +605,6 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                 tm_wait_ld();
                 const bool mask = !(j0 >= all_lo && j0 + KT <= all_hi) && !(j0 + KT <= p.a.n_sink && j0 + KT <= all_hi);
                 const float2 cc = make_float2(c, c);
-                float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 64; e += 4) {
                     float2 a = mul2(bits2(x[e], x[e + 1]), cc), b = mul2(bits2(x[e + 2], x[e + 3]), cc);
@@ -614,15 +614,23 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                         a = fma2(a, lo2(kf), lo2(ve));
                         b = fma2(b, hi2(kf), hi2(ve));
                     }
-                    float y[4] = {a.x, a.y, b.x, b.y};
+                    x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
+                    x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
+                }
+                if (mask) {
+                    const int jb = j0 + half * 64, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const int j = j0 + half * 64 + e + f;
-                        if (mask && !(j < r_hi && (j >= r_lo || j < r_sink))) y[f] = -INFINITY;
-                        mt[f] = fmaxf(mt[f], y[f]);
-                        x[e + f] = __float_as_uint(y[f]);
+                    for (int e = 0; e < 64; ++e) {
+                        const bool see = (e < e_hi) & ((e >= e_lo) | (e < e_sink));
+                        x[e] = see ? x[e] : 0xff800000u;  // -infinity
                     }
                 }
+                float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        mt[f] = fmaxf(fmaxf(mt[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + 4 + f]));
                 sm.mx[q & 1][half][row] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 named_sync(1, kRowThreads);
                 const float mn = fmaxf(sm.mx[q & 1][0][row], sm.mx[q & 1][1][row]);
@@ -916,13 +924,14 @@ size_t chunk_tiles_workspace(int nt, int n_seq, int nh, int nk, int hd_kv) {
     return tiles_layout(nt, n_seq, nh, nk, hd_kv).total;
 }
 
-int launch_chunk_tiles(const ChunkAttnArgs &a, cudaStream_t s) {
+int launch_chunk_tiles(const ChunkAttnArgs &a, void *workspace, int least, cudaStream_t s) {
     const int sms = sm_count();
     const PlanLayout lay = tiles_layout(a.sq.nt, a.sq.n_seq, a.nh, a.nk, a.hd_kv);
-    char *ws = static_cast<char *>(a.ws);
+    char *ws = static_cast<char *>(workspace);
     TileParams p = {};
     p.a = a;
     p.tt = BM / (a.nh / a.nk);
+    p.least = least;
     p.head = reinterpret_cast<const PlanHead *>(ws + lay.head);
     p.starts = reinterpret_cast<const PlanStart *>(ws + lay.starts);
     p.tickets = reinterpret_cast<int *>(ws + lay.tickets);
@@ -939,6 +948,8 @@ int launch_chunk_tiles(const ChunkAttnArgs &a, cudaStream_t s) {
     pl.n_sink = a.n_sink;
     pl.max_ctas = sms;
     pl.min_units = 1;
+    pl.least = least;
+    pl.most = 0x7fffffff;
     pl.head = const_cast<PlanHead *>(p.head);
     pl.starts = const_cast<PlanStart *>(p.starts);
     pl.tickets = p.tickets;

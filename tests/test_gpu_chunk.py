@@ -219,6 +219,17 @@ def test_chunks(m, geom, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("geom", GEOMS, ids=str)
+def test_few_tokens(m, geom, kind):
+    # drafted tokens: up to 8, 16 and 32 query rows a kv head, with and without a window
+    g = geom[0] // geom[1]
+    for rows, past in ((8, [0, 63, 200]), (16, [130, 5, 64]), (32, [700, 0, 31])):
+        n = max(1, rows // g)
+        check(m, Batch(geom, kind, [n, max(1, n - 1), 1], past, paged=True, block=32, seed=28))
+        check(m, Batch(geom, kind, [1, n], past[:2], paged=False, seed=29, window=70, sinks=2))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (16, 0), (40, 4), (63, 70), (64, 1), (1000, 4)])
 def test_window_and_sinks(m, kind, window, sinks):
     check(m, Batch((14, 2, 64, 64), kind, [1, 150, 9], [333, 20, 0], paged=False, seed=5, window=window, sinks=sinks))
