@@ -4,14 +4,17 @@
 // An item is 128 query rows: up to 128 / g consecutive tokens of one sequence with the g query
 // heads of one kv head (row = token * g + head), so that a K/V tile is read once for the whole
 // group.  A CTA walks its stretch of units (minf_chunk_plan.cuh); per tile of 128 keys:
-//   S = Q K^T   tcgen05.mma kind::f16, M = N = 128, into one of two TMEM buffers
+//   S = Q K^T   tcgen05.mma kind::f16, M = N = 128, Q from TMEM, into one of two TMEM buffers
 //   P = 2^(s - m)   two threads a row (64 keys each): read S, mask, share the row's maximum,
-//                   and write P as binary16 halves hi + lo into TMEM
+//                   and write P as binary16 halves hi + lo over the S they came from
 //   O += P V    tcgen05.mma kind::f16 with P from TMEM, V as it lies in memory (keys x dims, the
 //               transposed operand), into TMEM
-// S of the next tile runs while the row threads work on this one.  O is rescaled only when a
-// row's maximum has grown by more than 2^8 since the last time (P is then at most 2^15, still a
-// binary16 value, and the rescale is a rare pass over O instead of one a tile).
+// Q and P come from TMEM because an operand pair from shared memory (8 KB a 128x128x16 step) takes
+// 97 clocks of its bandwidth, against 64 of tensor work with one of them in TMEM.
+// S of the next tile runs while the row threads work on this one; the tile after next goes into the
+// buffer that P V has just finished with.  O is rescaled only when a row's maximum has grown by
+// more than 2^8 since the last time (P is then at most 2^15, still a binary16 value, and the rescale
+// is a rare pass over O instead of one a tile).
 //
 // Precision: fp32 results from binary16 products.  Every operand that is not exactly binary16 is
 // split into hi + lo halves (22 bits), scaled by a power of two that keeps both normal; a product
@@ -22,10 +25,10 @@
 // P'_j 2^-e_j is the term of the sum: a large row cannot push the others out of binary16's range for
 // the rows that do not see it.  (Rows below 2^-46 keep the scale 2^60: what they lose is below 2^-70.)
 //
-// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues the MMAs, then the producers: for
-// binary16 two warps that issue TMA copies of K and V (straight into the swizzled layout the tensor
-// cores read; a block or a stretch of rows a copy); otherwise eight warps that load, split and
-// write K (four) and V (four).
+// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues the MMAs, warp 11 copies the next
+// item's Q rows in, then the producers: for binary16 warps 9 and 10 issue TMA copies of K and V
+// (straight into the swizzled layout the tensor cores read; a block or a stretch of rows a copy);
+// otherwise warps 12-15 load, split and write K, and warps 16-19 V.
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
 // not); rows that only some tokens see can still carry infinities or NaN into the sums of those that
@@ -46,8 +49,9 @@ constexpr int BM = 128, KT = 128;
 constexpr int kRowThreads = 256;  // warps 0-7: two threads a query row
 constexpr int kMmaWarp = 8;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^(shift + slack) = 2^15
-// TMEM columns: S buffers, P (hi then lo, two keys a column), O
-constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
+// TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
+// column)
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kTmemCols = 512;
 
 template <int HD, typename T>
 struct Cfg {
@@ -58,20 +62,20 @@ struct Cfg {
     // Warp groups: rows (0, 1), then MMA and TMA warps (2), then the splitting producers (3, 4).  The
     // rows' threads hold 64 scores and their halves, so registers move to them from the other groups;
     // the shares add up to no more than the launch's: 256 * 208 + 128 * 88 = 384 * 168, and
-    // 256 * 152 + 384 * 56 < 640 * 96.
+    // 256 * 144 + 384 * 64 = 640 * 96.
     static constexpr int kThreads = HL ? 640 : 384;
-    static constexpr int kRowRegs = HL ? 152 : 208, kOtherRegs = HL ? 56 : 88;
+    static constexpr int kRowRegs = HL ? 144 : 208, kOtherRegs = HL ? 64 : 88;
+    static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
 template <int HD, typename T>
 struct Smem {
     using C = Cfg<HD, T>;
-    unsigned char q[2][C::SLABS][BM * 128];            // hi, lo
     unsigned char k[C::NS][C::TERMS][C::SLABS][KT * 128];
     unsigned char v[C::NS][C::TERMS][C::SLABS][KT * 128];
-    unsigned long long q_full, p_ready, o_done, s_full[2], k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
+    unsigned char q[BM * C::kQRow];                    // the item's Q rows, fp32
+    unsigned long long q_in, q_free, q_full, p_ready[2], o_done[2], s_full[2], k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
     unsigned long long k_stat[4], v_stat[4];           // hi + lo kinds: factors of a tile written
-    float q_fac[BM];
     float mx[2][2][BM], sum[2][BM];
     int odd[BM];                                       // rows whose result is not finite
     alignas(16) float k_fac[C::HL ? 4 : 1][KT];        // K row factors, V row exponents and 2^-e
@@ -109,11 +113,6 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t leading_byt
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
-                 : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
@@ -177,7 +176,7 @@ __device__ __forceinline__ float2 bits2(uint32_t a, uint32_t b) { return make_fl
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     const __half2 h = __floats2half2_rn(x, y);
     const float2 f = __half22float2(h);
-    const float2 r = add2(make_float2(x, y), make_float2(-f.x, -f.y));
+    const float2 r = fma2(f, make_float2(-1.0f, -1.0f), make_float2(x, y));
     const __half2 l = __floats2half2_rn(r.x, r.y);
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
@@ -291,6 +290,27 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     }
 }
 
+// One warp: the next item's Q rows into the stage as soon as the row threads have taken the last ones.
+template <int HD, typename T>
+__device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const TileParams &p, long long total, int ctas) {
+    using C = Cfg<HD, T>;
+    const int lane = threadIdx.x & 31, g = p.a.nh / p.a.nk;
+    volatile int *abort_flag = &sm.abort_flag;
+    Walk w;
+    int seg = 0;
+    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
+        if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
+        const int rows = w.cnt * g;
+        if (lane == 0) mbar_expect_tx(&sm.q_in, static_cast<uint32_t>(rows) * HD * 4);
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32) {
+            const long long t = w.lo + w.t0 + r / g;
+            bulk_load(sm.q + r * C::kQRow, p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd, HD * 4, &sm.q_in);
+        }
+        __syncwarp();
+    }
+}
+
 // Eight values of a cached row (8 * i8 ..), for the splitting producers.
 template <typename T>
 __device__ __forceinline__ void ld8(const unsigned char *row, int W, int i8, float (&x)[8]) {
@@ -312,147 +332,180 @@ __device__ __forceinline__ float amax8(const float (&x)[8]) {
                  fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
 }
 
-// Four warps: the stretch's K (or V) tiles as scaled hi + lo halves.  Eight lanes a row, eight
-// values of each slab a lane; a warp takes 32 of a tile's rows, four at a time.
+// Four warps: the stretch's K (or V) tiles as scaled hi + lo halves; a warp takes 32 of a tile's rows.
+// Lane r resolves row r (its block, and an L2 prefetch) one tile ahead; the values are loaded by eight
+// lanes a row, eight values of each slab a lane, four rows at a time and several such steps in flight.
+// V's row exponents also go out one tile ahead of its values: the row threads need them with S, while
+// the V stage may still be in use.
 template <int HD, typename T, bool kV>
 __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const TileParams &p, int warp, long long total, int ctas) {
     using C = Cfg<HD, T>;
+    constexpr bool Q = std::is_same<T, Q8>::value;
+    constexpr int STEP = Q ? 4 : 2;  // four-row steps in flight
     const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
     volatile int *abort_flag = &sm.abort_flag;
     const unsigned char *base = static_cast<const unsigned char *>(kV ? p.a.c.v : p.a.c.k);
-    // V's row exponents go out one tile ahead of its values: the row threads need them with S, while
-    // the V stage may still be in use
-    Walk w, ws;
-    bool more_s = false;
-    int ns = 0, us = 0;
-    auto row_ptr = [&](const Walk &x, int j, bool &missing) -> const unsigned char * {
-        if (!item_sees(x.keys, j)) return nullptr;
-        const long long row = seq_row(x.rows, j);
-        if (row < 0) {
-            missing = true;
-            return nullptr;
-        }
-        return base + row * p.a.c.row_bytes;
-    };
-    auto stats = [&]() {  // of V tile ns
-        const int j0 = unit_tile(ws.keys, us) * KT + warp * 32;
-        bool missing = false;
-#pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += 8) {
-            const unsigned char *ptr[2];
-            float am[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) ptr[i] = row_ptr(ws, j0 + r0 + 4 * i + sub, missing);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!ptr[i]) continue;
-                if constexpr (std::is_same<T, Q8>::value) {  // no value is above 127 scales
-                    if (l8 < HD / 32)
-                        am[i] = 127.0f * fabsf(__half2float(reinterpret_cast<const __half *>(ptr[i] + p.a.c.W)[ws.head * (HD / 32) + l8]));
-                } else {
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s) {
-                        float x[8];
-                        ld8<T>(ptr[i], p.a.c.W, ws.head * (HD / 8) + s * 8 + l8, x);
-                        am[i] = fmaxf(am[i], amax8(x));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) am[i] = fmaxf(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
-                if (l8 == 0) {
-                    const int sh = row_shift(am[i], 60), r = warp * 32 + r0 + 4 * i + sub;
-                    sm.v_exp[ns & 3][r] = static_cast<float>(-sh);
-                    sm.v_inv[ns & 3][r] = pow2i(sh);
-                }
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_stat[ns & 3]);
-        ++ns;
-        if (++us == ws.u1) {
-            more_s = walk_next(ws, p);
-            us = ws.u0;
-        }
-    };
+    Walk w;  // of the tile ahead
+    int u = 0, ahead = 0;
     bool more = walk_begin(w, p, total, ctas);
-    if constexpr (kV) {
-        ws = w;
-        more_s = more;
-        if (more) {
-            us = ws.u0;
-            stats();
+    if (more) u = w.u0;
+    // the tile ahead: this lane's row (null: hidden or missing), its head, and V's row exponents
+    const unsigned char *nxt = nullptr;
+    int nxt_head = 0;
+    auto look_ahead = [&]() {
+        nxt = nullptr;
+        nxt_head = w.head;
+        const int j = unit_tile(w.keys, u) * KT + warp * 32 + lane;
+        if (item_sees(w.keys, j)) {
+            const long long row = seq_row(w.rows, j);
+            if (row >= 0)
+                nxt = base + row * p.a.c.row_bytes;
+            else if (!kV)
+                flag_error(p.a.err, MINF_ERRBIT_BLOCK);
         }
-    }
-    int n = 0;
-    for (; more; more = walk_next(w, p)) {
-        for (int u = w.u0; u < w.u1; ++u, ++n) {
-            const int st = n % C::NS, j0 = unit_tile(w.keys, u) * KT + warp * 32;
-            if constexpr (kV) {
-                if (more_s) stats();
-            }
-            bool missing = false, ready = n < C::NS;
+        if (nxt) {
+            const unsigned char *v = nxt + w.head * (HD * (Q ? 1 : 4));
+#pragma unroll
+            for (int b = 0; b < HD * (Q ? 1 : 4); b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(v + b));
+        }
+        if constexpr (kV) {
+            const int r = warp * 32 + lane;
+            if constexpr (Q) {  // no value is above 127 scales
+                float am = 0.0f;
+                if (nxt) {
+                    const __half *sc = reinterpret_cast<const __half *>(nxt + p.a.c.W) + w.head * (HD / 32);
+#pragma unroll
+                    for (int b = 0; b < HD / 32; ++b) am = fmaxf(am, 127.0f * fabsf(__half2float(sc[b])));
+                }
+                const int sh = row_shift(am, 60);
+                sm.v_exp[ahead & 3][r] = static_cast<float>(-sh);
+                sm.v_inv[ahead & 3][r] = pow2i(sh);
+            } else {
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 8) {  // two rows of each lane group at a time
-                const unsigned char *ptr[2];
-                float x[2][C::SLABS][8];
+                for (int r0 = 0; r0 < 32; r0 += 8) {
+                    float am[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) ptr[i] = row_ptr(w, j0 + r0 + 4 * i + sub, missing);
+                    for (int i = 0; i < 2; ++i) {
+                        const unsigned char *ptr = reinterpret_cast<const unsigned char *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(nxt), r0 + 4 * i + sub));
+                        if (!ptr) continue;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s) {
-                        if (ptr[i]) {
-                            ld8<T>(ptr[i], p.a.c.W, w.head * (HD / 8) + s * 8 + l8, x[i][s]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[i][s][e] = 0.0f;
+                        for (int s = 0; s < C::SLABS; ++s) {
+                            float x[8];
+                            ld8<T>(ptr, p.a.c.W, w.head * (HD / 8) + s * 8 + l8, x);
+                            am[i] = fmaxf(am[i], amax8(x));
                         }
                     }
-                if (!ready) {  // (the first rows' loads are in flight)
-                    if (!__all_sync(0xffffffffu, mbar_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], ((n / C::NS) - 1) & 1,
-                                                           abort_flag, p.a.err)))
-                        return;
-                    ready = true;
-                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = warp * 32 + r0 + 4 * i + sub;
-                    float f;
-                    if constexpr (kV) {
-                        f = sm.v_inv[n & 3][r];
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1) am[i] = fmaxf(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
+                        if (l8 == 0) {
+                            const int sh = row_shift(am[i], 60), rr = warp * 32 + r0 + 4 * i + sub;
+                            sm.v_exp[ahead & 3][rr] = static_cast<float>(-sh);
+                            sm.v_inv[ahead & 3][rr] = pow2i(sh);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_stat[ahead & 3]);
+        }
+        ++ahead;
+        if (++u == w.u1) {
+            more = walk_next(w, p);
+            u = w.u0;
+        }
+    };
+    if (!more) return;
+    look_ahead();
+    for (int n = 0; n < ahead; ++n) {
+        const int st = n % C::NS, head = nxt_head;
+        const unsigned char *cur = nxt;
+        if (more) look_ahead();
+        bool ready = n < C::NS;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 4 * STEP) {
+            uint2 raw[Q ? STEP : 1][C::SLABS];  // quants, and their blocks' scales
+            float sc[Q ? STEP : 1][C::SLABS];
+            float x[Q ? 1 : STEP][C::SLABS][8];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                const unsigned char *ptr = reinterpret_cast<const unsigned char *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cur), r0 + 4 * i + sub));
+#pragma unroll
+                for (int s = 0; s < C::SLABS; ++s) {
+                    const int i8 = head * (HD / 8) + s * 8 + l8;
+                    if constexpr (Q) {
+                        raw[i][s] = make_uint2(0, 0);
+                        sc[i][s] = 0.0f;
+                        if (ptr) {
+                            raw[i][s] = __ldg(reinterpret_cast<const uint2 *>(ptr) + i8);
+                            sc[i][s] = __half2float(reinterpret_cast<const __half *>(ptr + p.a.c.W)[i8 >> 2]);
+                        }
+                    } else if (ptr) {
+                        ld8<T>(ptr, p.a.c.W, i8, x[i][s]);
                     } else {
-                        float am = amax8(x[i][0]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[i][s][e] = 0.0f;
+                    }
+                }
+            }
+            if (!ready) {  // (the first rows' loads are in flight)
+                if (!__all_sync(0xffffffffu, mbar_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], ((n / C::NS) - 1) & 1,
+                                                       abort_flag, p.a.err)))
+                    return;
+                ready = true;
+            }
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) {
+                const int r = warp * 32 + r0 + 4 * i + sub;
+                float f;
+                if constexpr (kV) {
+                    f = sm.v_inv[n & 3][r];
+                } else {
+                    float am;
+                    if constexpr (Q) {
+                        am = fabsf(sc[i][0]);
+                        if constexpr (C::SLABS == 2) am = fmaxf(am, fabsf(sc[i][1]));
+                        am *= 127.0f;  // no value is above 127 scales
+                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 4));  // (four lanes share a block)
+                    } else {
+                        am = amax8(x[i][0]);
                         if constexpr (C::SLABS == 2) am = fmaxf(am, amax8(x[i][1]));
 #pragma unroll
                         for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                        const int sh = row_shift(am, 126);
-                        f = pow2i(sh);
-                        if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-sh);
                     }
+                    const int sh = row_shift(am, 126);
+                    f = pow2i(sh);
+                    if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-sh);
+                }
 #pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s) {
-                        uint4 hi, lo;
-                        float(&y)[8] = x[i][s];
-                        split2(y[0] * f, y[1] * f, hi.x, lo.x);
-                        split2(y[2] * f, y[3] * f, hi.y, lo.y);
-                        split2(y[4] * f, y[5] * f, hi.z, lo.z);
-                        split2(y[6] * f, y[7] * f, hi.w, lo.w);
-                        unsigned char *h = kV ? sm.v[st][0][s] : sm.k[st][0][s], *l = kV ? sm.v[st][C::TERMS - 1][s] : sm.k[st][C::TERMS - 1][s];
-                        *reinterpret_cast<uint4 *>(h + sw16(r, l8)) = hi;
-                        *reinterpret_cast<uint4 *>(l + sw16(r, l8)) = lo;
+                for (int s = 0; s < C::SLABS; ++s) {
+                    float y[8];
+                    if constexpr (Q) {
+                        const float4 a = deq4(raw[i][s].x, sc[i][s] * f), b = deq4(raw[i][s].y, sc[i][s] * f);
+                        y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = x[i][s][e] * f;
                     }
+                    uint4 hi, lo;
+                    split2(y[0], y[1], hi.x, lo.x);
+                    split2(y[2], y[3], hi.y, lo.y);
+                    split2(y[4], y[5], hi.z, lo.z);
+                    split2(y[6], y[7], hi.w, lo.w);
+                    unsigned char *h = kV ? sm.v[st][0][s] : sm.k[st][0][s], *l = kV ? sm.v[st][C::TERMS - 1][s] : sm.k[st][C::TERMS - 1][s];
+                    *reinterpret_cast<uint4 *>(h + sw16(r, l8)) = hi;
+                    *reinterpret_cast<uint4 *>(l + sw16(r, l8)) = lo;
                 }
             }
-            if (!kV && missing) flag_error(p.a.err, MINF_ERRBIT_BLOCK);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (!kV) mbar_arrive(&sm.k_stat[n & 3]);
-                mbar_arrive(kV ? &sm.v_full[st] : &sm.k_full[st]);
-            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (!kV) mbar_arrive(&sm.k_stat[n & 3]);
+            mbar_arrive(kV ? &sm.v_full[st] : &sm.k_full[st]);
         }
     }
 }
@@ -464,9 +517,10 @@ __device__ __forceinline__ void issue_mmas(Smem<HD, T> &sm, const TileParams &p,
     volatile int *abort_flag = &sm.abort_flag;
     constexpr uint32_t kIdS = idesc_f16(BM, KT, false), kIdO = idesc_f16(BM, HD, true);
     constexpr uint32_t kSlab = KT * 128;
-    const uint64_t dq = desc128(su32(sm.q), 16), dk = desc128(su32(sm.k), 16), dv = desc128(su32(sm.v), kSlab);
+    const uint64_t dk = desc128(su32(sm.k), 16), dv = desc128(su32(sm.v), kSlab);
     constexpr uint64_t kStage = static_cast<uint64_t>(C::TERMS) * C::SLABS * kSlab >> 4;  // in descriptor units
     constexpr uint64_t kTerm = static_cast<uint64_t>(C::SLABS) * kSlab >> 4;
+    const uint32_t qh = tmem + kColQ, ql = qh + HD / 2;
     int n = 0, seg = 0;
     Walk w;
     for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
@@ -481,9 +535,9 @@ __device__ __forceinline__ void issue_mmas(Smem<HD, T> &sm, const TileParams &p,
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
                 const uint64_t o = static_cast<uint64_t>(kk >> 2) * (kSlab >> 4) + 2 * (kk & 3);
-                mma_ss(d, dq + o, k0 + o, kIdS, kk > 0);
-                mma_ss(d, dq + kTerm + o, k0 + o, kIdS, true);
-                if constexpr (C::HL) mma_ss(d, dq + o, k0 + kTerm + o, kIdS, true);
+                mma_ts(d, qh + kk * 8, k0 + o, kIdS, kk > 0);
+                mma_ts(d, ql + kk * 8, k0 + o, kIdS, true);
+                if constexpr (C::HL) mma_ts(d, qh + kk * 8, k0 + kTerm + o, kIdS, true);
             }
             commit(&sm.s_full[(n + i) & 1]);
             commit(&sm.k_empty[st]);
@@ -494,20 +548,24 @@ __device__ __forceinline__ void issue_mmas(Smem<HD, T> &sm, const TileParams &p,
         for (int i = 0; i < tiles; ++i) {
             const int st = (n + i) % C::NS;
             if (!mbar_wait(&sm.v_full[st], ((n + i) / C::NS) & 1, abort_flag, p.a.err)) return;
-            if (!mbar_wait(&sm.p_ready, (n + i) & 1, abort_flag, p.a.err)) return;
+            if (!mbar_wait(&sm.p_ready[(n + i) & 1], ((n + i) >> 1) & 1, abort_flag, p.a.err)) return;
             tc_after();
+            const uint32_t p0 = tmem + kColS + static_cast<uint32_t>((n + i) & 1) * KT;
             const uint64_t v0 = dv + st * kStage;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {
                 const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
-                const uint32_t ph = tmem + kColP + kk * 8, pl = ph + 64;
+                const uint32_t ph = p0 + kk * 8, pl = ph + 64;
                 mma_ts(tmem + kColO, ph, v0 + o, kIdO, i > 0 || kk > 0);
                 mma_ts(tmem + kColO, pl, v0 + o, kIdO, true);
                 if constexpr (C::HL) mma_ts(tmem + kColO, ph, v0 + kTerm + o, kIdO, true);
             }
-            commit(&sm.o_done);
+            commit(&sm.o_done[(n + i) & 1]);
             commit(&sm.v_empty[st]);
-            if (i + 2 < tiles && !scores(i + 2)) return;
+            if (i + 2 < tiles) {  // over P of this tile: once its product is done
+                if (!mbar_wait(&sm.o_done[(n + i) & 1], ((n + i) >> 1) & 1, abort_flag, p.a.err)) return;
+                if (!scores(i + 2)) return;
+            }
         }
         n += tiles;
     }
@@ -524,39 +582,46 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
     const int g = p.a.nh / p.a.nk;
     volatile int *abort_flag = &sm.abort_flag;
     int32_t *err = p.a.err;
-    int n = 0;
+    int n = 0, seg = 0;
     Walk w;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p)) {
+    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
-        // Q rows, scaled, as hi + lo halves: a warp takes 16 rows (all MMAs that read the last ones are done)
-        for (int i = 0; i < 16; i += 128 / HD) {
-            constexpr int LPR = HD / 4;  // lanes a row
-            const int r = warp * 16 + i + lane / LPR, d4 = lane % LPR;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows) {
-                const long long t = w.lo + w.t0 + r / g;
-                x = __ldg(reinterpret_cast<const float4 *>(p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd) + d4);
-            }
-            float am = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+        // this half row of Q, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
+        float c;
+        {
+            mbar_wait(&sm.q_in, seg & 1, abort_flag, err);
+            float4 x[HALF / 4];
+            float am = 0.0f;
 #pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-            const int sh = row_shift(am, 126);
+            for (int d = 0; d < HALF / 4; ++d) {
+                x[d] = row < rows ? *reinterpret_cast<const float4 *>(sm.q + row * C::kQRow + (half * (HALF / 4) + d) * 16)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                am = fmaxf(am, fmaxf(fmaxf(fabsf(x[d].x), fabsf(x[d].y)), fmaxf(fabsf(x[d].z), fabsf(x[d].w))));
+            }
+            sm.sum[half][row] = am;
+            if (half == 0) sm.odd[row] = 0;
+            named_sync(1, kRowThreads);
+            if (tid == 0) mbar_arrive(&sm.q_free);  // (every thread has read its part)
+            const int sh = row_shift(fmaxf(sm.sum[0][row], sm.sum[1][row]), 126);
             const float f = pow2i(sh);
-            uint2 hi, lo;
-            split2(x.x * f, x.y * f, hi.x, lo.x);
-            split2(x.z * f, x.w * f, hi.y, lo.y);
-            const uint32_t at = sw16(r, (d4 & 15) >> 1) + (d4 & 1) * 8;
-            *reinterpret_cast<uint2 *>(sm.q[0][d4 >> 4] + at) = hi;
-            *reinterpret_cast<uint2 *>(sm.q[1][d4 >> 4] + at) = lo;
-            if (d4 == 0) sm.q_fac[r] = pow2i(-sh);
+            c = p.scale_log2 * pow2i(-sh);
+#pragma unroll
+            for (int d0 = 0; d0 < HALF / 4; d0 += 8) {  // 32 dims: 16 columns
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                    split2(x[d0 + d].x * f, x[d0 + d].y * f, hi[2 * d], lo[2 * d]);
+                    split2(x[d0 + d].z * f, x[d0 + d].w * f, hi[2 * d + 1], lo[2 * d + 1]);
+                }
+                tm_st16(lanes + kColQ + half * (HALF / 2) + d0 * 2, hi);
+                tm_st16(lanes + kColQ + HD / 2 + half * (HALF / 2) + d0 * 2, lo);
+            }
+            tm_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full);
         }
-        if (half == 0) sm.odd[row] = 0;
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
-        named_sync(1, kRowThreads);
         const bool warp_live = (row & ~31) < rows, live = row < rows;
-        const float c = p.scale_log2 * sm.q_fac[row];
         // this row's window: keys [r_lo, r_hi) and [0, r_sink)
         const long long pos = w.past + w.t0 + row / g;
         int r_hi = 0, r_lo = 0, r_sink = 0;
@@ -575,26 +640,23 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
         float m = -INFINITY, l = 0.0f;
         for (int i = 0; i < tiles; ++i) {
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
-            if (!C::HL) {
+            mbar_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
+            tc_after();
+            if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
                 // rows of this tile that no token sees: V must hold zeros there
-                if (j0 < w.keys.lo || j0 + KT > w.keys.hi) {
-                    mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
-                    if (half == 0 && !item_sees(w.keys, j0 + row)) {
+                mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
+                if (half == 0 && !item_sees(w.keys, j0 + row)) {
 #pragma unroll
-                        for (int s = 0; s < C::SLABS; ++s)
+                    for (int s = 0; s < C::SLABS; ++s)
 #pragma unroll
-                            for (int ch = 0; ch < 8; ++ch)
-                                *reinterpret_cast<uint4 *>(sm.v[q % C::NS][0][s] + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
+                        for (int ch = 0; ch < 8; ++ch)
+                            *reinterpret_cast<uint4 *>(sm.v[q % C::NS][0][s] + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
                 }
+                fence_async_smem();
             }
             if (!warp_live) {
                 named_sync(1, kRowThreads);
-                if (i > 0) mbar_wait(&sm.o_done, (q - 1) & 1, abort_flag, err);
             } else {
-                mbar_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
-                tc_after();
                 uint32_t x[64];  // scores, as bits
                 tm_ld32(lanes + kColS + (q & 1) * KT + half * 64, x);
                 tm_ld32(lanes + kColS + (q & 1) * KT + half * 64 + 32, x + 32);
@@ -632,7 +694,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                     for (int f = 0; f < 4; ++f)
                         mt[f] = fmaxf(fmaxf(mt[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + 4 + f]));
                 sm.mx[q & 1][half][row] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
-                named_sync(1, kRowThreads);
+                tc_before();
+                named_sync(1, kRowThreads);  // both threads of a row have read S: P may go over it
+                tc_after();
                 const float mn = fmaxf(sm.mx[q & 1][0][row], sm.mx[q & 1][1][row]);
                 const bool grow = mn > m + kSlack || (m == -INFINITY && mn > m);
                 float corr = 1.0f;
@@ -640,9 +704,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                     corr = ex2_approx(m - mn);
                     m = mn;
                 }
-                if (i > 0) mbar_wait(&sm.o_done, (q - 1) & 1, abort_flag, err);  // P and O are free
-                tc_after();
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
+                    mbar_wait(&sm.o_done[(q - 1) & 1], ((q - 1) >> 1) & 1, abort_flag, err);
+                    tc_after();
 #pragma unroll 1
                     for (int d = 0; d < HALF; d += 16) {
                         uint32_t o[16];
@@ -675,18 +739,18 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                         split2(a.x, a.y, ph[e >> 1], pl[e >> 1]);
                         split2(b.x, b.y, ph[(e >> 1) + 1], pl[(e >> 1) + 1]);
                     }
-                    tm_st16(lanes + kColP + half * 32 + (e0 >> 1), ph);
-                    tm_st16(lanes + kColP + 64 + half * 32 + (e0 >> 1), pl);
+                    tm_st16(lanes + kColS + (q & 1) * KT + half * 32 + (e0 >> 1), ph);
+                    tm_st16(lanes + kColS + (q & 1) * KT + 64 + half * 32 + (e0 >> 1), pl);
                 }
                 l = l * corr + ((s2.x + s2.y) + (s3.x + s3.y));
                 tm_wait_st();
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_ready);
+            if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
         }
         n += tiles;
-        mbar_wait(&sm.o_done, (n - 1) & 1, abort_flag, err);
+        mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, err);
         tc_after();
         sm.sum[half][row] = l;
         named_sync(1, kRowThreads);
@@ -749,6 +813,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                 __threadfence();
                 // join the parts in the order of their keys
                 float M = -INFINITY;
+#pragma unroll 4
                 for (int b = b0; b <= b1; ++b) {
                     const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                     M = fmaxf(M, __ldcg(q + BM * HD + row));
@@ -759,20 +824,22 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                     float4 acc[8];
 #pragma unroll
                     for (int d = 0; d < 8; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
                     for (int b = b0; b <= b1; ++b) {
                         const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                         const float mb = __ldcg(q + BM * HD + row), lb = __ldcg(q + BM * (HD + 1) + row);
+                        float4 y[8];
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) y[d] = __ldcg(reinterpret_cast<const float4 *>(q) + (half * (HALF / 4) + d0 + d) * BM + row);
                         if (mb == -INFINITY && lb == 0.0f) continue;  // saw nothing
                         const float f = ex2_approx(mb - M);
                         L = fmaf(lb, f, L);
 #pragma unroll
                         for (int d = 0; d < 8; ++d) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(q) + (half * (HALF / 4) + d0 + d) * BM + row);
-                            acc[d].x = fmaf(y.x, f, acc[d].x);
-                            acc[d].y = fmaf(y.y, f, acc[d].y);
-                            acc[d].z = fmaf(y.z, f, acc[d].z);
-                            acc[d].w = fmaf(y.w, f, acc[d].w);
+                            acc[d].x = fmaf(y[d].x, f, acc[d].x);
+                            acc[d].y = fmaf(y[d].y, f, acc[d].y);
+                            acc[d].z = fmaf(y[d].z, f, acc[d].z);
+                            acc[d].w = fmaf(y[d].w, f, acc[d].w);
                         }
                     }
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -803,7 +870,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
             }
         }
         tc_before();
-        named_sync(1, kRowThreads);  // sm.odd, sm.sum and Q are free for the next segment
+        named_sync(1, kRowThreads);  // sm.odd and sm.sum are free for the next segment
     }
 }
 
@@ -816,10 +883,14 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     Smem<HD, T> &sm = *reinterpret_cast<Smem<HD, T> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        mbar_init(&sm.q_in, 1);
+        mbar_init(&sm.q_free, 1);
         mbar_init(&sm.q_full, kRowThreads / 32);
-        mbar_init(&sm.p_ready, kRowThreads / 32);
-        mbar_init(&sm.o_done, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.p_ready[i], kRowThreads / 32);
+            mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+        }
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&sm.k_full[i], C::HL ? 4 : 1);
             mbar_init(&sm.v_full[i], C::HL ? 4 : 1);
@@ -858,6 +929,8 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
         if (warp == kMmaWarp) {
             if (lane == 0) issue_mmas<HD, T>(sm, p, tmem, total, ctas);
             __syncwarp();
+        } else if (warp == kMmaWarp + 3) {
+            copy_q<HD, T>(sm, p, total, ctas);
         } else if constexpr (C::HL) {
             if (warp >= 16)
                 split_tiles<HD, T, true>(sm, p, warp - 16, total, ctas);
