@@ -46,47 +46,41 @@ __device__ __forceinline__ int chunk_seq_of(const int32_t *chunk_off, int n_seq,
     return t < __ldg(chunk_off + lo + 1) ? lo : -1;
 }
 
-// One sequence's cached rows.
+// One sequence's cached rows: rows 0 .. cap-1 exist.  (Two registers' worth: the kernels' roles keep
+// it across a whole walk.)
 struct SeqRows {
-    const int32_t *table;  // paged: this sequence's block ids (null: contiguous)
-    long long row0;        // contiguous: the sequence's first row
-    int cap;               // rows 0 .. cap-1 exist
-    int shift, mask;       // paged: j >> shift is the block, j & mask the row in it
-    int pool_blocks;
+    unsigned long long at;  // paged: the address of this sequence's block ids; contiguous: its first row
+    int cap;
 };
 
 __device__ __forceinline__ SeqRows seq_rows(const ChunkKv &c, int s) {
     SeqRows r;
-    r.shift = c.block_shift;
-    r.mask = (1 << c.block_shift) - 1;
-    r.pool_blocks = c.pool_blocks;
     if (c.table) {
-        r.table = c.table + static_cast<size_t>(s) * c.max_blocks;
-        r.row0 = 0;
+        r.at = reinterpret_cast<unsigned long long>(c.table + static_cast<size_t>(s) * c.max_blocks);
         r.cap = c.cap;
     } else {
-        r.table = nullptr;
-        r.row0 = c.row_off ? __ldg(reinterpret_cast<const long long *>(c.row_off) + s) : 0;
+        long long row0 = c.row_off ? __ldg(reinterpret_cast<const long long *>(c.row_off) + s) : 0;
         long long cap = c.caps ? __ldg(c.caps + s) : c.cap;
         // rows exist only inside the arena
-        if (r.row0 < 0 || r.row0 >= c.rows) {
-            r.row0 = 0;
+        if (row0 < 0 || row0 >= c.rows) {
+            row0 = 0;
             cap = 0;
-        } else if (cap > c.rows - r.row0) {
-            cap = c.rows - r.row0;
+        } else if (cap > c.rows - row0) {
+            cap = c.rows - row0;
         }
         if (cap > c.cap) cap = c.cap;  // max_cap bounds every cap_s
+        r.at = static_cast<unsigned long long>(row0);
         r.cap = cap < 0 ? 0 : static_cast<int>(cap);
     }
     return r;
 }
 
 // The pool (or arena) row of logical row j in [0, cap), or -1 where the block is missing.
-__device__ __forceinline__ long long seq_row(const SeqRows &r, int j) {
-    if (!r.table) return r.row0 + j;
-    const int b = __ldg(r.table + (j >> r.shift));
-    if (b < 0 || b >= r.pool_blocks) return -1;
-    return (static_cast<long long>(b) << r.shift) + (j & r.mask);
+__device__ __forceinline__ long long seq_row(const ChunkKv &c, const SeqRows &r, int j) {
+    if (!c.table) return static_cast<long long>(r.at) + j;
+    const int b = __ldg(reinterpret_cast<const int32_t *>(r.at) + (j >> c.block_shift));
+    if (b < 0 || b >= c.pool_blocks) return -1;
+    return (static_cast<long long>(b) << c.block_shift) + (j & ((1 << c.block_shift) - 1));
 }
 
 // Four consecutive values of a cached row (element 4*i4 of the row), in fp32.

@@ -110,4 +110,122 @@ __host__ __device__ __forceinline__ int stretch_of(long long total, int ctas, lo
 
 int launch_chunk_plan(const PlanArgs &a, cudaStream_t s);
 
+// What both attention kernels are launched with.
+struct AttnParams {
+    ChunkAttnArgs a;
+    const PlanHead *head;
+    const PlanStart *starts;
+    int *tickets;
+    float *parts;
+    float scale_log2;
+    int tt, kt;       // tokens of an item, keys of a tile
+    int box_rows;     // rows of a TMA copy
+    int least, most;  // chunk lengths this launch takes
+};
+
+// Fills the plan's arguments and the kernel's pointers for a workspace laid out as `lay`.
+inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int max_ctas, int min_units) {
+    PlanArgs pl = {};
+    pl.c = p.a.c;
+    pl.sq = p.a.sq;
+    pl.nk = p.a.nk;
+    pl.tt = p.tt;
+    pl.kt = p.kt;
+    pl.window = p.a.window;
+    pl.n_sink = p.a.n_sink;
+    pl.max_ctas = max_ctas;
+    pl.min_units = min_units;
+    pl.least = p.least;
+    pl.most = p.most;
+    pl.head = reinterpret_cast<PlanHead *>(ws + lay.head);
+    pl.starts = reinterpret_cast<PlanStart *>(ws + lay.starts);
+    pl.tickets = reinterpret_cast<int *>(ws + lay.tickets);
+    pl.seq_units = reinterpret_cast<long long *>(ws + lay.seq_units);
+    pl.tile_units = reinterpret_cast<long long *>(ws + lay.tile_units);
+    pl.err = p.a.err;
+    p.head = pl.head;
+    p.starts = pl.starts;
+    p.tickets = pl.tickets;
+    p.parts = reinterpret_cast<float *>(ws + lay.parts);
+    return pl;
+}
+
+// A CTA's way through its stretch, segment by segment: a segment is the stretch's part of one item.
+// Every role of a CTA walks the same segments on its own.
+struct Walk {
+    long long unit;       // of all units: the segment's first
+    int left;             // units of the stretch from the segment's first on
+    int seq, head, tile;  // the item
+    int lo, n, past;      // its sequence: first packed row, new tokens, cached rows before them
+    SeqRows rows;
+    ItemKeys keys;
+    int cnt;              // tokens of the item
+    int u0, u1;           // the segment's units of the item
+};
+
+__device__ __forceinline__ void walk_seq(Walk &w, const AttnParams &p) {
+    int hi;
+    chunk_rows(p.a.sq.off, p.a.sq.nt, w.seq, w.lo, hi);
+    w.n = hi - w.lo;
+    w.past = __ldg(p.a.sq.n_past + w.seq);
+    w.rows = seq_rows(p.a.c, w.seq);
+}
+// Position of the item's first token.
+__device__ __forceinline__ long long walk_pos(const Walk &w, const AttnParams &p) {
+    return static_cast<long long>(w.past) + w.tile * p.tt;
+}
+// Packed row of the item's first token.
+__device__ __forceinline__ int walk_row(const Walk &w, const AttnParams &p) { return w.lo + w.tile * p.tt; }
+
+template <int KT>
+__device__ __forceinline__ void walk_item(Walk &w, const AttnParams &p) {
+    w.cnt = min(p.tt, w.n - w.tile * p.tt);
+    const long long p0 = walk_pos(w, p);
+    w.keys = item_keys(p0, p0 + w.cnt - 1, w.rows.cap, p.a.window, p.a.n_sink, KT);
+    w.u1 = w.left < w.keys.units - w.u0 ? w.u0 + w.left : w.keys.units;
+}
+// The first segment; false where the stretch is empty.
+template <int KT>
+__device__ __forceinline__ bool walk_begin(Walk &w, const AttnParams &p, long long total, int ctas) {
+    if (static_cast<int>(blockIdx.x) >= ctas) return false;
+    const PlanStart st = p.starts[blockIdx.x];
+    w.unit = st.unit;
+    w.left = static_cast<int>(stretch_start(total, ctas, blockIdx.x + 1LL) - st.unit);
+    w.seq = st.seq;
+    w.head = st.head;
+    w.tile = st.tile;
+    w.u0 = st.u;
+    if (w.left <= 0) return false;
+    walk_seq(w, p);
+    walk_item<KT>(w, p);
+    return true;
+}
+template <int KT>
+__device__ __forceinline__ bool walk_next(Walk &w, const AttnParams &p) {
+    w.unit += w.u1 - w.u0;
+    w.left -= w.u1 - w.u0;
+    if (w.left <= 0) return false;
+    w.u0 = 0;  // units are left, so the item was finished
+    if ((w.tile + 1) * p.tt < w.n) {
+        ++w.tile;
+    } else {
+        w.tile = 0;
+        if (++w.head == p.a.nk) {
+            w.head = 0;
+            do {
+                ++w.seq;
+                walk_seq(w, p);
+            } while (w.n < p.least || w.n > p.most);
+        }
+    }
+    walk_item<KT>(w, p);
+    return true;
+}
+
+// Row j of the sequence is seen by some token of the item; some row of [j, j + n) is.
+__device__ __forceinline__ bool item_sees(const ItemKeys &k, int j) { return (j >= k.lo && j < k.hi) || j < k.sink; }
+__device__ __forceinline__ bool item_sees_some(const ItemKeys &k, int j, int n) {
+    return (j < k.hi && j + n > k.lo && k.lo < k.hi) || j < k.sink;
+}
+
 }  // namespace minf

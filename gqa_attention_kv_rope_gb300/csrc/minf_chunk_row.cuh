@@ -37,7 +37,7 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
         const bool see = j <= last && chunk_sees(job.p, j, window, n_sink);
         long long row = -1;
         if (see) {
-            row = seq_row(job.rows, j);
+            row = seq_row(c, job.rows, j);
             if (row < 0) missing = true;
         }
         float s = 0.0f;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) chunk_store_kernel(const ChunkStoreA
             if (p < 0 || p >= r.cap) {
                 if (first) flag_error(a.err, MINF_ERRBIT_STORE_POS);
             } else {
-                row = seq_row(r, static_cast<int>(p));
+                row = seq_row(a.c, r, static_cast<int>(p));
                 if (row < 0 && first) flag_error(a.err, MINF_ERRBIT_BLOCK);
             }
         }
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) chunk_read_kernel(const ChunkReadArg
             if (p < 0 || p >= r.cap) {
                 if (first) flag_error(a.err, MINF_ERRBIT_STORE_POS);
             } else {
-                row = seq_row(r, static_cast<int>(p));
+                row = seq_row(a.c, r, static_cast<int>(p));
                 if (row < 0 && first) flag_error(a.err, MINF_ERRBIT_BLOCK);
             }
         }

@@ -74,18 +74,6 @@ struct Meta {
     int abort_flag, last;
 };
 
-struct StreamParams {
-    ChunkAttnArgs a;
-    const PlanHead *head;
-    const PlanStart *starts;
-    int *tickets;
-    float *parts;
-    float scale_log2;
-    int tt;        // tokens of an item
-    int box_rows;  // rows of a TMA copy
-    int most;      // sequences with longer chunks are not this kernel's (see launch_chunk_attn)
-};
-
 // ----------------------------------------------------------------------------- warp-level wrappers
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -158,74 +146,13 @@ __device__ __forceinline__ uint32_t at16(int r, int c) {
     return static_cast<uint32_t>(r) * C::kRow + (static_cast<uint32_t>(C::SW ? c ^ (r & 7) : c) << 4);
 }
 
-// ----------------------------------------------------------------------------- the walk over segments
-struct Walk {
-    long long unit, end;
-    int seq, head, tile, u;
-    int lo, hi;
-    long long past;
-    SeqRows rows;
-    ItemKeys keys;
-    int t0, cnt, u0, u1;
-};
-__device__ __forceinline__ void walk_seq(Walk &w, const StreamParams &p) {
-    chunk_rows(p.a.sq.off, p.a.sq.nt, w.seq, w.lo, w.hi);
-    w.past = __ldg(p.a.sq.n_past + w.seq);
-    w.rows = seq_rows(p.a.c, w.seq);
-}
-__device__ __forceinline__ void walk_item(Walk &w, const StreamParams &p) {
-    w.t0 = w.tile * p.tt;
-    w.cnt = min(p.tt, w.hi - w.lo - w.t0);
-    const long long p0 = w.past + w.t0;
-    w.keys = item_keys(p0, p0 + w.cnt - 1, w.rows.cap, p.a.window, p.a.n_sink, KT);
-    w.u0 = w.u;
-    const long long left = w.end - w.unit;
-    w.u1 = left < w.keys.units - w.u0 ? w.u0 + static_cast<int>(left) : w.keys.units;
-}
-__device__ __forceinline__ bool walk_begin(Walk &w, const StreamParams &p, long long total, int ctas) {
-    if (static_cast<int>(blockIdx.x) >= ctas) return false;
-    const PlanStart st = p.starts[blockIdx.x];
-    w.unit = st.unit;
-    w.end = stretch_start(total, ctas, blockIdx.x + 1LL);
-    w.seq = st.seq;
-    w.head = st.head;
-    w.tile = st.tile;
-    w.u = st.u;
-    if (w.unit >= w.end) return false;
-    walk_seq(w, p);
-    walk_item(w, p);
-    return true;
-}
-__device__ __forceinline__ bool walk_next(Walk &w, const StreamParams &p) {
-    w.unit += w.u1 - w.u0;
-    if (w.unit >= w.end) return false;
-    w.u = 0;
-    if ((w.tile + 1) * p.tt < w.hi - w.lo) {
-        ++w.tile;
-    } else {
-        w.tile = 0;
-        if (++w.head == p.a.nk) {
-            w.head = 0;
-            do {
-                ++w.seq;
-                walk_seq(w, p);
-            } while (w.hi == w.lo || w.hi - w.lo > p.most);
-        }
-    }
-    walk_item(w, p);
-    return true;
-}
-__device__ __forceinline__ bool item_sees(const ItemKeys &k, int j) {
-    return (j >= k.lo && j < k.hi) || j < k.sink;
-}
-
 // ----------------------------------------------------------------------------- the producer
 struct Maps {
     CUtensorMap k, v, ks, vs;  // ks, vs: Q8_0 scales
 };
 
 template <int HD, typename T, int NT>
-__device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const StreamParams &p,
+__device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const AttnParams &p,
                                         long long total, int ctas) {
     using C = Cfg<HD, T, NT>;
     const int lane = threadIdx.x & 31;
@@ -236,13 +163,12 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
     volatile int *abort_flag = &mt.abort_flag;
     Walk w;
     int n = 0;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p)) {
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
         for (int u = w.u0; u < w.u1; ++u, ++n) {
             const int st = n % C::NS, j0 = unit_tile(w.keys, u) * KT, j = j0 + piece * p.box_rows;
             long long row = p.a.c.rows;  // past the map's end: zeros
             if (lane < copies) {
-                const bool need = (j < w.keys.hi && j + p.box_rows > w.keys.lo && w.keys.lo < w.keys.hi) || j < w.keys.sink;
-                if (need) row = seq_row(w.rows, j);
+                if (item_sees_some(w.keys, j, p.box_rows)) row = seq_row(p.a.c, w.rows, j);
                 if (row < 0) {
                     if (!is_v) flag_error(p.a.err, MINF_ERRBIT_BLOCK);
                     row = p.a.c.rows;
@@ -288,7 +214,7 @@ __device__ __forceinline__ void join_warps(float (&acc)[C::kRegs], float *buf, i
 }
 
 template <int HD, typename T, int NT>
-__device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const StreamParams &p, long long total, int ctas) {
+__device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const AttnParams &p, long long total, int ctas) {
     using C = Cfg<HD, T, NT>;
     constexpr int R = C::R, MT = HD / 16, NB = HD / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n8 = lane >> 2, c4 = lane & 3;
@@ -300,7 +226,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
     constexpr size_t kPart = static_cast<size_t>(R) * (HD + 2);
     int n = 0;
     Walk w;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p)) {
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
         // Q: a warp a row
         for (int r = warp; r < R; r += kWarps) {
@@ -309,7 +235,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
 #pragma unroll
             for (int e = 0; e < V; ++e) x[e] = 0.0f;
             if (r < rows) {
-                const long long t = w.lo + w.t0 + r / g;
+                const long long t = walk_row(w, p) + r / g;
                 const float *src = p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd + lane * V;
                 if constexpr (V == 4) {
                     const float4 y = __ldg(reinterpret_cast<const float4 *>(src));
@@ -348,7 +274,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
                 if (lane == 0) mt.q_fac[r] = pow2i(-sh);
             }
             if (lane == 0) {
-                const long long pos = w.past + w.t0 + r / g;
+                const long long pos = walk_pos(w, p) + r / g;
                 int4 lim = make_int4(0, 0, 0, 0);
                 if (r < rows && pos >= 0) {
                     lim.x = pos + 1 < w.rows.cap ? static_cast<int>(pos + 1) : w.rows.cap;
@@ -376,7 +302,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
 #pragma unroll
         for (int r = 0; r < C::kRegs; ++r) acc[r] = 0.0f;
         // keys seen by every row: no mask
-        const long long first = w.past + w.t0, last = first + w.cnt - 1;
+        const long long first = walk_pos(w, p), last = first + w.cnt - 1;
         const long long all_hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
         const long long all_lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
         for (int i = 0; i < tiles; ++i) {
@@ -385,8 +311,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
             const int st = q % C::NS, j0 = unit_tile(w.keys, w.u0 + i) * KT + key0;
             unsigned char *kst = smem + st * C::kStage, *vst = kst + C::kTile;
             mbar_wait(&mt.full[st], (q / C::NS) & 1, abort_flag, p.a.err);
-            const bool any = (j0 < w.keys.hi && j0 + 16 > w.keys.lo && w.keys.lo < w.keys.hi) || j0 < w.keys.sink;
-            if (any) {
+            if (item_sees_some(w.keys, j0, 16)) {
                 const bool edge = j0 < w.keys.lo || j0 + 16 > w.keys.hi;
                 if (!C::Q && edge) {
                     // rows that no token sees must hold zeros in V (their weight is zero, but 0 * inf is not)
@@ -750,7 +675,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
                         const int r = t * 8 + 2 * c4 + e;
                         if (r >= rows) continue;
                         const float inv = L[t][e] == 0.0f ? 0.0f : 1.0f / L[t][e];
-                        float *out = p.a.out + (static_cast<long long>(w.lo + w.t0 + r / g) * p.a.nh + w.head * g + r % g) * HD;
+                        float *out = p.a.out + (static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g) * HD;
                         bool odd = false;
 #pragma unroll
                         for (int k = 0; k < MT; ++k)
@@ -769,11 +694,11 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
             for (int r = warp; r < rows; r += kWarps) {
                 if (!mt.odd[r]) continue;
                 RowJob job;
-                const long long t = w.lo + w.t0 + r / g;
+                const long long t = walk_row(w, p) + r / g;
                 job.q = p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd;
                 job.out = p.a.out + (t * p.a.nh + w.head * g + r % g) * HD;
                 job.rows = w.rows;
-                job.p = w.past + w.t0 + r / g;
+                job.p = walk_pos(w, p) + r / g;
                 job.hk = w.head;
                 attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
             }
@@ -784,7 +709,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Str
 
 template <int HD, typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ StreamParams p) {
+    chunk_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams p) {
     using C = Cfg<HD, T, NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -820,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int HD, typename T, int NT>
-int launch(const StreamParams &p, int grid, cudaStream_t s) {
+int launch(const AttnParams &p, int grid, cudaStream_t s) {
     using C = Cfg<HD, T, NT>;
     const ChunkKv &c = p.a.c;
     Maps maps;
@@ -853,7 +778,7 @@ int launch(const StreamParams &p, int grid, cudaStream_t s) {
 }
 
 template <int HD, int NT>
-int launch_kind(const StreamParams &p, int grid, cudaStream_t s) {
+int launch_kind(const AttnParams &p, int grid, cudaStream_t s) {
     return p.a.c.kv == kKvQ8    ? launch<HD, Q8, NT>(p, grid, s)
            : p.a.c.kv == kKvF16 ? launch<HD, __half, NT>(p, grid, s)
                                 : launch<HD, float, NT>(p, grid, s);
@@ -874,36 +799,16 @@ size_t chunk_stream_workspace(int nt, int n_seq, int nh, int nk, int hd_kv, int 
 int launch_chunk_stream(const ChunkAttnArgs &a, void *workspace, int rows, int most, cudaStream_t s) {
     const int sms = sm_count(), g = a.nh / a.nk, n8 = row_tiles(rows);
     const PlanLayout lay = stream_layout(a.sq.nt, a.sq.n_seq, g, a.hd_kv, n8);
-    char *ws = static_cast<char *>(workspace);
-    StreamParams p = {};
+    AttnParams p = {};
     p.a = a;
     p.tt = 8 * n8 / g;
+    p.kt = KT;
+    p.least = 1;
     p.most = most;
-    p.head = reinterpret_cast<const PlanHead *>(ws + lay.head);
-    p.starts = reinterpret_cast<const PlanStart *>(ws + lay.starts);
-    p.tickets = reinterpret_cast<int *>(ws + lay.tickets);
-    p.parts = reinterpret_cast<float *>(ws + lay.parts);
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    PlanArgs pl = {};
-    pl.c = a.c;
-    pl.sq = a.sq;
-    pl.nk = a.nk;
-    pl.tt = p.tt;
-    pl.kt = KT;
-    pl.window = a.window;
-    pl.n_sink = a.n_sink;
-    pl.max_ctas = sms;
-    pl.min_units = 2;  // a tile for each group of warps
-    pl.least = 1;
-    pl.most = most;
-    pl.head = const_cast<PlanHead *>(p.head);
-    pl.starts = const_cast<PlanStart *>(p.starts);
-    pl.tickets = p.tickets;
-    pl.seq_units = reinterpret_cast<long long *>(ws + lay.seq_units);
-    pl.tile_units = reinterpret_cast<long long *>(ws + lay.tile_units);
-    pl.err = a.err;
-    const int st = launch_chunk_plan(pl, s);
+    // at least a tile for each group of warps in a stretch
+    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms, 2), s);
     if (st != MINF_OK) return st;
     if (a.hd_kv == 64)
         return n8 == 1 ? launch_kind<64, 1>(p, sms, s) : n8 == 2 ? launch_kind<64, 2>(p, sms, s) : launch_kind<64, 4>(p, sms, s);

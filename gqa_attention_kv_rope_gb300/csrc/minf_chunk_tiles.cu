@@ -25,10 +25,11 @@
 // P'_j 2^-e_j is the term of the sum: a large row cannot push the others out of binary16's range for
 // the rows that do not see it.  (Rows below 2^-46 keep the scale 2^60: what they lose is below 2^-70.)
 //
-// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues the MMAs, warp 11 copies the next
-// item's Q rows in, then the producers: for binary16 warps 9 and 10 issue TMA copies of K and V
-// (straight into the swizzled layout the tensor cores read; a block or a stretch of rows a copy);
-// otherwise warps 12-15 load, split and write K, and warps 16-19 V.
+// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues S, warp 10 issues P V (two threads, so
+// that neither's waits hold up the other's products), warp 11 copies the next item's Q rows in; then
+// the producers: for binary16 warps 9 (K) and 11 (V) issue TMA copies straight into the swizzled
+// layout that the tensor cores read, a block or a stretch of rows a copy; otherwise warps 12-15 load,
+// split and write K and V in turn (K of the next tile while P V runs, V while S does).
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
 // not); rows that only some tokens see can still carry infinities or NaN into the sums of those that
@@ -47,7 +48,7 @@ namespace {
 
 constexpr int BM = 128, KT = 128;
 constexpr int kRowThreads = 256;  // warps 0-7: two threads a query row
-constexpr int kMmaWarp = 8;
+constexpr int kScoreWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^(shift + slack) = 2^15
 // TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
 // column)
@@ -59,12 +60,12 @@ struct Cfg {
     static constexpr int SLABS = HD / 64;                        // 128-byte-wide slabs of a tile
     static constexpr int TERMS = HL ? 2 : 1;
     static constexpr int NS = HL ? (HD == 64 ? 2 : 1) : (HD == 64 ? 4 : 2);  // K and V stages
-    // Warp groups: rows (0, 1), then MMA and TMA warps (2), then the splitting producers (3, 4).  The
-    // rows' threads hold 64 scores and their halves, so registers move to them from the other groups;
-    // the shares add up to no more than the launch's: 256 * 208 + 128 * 88 = 384 * 168, and
-    // 256 * 144 + 384 * 64 = 640 * 96.
-    static constexpr int kThreads = HL ? 640 : 384;
-    static constexpr int kRowRegs = HL ? 144 : 208, kOtherRegs = HL ? 64 : 88;
+    // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3).  The rows'
+    // threads hold 64 scores and their halves and the producers a tile's rows, so registers move to
+    // them; the shares add up to no more than the launch's: 256 * 208 + 128 * 88 = 384 * 168, and
+    // 256 * 152 + 128 * 56 + 128 * 144 < 512 * 128.
+    static constexpr int kThreads = HL ? 512 : 384;
+    static constexpr int kRowRegs = HL ? 152 : 208, kIssueRegs = HL ? 56 : 88, kSplitRegs = 144;
     static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
@@ -76,24 +77,13 @@ struct Smem {
     unsigned char q[BM * C::kQRow];                    // the item's Q rows, fp32
     unsigned long long q_in, q_free, q_full, p_ready[2], o_done[2], s_full[2], k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
     unsigned long long k_stat[4], v_stat[4];           // hi + lo kinds: factors of a tile written
+    alignas(16) float out[BM][36];                     // 32 dims of the output rows on their way out
     float mx[2][2][BM], sum[2][BM];
     int odd[BM];                                       // rows whose result is not finite
     alignas(16) float k_fac[C::HL ? 4 : 1][KT];        // K row factors, V row exponents and 2^-e
     alignas(16) float v_exp[C::HL ? 4 : 1][KT], v_inv[C::HL ? 4 : 1][KT];
     uint32_t tmem_base;
     int abort_flag, last;
-};
-
-struct TileParams {
-    ChunkAttnArgs a;
-    const PlanHead *head;
-    const PlanStart *starts;
-    int *tickets;
-    float *parts;
-    float scale_log2;
-    int tt;        // tokens of a tile
-    int box_rows;  // rows of a TMA copy
-    int least;     // sequences with shorter chunks are not this kernel's (see launch_chunk_attn)
 };
 
 // ----------------------------------------------------------------------------- tensor-core wrappers
@@ -182,79 +172,14 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// ----------------------------------------------------------------------------- the walk over segments
-// A segment is a stretch's part of one item.  Every role walks the same segments.
-struct Walk {
-    long long unit, end;  // of all units
-    int seq, head, tile, u;
-    int lo, hi;           // packed rows of the sequence
-    long long past;
-    SeqRows rows;
-    // the segment
-    ItemKeys keys;
-    int t0, cnt;          // tokens of the item: first (in the chunk) and count
-    int u0, u1;           // its units in this stretch
-};
-
-__device__ __forceinline__ void walk_seq(Walk &w, const TileParams &p) {
-    chunk_rows(p.a.sq.off, p.a.sq.nt, w.seq, w.lo, w.hi);
-    w.past = __ldg(p.a.sq.n_past + w.seq);
-    w.rows = seq_rows(p.a.c, w.seq);
-}
-__device__ __forceinline__ void walk_item(Walk &w, const TileParams &p) {
-    w.t0 = w.tile * p.tt;
-    w.cnt = min(p.tt, w.hi - w.lo - w.t0);
-    const long long p0 = w.past + w.t0;
-    w.keys = item_keys(p0, p0 + w.cnt - 1, w.rows.cap, p.a.window, p.a.n_sink, KT);
-    w.u0 = w.u;
-    const long long left = w.end - w.unit;
-    w.u1 = left < w.keys.units - w.u0 ? w.u0 + static_cast<int>(left) : w.keys.units;
-}
-// The first segment; false where the stretch is empty.
-__device__ __forceinline__ bool walk_begin(Walk &w, const TileParams &p, long long total, int ctas) {
-    if (static_cast<int>(blockIdx.x) >= ctas) return false;
-    const PlanStart st = p.starts[blockIdx.x];
-    w.unit = st.unit;
-    w.end = stretch_start(total, ctas, blockIdx.x + 1LL);
-    w.seq = st.seq;
-    w.head = st.head;
-    w.tile = st.tile;
-    w.u = st.u;
-    if (w.unit >= w.end) return false;
-    walk_seq(w, p);
-    walk_item(w, p);
-    return true;
-}
-__device__ __forceinline__ bool walk_next(Walk &w, const TileParams &p) {
-    w.unit += w.u1 - w.u0;
-    if (w.unit >= w.end) return false;
-    w.u = 0;  // units are left, so the item was finished
-    if ((w.tile + 1) * p.tt < w.hi - w.lo) {
-        ++w.tile;
-    } else {
-        w.tile = 0;
-        if (++w.head == p.a.nk) {
-            w.head = 0;
-            do {
-                ++w.seq;
-                walk_seq(w, p);
-            } while (w.hi - w.lo < p.least);
-        }
-    }
-    walk_item(w, p);
-    return true;
-}
-
-// Row j of the sequence is seen by some token of the item.
-__device__ __forceinline__ bool item_sees(const ItemKeys &k, int j) {
-    return (j >= k.lo && j < k.hi) || j < k.sink;
-}
-
 // ----------------------------------------------------------------------------- producers
 // One warp: TMA copies of the stretch's K (or V) tiles, a lane a copy.  A copy that no visible row
 // lies in, or whose block is missing, reads past the map's end: zeros.
+template <int HD, typename T>
+__device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w);
+
 template <int HD, typename T, bool kV>
-__device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &map, const TileParams &p, long long total,
+__device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &map, const AttnParams &p, long long total,
                                            int ctas) {
     using C = Cfg<HD, T>;
     const int lane = threadIdx.x & 31;
@@ -262,8 +187,13 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     const int pieces = KT / p.box_rows, copies = pieces * C::SLABS;
     volatile int *abort_flag = &sm.abort_flag;
     Walk w;
-    int n = 0;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p)) {
+    int n = 0, seg = 0;
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
+        if constexpr (kV) {
+            // (the last item's rows were taken when it began, tiles ago)
+            if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
+            copy_q_rows<HD, T>(sm, p, w);
+        }
         for (int u = w.u0; u < w.u1; ++u, ++n) {
             const int st = n % C::NS, j0 = unit_tile(w.keys, u) * KT;
             unsigned long long *full = kV ? &sm.v_full[st] : &sm.k_full[st], *empty = kV ? &sm.v_empty[st] : &sm.k_empty[st];
@@ -272,8 +202,7 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
             const int j = j0 + piece * p.box_rows;
             if (lane < copies) {  // (at most 8 pieces of 16 rows x 2 slabs)
                 // any visible row in [j, j + box)?
-                const bool need = (j < w.keys.hi && j + p.box_rows > w.keys.lo && w.keys.lo < w.keys.hi) || j < w.keys.sink;
-                row = need ? seq_row(w.rows, j) : p.a.c.rows;
+                row = item_sees_some(w.keys, j, p.box_rows) ? seq_row(p.a.c, w.rows, j) : p.a.c.rows;
                 if (row < 0) {
                     if (!kV) flag_error(p.a.err, MINF_ERRBIT_BLOCK);
                     row = p.a.c.rows;
@@ -290,290 +219,350 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     }
 }
 
-// One warp: the next item's Q rows into the stage as soon as the row threads have taken the last ones.
+// One warp: an item's Q rows into the stage.
 template <int HD, typename T>
-__device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const TileParams &p, long long total, int ctas) {
+__device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w) {
     using C = Cfg<HD, T>;
-    const int lane = threadIdx.x & 31, g = p.a.nh / p.a.nk;
+    const int lane = threadIdx.x & 31, g = p.a.nh / p.a.nk, rows = w.cnt * g;
+    if (lane == 0) mbar_expect_tx(&sm.q_in, static_cast<uint32_t>(rows) * HD * 4);
+    __syncwarp();
+    for (int r = lane; r < rows; r += 32) {
+        const long long t = walk_row(w, p) + r / g;
+        bulk_load(sm.q + r * C::kQRow, p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd, HD * 4, &sm.q_in);
+    }
+    __syncwarp();
+}
+// The same for all items, as soon as the row threads have taken the last one's.
+template <int HD, typename T>
+__device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, long long total, int ctas) {
     volatile int *abort_flag = &sm.abort_flag;
     Walk w;
     int seg = 0;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
-        const int rows = w.cnt * g;
-        if (lane == 0) mbar_expect_tx(&sm.q_in, static_cast<uint32_t>(rows) * HD * 4);
-        __syncwarp();
-        for (int r = lane; r < rows; r += 32) {
-            const long long t = w.lo + w.t0 + r / g;
-            bulk_load(sm.q + r * C::kQRow, p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd, HD * 4, &sm.q_in);
-        }
-        __syncwarp();
+        copy_q_rows<HD, T>(sm, p, w);
     }
 }
 
-// Eight values of a cached row (8 * i8 ..), for the splitting producers.
-template <typename T>
-__device__ __forceinline__ void ld8(const unsigned char *row, int W, int i8, float (&x)[8]) {
-    float4 a, b;
-    if constexpr (std::is_same<T, Q8>::value) {
-        const uint2 q = reinterpret_cast<const uint2 *>(row)[i8];
-        const float s = __half2float(reinterpret_cast<const __half *>(row + W)[i8 >> 2]);
-        a = deq4(q.x, s);
-        b = deq4(q.y, s);
-    } else {
-        a = reinterpret_cast<const float4 *>(row)[2 * i8];
-        b = reinterpret_cast<const float4 *>(row)[2 * i8 + 1];
-    }
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-__device__ __forceinline__ float amax8(const float (&x)[8]) {
-    return fmaxf(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))),
-                 fmaxf(fmaxf(fabsf(x[4]), fabsf(x[5])), fmaxf(fabsf(x[6]), fabsf(x[7]))));
-}
-
-// Four warps: the stretch's K (or V) tiles as scaled hi + lo halves; a warp takes 32 of a tile's rows.
-// Lane r resolves row r (its block, and an L2 prefetch) one tile ahead; the values are loaded by eight
-// lanes a row, eight values of each slab a lane, four rows at a time and several such steps in flight.
-// V's row exponents also go out one tile ahead of its values: the row threads need them with S, while
-// the V stage may still be in use.
-template <int HD, typename T, bool kV>
-__device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const TileParams &p, int warp, long long total, int ctas) {
+// Four warps: the stretch's K and V tiles as scaled hi + lo halves; a warp takes 32 of a tile's rows.
+// Lane r resolves row r of the tile ahead (its block, and an L2 prefetch).  The values are loaded by
+// eight lanes a row, eight values of each slab a lane, four rows a step; Q8_0 rows of a whole tile are
+// held as they are stored, so that K's are in flight while V is split and the other way round.  V's
+// row exponents go out one tile ahead of its values: the row threads need them with S, while the V
+// stage may still be in use.
+template <int HD, typename T>
+struct Splitter {
     using C = Cfg<HD, T>;
-    constexpr bool Q = std::is_same<T, Q8>::value;
-    constexpr int STEP = Q ? 4 : 2;  // four-row steps in flight
-    const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
+    static constexpr bool Q = std::is_same<T, Q8>::value;
+    static constexpr int STEP = Q ? 8 : 4;  // four-row steps held at a time
+    Smem<HD, T> &sm;
+    const AttnParams &p;
+    int warp, lane, l8, sub;
+    uint2 raw[Q ? STEP : 1][C::SLABS];
+    __half2 sc[Q ? STEP : 1];  // the slabs' blocks' scales
+    float x[Q ? 1 : STEP][C::SLABS][8];
+
+    __device__ __forceinline__ Splitter(Smem<HD, T> &s, const AttnParams &pp, int wp)
+        : sm(s), p(pp), warp(wp), lane(threadIdx.x & 31), l8(lane & 7), sub(lane >> 3) {}
+
+    // Rows r0 .. of the tile; `at`: this lane's row's byte offset in the pool (negative: zeros).
+    __device__ __forceinline__ void load(const void *base, long long at, int head, int r0) {
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+            const long long o = __shfl_sync(0xffffffffu, at, r0 + 4 * i + sub);
+            const unsigned char *row = static_cast<const unsigned char *>(base) + o;
+            if constexpr (Q) {
+#pragma unroll
+                for (int s = 0; s < C::SLABS; ++s) raw[i][s] = make_uint2(0, 0);
+                sc[i] = __floats2half2_rn(0.0f, 0.0f);
+                if (o >= 0) {
+                    const __half *d = reinterpret_cast<const __half *>(row + p.a.c.W) + head * (HD / 32) + (l8 >> 2);
+#pragma unroll
+                    for (int s = 0; s < C::SLABS; ++s) raw[i][s] = __ldg(reinterpret_cast<const uint2 *>(row) + head * (HD / 8) + s * 8 + l8);
+                    sc[i] = __halves2half2(d[0], C::SLABS == 2 ? d[2] : d[0]);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < C::SLABS; ++s) {
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                    if (o >= 0) {
+                        const float4 *f = reinterpret_cast<const float4 *>(row) + head * (HD / 4) + s * 16 + 2 * l8;
+                        a = __ldg(f);
+                        b = __ldg(f + 1);
+                    }
+                    x[i][s][0] = a.x, x[i][s][1] = a.y, x[i][s][2] = a.z, x[i][s][3] = a.w;
+                    x[i][s][4] = b.x, x[i][s][5] = b.y, x[i][s][6] = b.z, x[i][s][7] = b.w;
+                }
+            }
+        }
+    }
+    // The loaded rows, scaled, split and written (K: with their factors).
+    template <bool kV>
+    __device__ __forceinline__ void put(int n, int r0) {
+        const int st = n % C::NS;
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+            const int r = warp * 32 + r0 + 4 * i + sub;
+            float f;
+            if constexpr (kV) {
+                f = sm.v_inv[n & 3][r];
+            } else {
+                float am;
+                if constexpr (Q) {  // no value is above 127 scales; four lanes share a block
+                    const float2 d = __half22float2(sc[i]);
+                    am = 127.0f * fmaxf(fabsf(d.x), fabsf(d.y));
+                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 4));
+                } else {
+                    am = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(x[i][s][e]));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+                }
+                const int sh = row_shift(am, 126);
+                f = pow2i(sh);
+                if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-sh);
+            }
+#pragma unroll
+            for (int s = 0; s < C::SLABS; ++s) {
+                uint32_t hi[4], lo[4];
+                if constexpr (Q) {
+                    // scale * 2^sh is a binary16 value (2^sh is exact; what a far smaller block's scale loses
+                    // is below 2^-33 of the row's largest value), a quant another; hi is their rounded product,
+                    // and the rest, at most 7 bits, comes exactly out of a fused multiply-add
+                    const __half d = __float2half_rn((s == 0 ? __low2float(sc[i]) : __high2float(sc[i])) * f);
+                    const __half2 dd = __halves2half2(d, d);
+                    const uint32_t u[2] = {raw[i][s].x ^ 0x80808080u, raw[i][s].y ^ 0x80808080u};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t b = __byte_perm(u[e >> 1], 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
+                        const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&b), __floats2half2_rn(1152.0f, 1152.0f));
+                        const __half2 h = __hmul2_rn(q, dd), l = __hfma2(q, dd, __hneg2(h));
+                        hi[e] = *reinterpret_cast<const uint32_t *>(&h);
+                        lo[e] = *reinterpret_cast<const uint32_t *>(&l);
+                    }
+                } else {
+                    const float2 ff = make_float2(f, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = mul2(make_float2(x[i][s][2 * e], x[i][s][2 * e + 1]), ff);
+                        split2(y.x, y.y, hi[e], lo[e]);
+                    }
+                }
+                unsigned char *h = kV ? sm.v[st][0][s] : sm.k[st][0][s], *l = kV ? sm.v[st][C::TERMS - 1][s] : sm.k[st][C::TERMS - 1][s];
+                *reinterpret_cast<uint4 *>(h + sw16(r, l8)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(l + sw16(r, l8)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+    }
+    // V's row exponents of tile n.
+    __device__ __forceinline__ void exponents(int n, long long at, int head) {
+        const int r = warp * 32 + lane;
+        float am = 0.0f;
+        if constexpr (Q) {  // no value is above 127 scales
+            if (at >= 0) {
+                const __half *d = reinterpret_cast<const __half *>(static_cast<const unsigned char *>(p.a.c.v) + at + p.a.c.W) + head * (HD / 32);
+#pragma unroll
+                for (int b = 0; b < HD / 32; ++b) am = fmaxf(am, 127.0f * fabsf(__half2float(d[b])));
+            }
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 4 * STEP) {
+                load(p.a.c.v, at, head, r0);
+#pragma unroll
+                for (int i = 0; i < STEP; ++i) {
+                    float m = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][s][e]));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    // to the lane of this row
+                    const float y = __shfl_sync(0xffffffffu, m, (lane & 3) * 8);
+                    if ((lane >> 2) == (r0 >> 2) + i) am = y;
+                }
+            }
+        }
+        const int sh = row_shift(am, 60);
+        sm.v_exp[n & 3][r] = static_cast<float>(-sh);
+        sm.v_inv[n & 3][r] = pow2i(sh);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_stat[n & 3]);
+    }
+};
+
+template <int HD, typename T>
+__device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p, int warp, long long total, int ctas) {
+    using S = Splitter<HD, T>;
+    using C = Cfg<HD, T>;
+    S sp(sm, p, warp);
+    const int lane = sp.lane;
     volatile int *abort_flag = &sm.abort_flag;
-    const unsigned char *base = static_cast<const unsigned char *>(kV ? p.a.c.v : p.a.c.k);
     Walk w;  // of the tile ahead
-    int u = 0, ahead = 0;
-    bool more = walk_begin(w, p, total, ctas);
-    if (more) u = w.u0;
-    // the tile ahead: this lane's row (null: hidden or missing), its head, and V's row exponents
-    const unsigned char *nxt = nullptr;
-    int nxt_head = 0;
+    bool more = walk_begin<KT>(w, p, total, ctas);
+    if (!more) return;
+    int u = w.u0, ahead = 0, nxt_head = 0;
+    long long nxt = -1;  // this lane's row of the tile ahead, as a byte offset (negative: hidden or missing)
     auto look_ahead = [&]() {
-        nxt = nullptr;
+        nxt = -1;
         nxt_head = w.head;
         const int j = unit_tile(w.keys, u) * KT + warp * 32 + lane;
         if (item_sees(w.keys, j)) {
-            const long long row = seq_row(w.rows, j);
+            const long long row = seq_row(p.a.c, w.rows, j);
             if (row >= 0)
-                nxt = base + row * p.a.c.row_bytes;
-            else if (!kV)
+                nxt = row * p.a.c.row_bytes;
+            else
                 flag_error(p.a.err, MINF_ERRBIT_BLOCK);
         }
-        if (nxt) {
-            const unsigned char *v = nxt + w.head * (HD * (Q ? 1 : 4));
+        constexpr int kBytes = HD * (S::Q ? 1 : 4);
+        if (nxt >= 0) {
+            const unsigned char *k = static_cast<const unsigned char *>(p.a.c.k) + nxt + w.head * kBytes;
+            const unsigned char *v = static_cast<const unsigned char *>(p.a.c.v) + nxt + w.head * kBytes;
 #pragma unroll
-            for (int b = 0; b < HD * (Q ? 1 : 4); b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(v + b));
-        }
-        if constexpr (kV) {
-            const int r = warp * 32 + lane;
-            if constexpr (Q) {  // no value is above 127 scales
-                float am = 0.0f;
-                if (nxt) {
-                    const __half *sc = reinterpret_cast<const __half *>(nxt + p.a.c.W) + w.head * (HD / 32);
-#pragma unroll
-                    for (int b = 0; b < HD / 32; ++b) am = fmaxf(am, 127.0f * fabsf(__half2float(sc[b])));
-                }
-                const int sh = row_shift(am, 60);
-                sm.v_exp[ahead & 3][r] = static_cast<float>(-sh);
-                sm.v_inv[ahead & 3][r] = pow2i(sh);
-            } else {
-#pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += 8) {
-                    float am[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const unsigned char *ptr = reinterpret_cast<const unsigned char *>(
-                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(nxt), r0 + 4 * i + sub));
-                        if (!ptr) continue;
-#pragma unroll
-                        for (int s = 0; s < C::SLABS; ++s) {
-                            float x[8];
-                            ld8<T>(ptr, p.a.c.W, w.head * (HD / 8) + s * 8 + l8, x);
-                            am[i] = fmaxf(am[i], amax8(x));
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                        for (int o = 1; o < 8; o <<= 1) am[i] = fmaxf(am[i], __shfl_xor_sync(0xffffffffu, am[i], o));
-                        if (l8 == 0) {
-                            const int sh = row_shift(am[i], 60), rr = warp * 32 + r0 + 4 * i + sub;
-                            sm.v_exp[ahead & 3][rr] = static_cast<float>(-sh);
-                            sm.v_inv[ahead & 3][rr] = pow2i(sh);
-                        }
-                    }
-                }
+            for (int b = 0; b < kBytes; b += 128) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(k + b));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + b));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_stat[ahead & 3]);
         }
         ++ahead;
         if (++u == w.u1) {
-            more = walk_next(w, p);
+            more = walk_next<KT>(w, p);
             u = w.u0;
         }
     };
-    if (!more) return;
     look_ahead();
+    sp.exponents(0, nxt, nxt_head);
+    if constexpr (S::Q) sp.load(p.a.c.k, nxt, nxt_head, 0);
     for (int n = 0; n < ahead; ++n) {
-        const int st = n % C::NS, head = nxt_head;
-        const unsigned char *cur = nxt;
+        const int st = n % C::NS, head = nxt_head, phase = ((n / C::NS) - 1) & 1;
+        const long long cur = nxt;
         if (more) look_ahead();
-        bool ready = n < C::NS;
+        const bool next = ahead > n + 1;
+        // K of tile n
+        auto wait_empty = [&](unsigned long long *bar) -> bool {
+            return n < C::NS || __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, p.a.err));
+        };
+        if constexpr (S::Q) {
+            if (!wait_empty(&sm.k_empty[st])) return;
+            sp.template put<false>(n, 0);
+        } else {
 #pragma unroll 1
-        for (int r0 = 0; r0 < 32; r0 += 4 * STEP) {
-            uint2 raw[Q ? STEP : 1][C::SLABS];  // quants, and their blocks' scales
-            float sc[Q ? STEP : 1][C::SLABS];
-            float x[Q ? 1 : STEP][C::SLABS][8];
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-                const unsigned char *ptr = reinterpret_cast<const unsigned char *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(cur), r0 + 4 * i + sub));
-#pragma unroll
-                for (int s = 0; s < C::SLABS; ++s) {
-                    const int i8 = head * (HD / 8) + s * 8 + l8;
-                    if constexpr (Q) {
-                        raw[i][s] = make_uint2(0, 0);
-                        sc[i][s] = 0.0f;
-                        if (ptr) {
-                            raw[i][s] = __ldg(reinterpret_cast<const uint2 *>(ptr) + i8);
-                            sc[i][s] = __half2float(reinterpret_cast<const __half *>(ptr + p.a.c.W)[i8 >> 2]);
-                        }
-                    } else if (ptr) {
-                        ld8<T>(ptr, p.a.c.W, i8, x[i][s]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[i][s][e] = 0.0f;
-                    }
-                }
-            }
-            if (!ready) {  // (the first rows' loads are in flight)
-                if (!__all_sync(0xffffffffu, mbar_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], ((n / C::NS) - 1) & 1,
-                                                       abort_flag, p.a.err)))
-                    return;
-                ready = true;
-            }
-#pragma unroll
-            for (int i = 0; i < STEP; ++i) {
-                const int r = warp * 32 + r0 + 4 * i + sub;
-                float f;
-                if constexpr (kV) {
-                    f = sm.v_inv[n & 3][r];
-                } else {
-                    float am;
-                    if constexpr (Q) {
-                        am = fabsf(sc[i][0]);
-                        if constexpr (C::SLABS == 2) am = fmaxf(am, fabsf(sc[i][1]));
-                        am *= 127.0f;  // no value is above 127 scales
-                        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 4));  // (four lanes share a block)
-                    } else {
-                        am = amax8(x[i][0]);
-                        if constexpr (C::SLABS == 2) am = fmaxf(am, amax8(x[i][1]));
-#pragma unroll
-                        for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                    }
-                    const int sh = row_shift(am, 126);
-                    f = pow2i(sh);
-                    if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-sh);
-                }
-#pragma unroll
-                for (int s = 0; s < C::SLABS; ++s) {
-                    float y[8];
-                    if constexpr (Q) {
-                        const float4 a = deq4(raw[i][s].x, sc[i][s] * f), b = deq4(raw[i][s].y, sc[i][s] * f);
-                        y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = x[i][s][e] * f;
-                    }
-                    uint4 hi, lo;
-                    split2(y[0], y[1], hi.x, lo.x);
-                    split2(y[2], y[3], hi.y, lo.y);
-                    split2(y[4], y[5], hi.z, lo.z);
-                    split2(y[6], y[7], hi.w, lo.w);
-                    unsigned char *h = kV ? sm.v[st][0][s] : sm.k[st][0][s], *l = kV ? sm.v[st][C::TERMS - 1][s] : sm.k[st][C::TERMS - 1][s];
-                    *reinterpret_cast<uint4 *>(h + sw16(r, l8)) = hi;
-                    *reinterpret_cast<uint4 *>(l + sw16(r, l8)) = lo;
-                }
+            for (int r0 = 0; r0 < 32; r0 += 4 * S::STEP) {
+                sp.load(p.a.c.k, cur, head, r0);
+                if (r0 == 0 && !wait_empty(&sm.k_empty[st])) return;
+                sp.template put<false>(n, r0);
             }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (!kV) mbar_arrive(&sm.k_stat[n & 3]);
-            mbar_arrive(kV ? &sm.v_full[st] : &sm.k_full[st]);
+            mbar_arrive(&sm.k_stat[n & 3]);
+            mbar_arrive(&sm.k_full[st]);
+        }
+        if constexpr (S::Q) sp.load(p.a.c.v, cur, head, 0);
+        if (next) sp.exponents(n + 1, nxt, nxt_head);
+        // V of tile n
+        if constexpr (S::Q) {
+            if (!wait_empty(&sm.v_empty[st])) return;
+            sp.template put<true>(n, 0);
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 4 * S::STEP) {
+                sp.load(p.a.c.v, cur, head, r0);
+                if (r0 == 0 && !wait_empty(&sm.v_empty[st])) return;
+                sp.template put<true>(n, r0);
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_full[st]);
+        if constexpr (S::Q) {
+            if (next) sp.load(p.a.c.k, nxt, nxt_head, 0);
         }
     }
 }
 
 // ----------------------------------------------------------------------------- the MMAs
+// In descriptor units: the halves of a tile, and a stage.
 template <int HD, typename T>
-__device__ __forceinline__ void issue_mmas(Smem<HD, T> &sm, const TileParams &p, uint32_t tmem, long long total, int ctas) {
+struct Desc {
     using C = Cfg<HD, T>;
+    static constexpr uint32_t kSlab = KT * 128;
+    static constexpr uint64_t kTerm = static_cast<uint64_t>(C::SLABS) * kSlab >> 4;
+    static constexpr uint64_t kStage = C::TERMS * kTerm;
+};
+
+template <int HD, typename T>
+__device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
+    using C = Cfg<HD, T>;
+    using D = Desc<HD, T>;
     volatile int *abort_flag = &sm.abort_flag;
-    constexpr uint32_t kIdS = idesc_f16(BM, KT, false), kIdO = idesc_f16(BM, HD, true);
-    constexpr uint32_t kSlab = KT * 128;
-    const uint64_t dk = desc128(su32(sm.k), 16), dv = desc128(su32(sm.v), kSlab);
-    constexpr uint64_t kStage = static_cast<uint64_t>(C::TERMS) * C::SLABS * kSlab >> 4;  // in descriptor units
-    constexpr uint64_t kTerm = static_cast<uint64_t>(C::SLABS) * kSlab >> 4;
+    constexpr uint32_t kId = idesc_f16(BM, KT, false);
+    const uint64_t dk = desc128(su32(sm.k), 16);
     const uint32_t qh = tmem + kColQ, ql = qh + HD / 2;
     int n = 0, seg = 0;
     Walk w;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
-        const int tiles = w.u1 - w.u0;
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         if (!mbar_wait(&sm.q_full, seg & 1, abort_flag, p.a.err)) return;
-        auto scores = [&](int i) -> bool {
-            const int st = (n + i) % C::NS;
-            if (!mbar_wait(&sm.k_full[st], ((n + i) / C::NS) & 1, abort_flag, p.a.err)) return false;
+        const int tiles = w.u1 - w.u0;
+        for (int i = 0; i < tiles; ++i, ++n) {
+            const int st = n % C::NS;
+            if (!mbar_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, p.a.err)) return;
+            // this buffer's last P: its product must be done (the item's first two tiles: with the last item)
+            if (i >= 2 && !mbar_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, p.a.err)) return;
             tc_after();
-            const uint32_t d = tmem + kColS + static_cast<uint32_t>((n + i) & 1) * KT;
-            const uint64_t k0 = dk + st * kStage;
+            const uint32_t d = tmem + kColS + static_cast<uint32_t>(n & 1) * KT;
+            const uint64_t k0 = dk + st * D::kStage;
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint64_t o = static_cast<uint64_t>(kk >> 2) * (kSlab >> 4) + 2 * (kk & 3);
-                mma_ts(d, qh + kk * 8, k0 + o, kIdS, kk > 0);
-                mma_ts(d, ql + kk * 8, k0 + o, kIdS, true);
-                if constexpr (C::HL) mma_ts(d, qh + kk * 8, k0 + kTerm + o, kIdS, true);
+                const uint64_t o = static_cast<uint64_t>(kk >> 2) * (D::kSlab >> 4) + 2 * (kk & 3);
+                mma_ts(d, qh + kk * 8, k0 + o, kId, kk > 0);
+                mma_ts(d, ql + kk * 8, k0 + o, kId, true);
+                if constexpr (C::HL) mma_ts(d, qh + kk * 8, k0 + D::kTerm + o, kId, true);
             }
-            commit(&sm.s_full[(n + i) & 1]);
+            commit(&sm.s_full[n & 1]);
             commit(&sm.k_empty[st]);
-            return true;
-        };
-        if (!scores(0)) return;
-        if (tiles > 1 && !scores(1)) return;
-        for (int i = 0; i < tiles; ++i) {
-            const int st = (n + i) % C::NS;
-            if (!mbar_wait(&sm.v_full[st], ((n + i) / C::NS) & 1, abort_flag, p.a.err)) return;
-            if (!mbar_wait(&sm.p_ready[(n + i) & 1], ((n + i) >> 1) & 1, abort_flag, p.a.err)) return;
+        }
+    }
+}
+
+template <int HD, typename T>
+__device__ __forceinline__ void issue_values(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
+    using C = Cfg<HD, T>;
+    using D = Desc<HD, T>;
+    volatile int *abort_flag = &sm.abort_flag;
+    constexpr uint32_t kId = idesc_f16(BM, HD, true);
+    const uint64_t dv = desc128(su32(sm.v), D::kSlab);
+    int n = 0;
+    Walk w;
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
+        const int tiles = w.u1 - w.u0;
+        for (int i = 0; i < tiles; ++i, ++n) {
+            const int st = n % C::NS;
+            if (!mbar_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, p.a.err)) return;
+            if (!mbar_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, p.a.err)) return;
             tc_after();
-            const uint32_t p0 = tmem + kColS + static_cast<uint32_t>((n + i) & 1) * KT;
-            const uint64_t v0 = dv + st * kStage;
+            const uint64_t v0 = dv + st * D::kStage;
+            const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {
                 const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
-                const uint32_t ph = p0 + kk * 8, pl = ph + 64;
-                mma_ts(tmem + kColO, ph, v0 + o, kIdO, i > 0 || kk > 0);
-                mma_ts(tmem + kColO, pl, v0 + o, kIdO, true);
-                if constexpr (C::HL) mma_ts(tmem + kColO, ph, v0 + kTerm + o, kIdO, true);
+                mma_ts(tmem + kColO, ph + kk * 8, v0 + o, kId, i > 0 || kk > 0);
+                mma_ts(tmem + kColO, pl + kk * 8, v0 + o, kId, true);
+                if constexpr (C::HL) mma_ts(tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
             }
-            commit(&sm.o_done[(n + i) & 1]);
+            commit(&sm.o_done[n & 1]);
             commit(&sm.v_empty[st]);
-            if (i + 2 < tiles) {  // over P of this tile: once its product is done
-                if (!mbar_wait(&sm.o_done[(n + i) & 1], ((n + i) >> 1) & 1, abort_flag, p.a.err)) return;
-                if (!scores(i + 2)) return;
-            }
         }
-        n += tiles;
     }
 }
 
 // ----------------------------------------------------------------------------- the rows
 template <int HD, typename T>
-__device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, uint32_t tmem, long long total, int ctas) {
+__device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
     using C = Cfg<HD, T>;
     constexpr int HALF = HD / 2;  // dims of O a thread owns
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -582,9 +571,16 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
     const int g = p.a.nh / p.a.nk;
     volatile int *abort_flag = &sm.abort_flag;
     int32_t *err = p.a.err;
+    // where this thread's four rows of an output pass lie in an item (32 bits: an item spans 128 / g tokens)
+    int out_at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = k * 32 + (tid >> 3), q = tid & 7;
+        out_at[k] = ((r / g) * p.a.nh + r % g) * HD + (q >> 2) * HALF + (q & 3) * 4;
+    }
     int n = 0, seg = 0;
     Walk w;
-    for (bool more = walk_begin(w, p, total, ctas); more; more = walk_next(w, p), ++seg) {
+    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
         // this half row of Q, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
         float c;
@@ -623,7 +619,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
         }
         const bool warp_live = (row & ~31) < rows, live = row < rows;
         // this row's window: keys [r_lo, r_hi) and [0, r_sink)
-        const long long pos = w.past + w.t0 + row / g;
+        const long long pos = walk_pos(w, p) + row / g;
         int r_hi = 0, r_lo = 0, r_sink = 0;
         if (live && pos >= 0) {
             r_hi = pos + 1 < w.rows.cap ? static_cast<int>(pos + 1) : w.rows.cap;
@@ -634,7 +630,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
             }
         }
         // tiles in [all_lo, all_hi) (rows) are seen whole by every row: no mask
-        const long long first = w.past + w.t0, last = first + w.cnt - 1;
+        const long long first = walk_pos(w, p), last = first + w.cnt - 1;
         const long long all_hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
         const long long all_lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
         float m = -INFINITY, l = 0.0f;
@@ -642,18 +638,6 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
             mbar_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
             tc_after();
-            if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
-                // rows of this tile that no token sees: V must hold zeros there
-                mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
-                if (half == 0 && !item_sees(w.keys, j0 + row)) {
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll
-                        for (int ch = 0; ch < 8; ++ch)
-                            *reinterpret_cast<uint4 *>(sm.v[q % C::NS][0][s] + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_async_smem();
-            }
             if (!warp_live) {
                 named_sync(1, kRowThreads);
             } else {
@@ -745,6 +729,18 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
                 l = l * corr + ((s2.x + s2.y) + (s3.x + s3.y));
                 tm_wait_st();
             }
+            if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
+                // rows of this tile that no token sees: V must hold zeros there
+                mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
+                if (half == 0 && !item_sees(w.keys, j0 + row)) {
+#pragma unroll
+                    for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll
+                        for (int ch = 0; ch < 8; ++ch)
+                            *reinterpret_cast<uint4 *>(sm.v[q % C::NS][0][s] + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+            }
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
@@ -757,29 +753,38 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
         l = sm.sum[0][row] + sm.sum[1][row];
         const long long item0 = w.unit - w.u0;  // the item's first unit
         const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
-        float *out = p.a.out + (static_cast<long long>(w.lo + w.t0 + row / g) * p.a.nh + w.head * g + row % g) * HD + half * HALF;
+        // 16 dims of each half at a time through shared memory, so that a row's dims go out together
+        // (a thread's own 16 bytes a row at a time cost 32 transactions an instruction)
+        float *item_out = p.a.out + (static_cast<long long>(walk_row(w, p)) * p.a.nh + w.head * g) * HD;
+        auto put = [&](const float *y, int d) {
+            *reinterpret_cast<float4 *>(&sm.out[row][half * 16]) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 8]) = make_float4(y[8], y[9], y[10], y[11]);
+            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 12]) = make_float4(y[12], y[13], y[14], y[15]);
+            named_sync(1, kRowThreads);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = k * 32 + (tid >> 3);  // eight lanes a row: four of each half
+                if (r < rows)
+                    *reinterpret_cast<float4 *>(item_out + out_at[k] + d) = *reinterpret_cast<const float4 *>(&sm.out[r][(tid & 7) * 4]);
+            }
+            named_sync(1, kRowThreads);
+        };
         bool finish = whole, odd = false;
         if (whole) {
-            if (warp_live) {
-                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll 1
+            for (int d = 0; d < HALF; d += 16) {
+                uint32_t o[16];
+                float y[16];
+                tm_ld16(lanes + kColO + half * HALF + d, o);
+                tm_wait_ld();
 #pragma unroll
-                for (int d = 0; d < HALF; d += 32) {
-                    uint32_t o[32];
-                    tm_ld32(lanes + kColO + half * HALF + d, o);
-                    tm_wait_ld();
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 y;
-                            y.x = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
-                            y.y = l == 0.0f ? 0.0f : __uint_as_float(o[e + 1]) * inv;
-                            y.z = l == 0.0f ? 0.0f : __uint_as_float(o[e + 2]) * inv;
-                            y.w = l == 0.0f ? 0.0f : __uint_as_float(o[e + 3]) * inv;
-                            odd |= !(fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY);
-                            reinterpret_cast<float4 *>(out)[(d + e) >> 2] = y;
-                        }
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    y[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                    odd |= !(fabsf(y[e]) < INFINITY);
                 }
+                put(y, d);
             }
         } else {
             // this stretch's part: O as [dims / 4][rows] float4, then the rows' maxima and sums
@@ -809,65 +814,67 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
             if (tid == 0) sm.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
             named_sync(1, kRowThreads);
             finish = sm.last != 0;
-            if (finish && live) {
+            if (finish) {
                 __threadfence();
-                // join the parts in the order of their keys
+                // join the parts in the order of their keys (dead rows read what is there and are not put)
                 float M = -INFINITY;
 #pragma unroll 4
                 for (int b = b0; b <= b1; ++b) {
                     const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                     M = fmaxf(M, __ldcg(q + BM * HD + row));
                 }
+                constexpr int JD = 32;  // dims of a pass
 #pragma unroll 1
-                for (int d0 = 0; d0 < HALF / 4; d0 += 8) {  // 32 dims at a time
+                for (int d0 = 0; d0 < HALF; d0 += JD) {
                     float L = 0.0f;
-                    float4 acc[8];
+                    float y[JD];
 #pragma unroll
-                    for (int d = 0; d < 8; ++d) acc[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+                    for (int d = 0; d < JD; ++d) y[d] = 0.0f;
+#pragma unroll(C::HL ? 2 : 3)
                     for (int b = b0; b <= b1; ++b) {
                         const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                         const float mb = __ldcg(q + BM * HD + row), lb = __ldcg(q + BM * (HD + 1) + row);
-                        float4 y[8];
+                        float4 x[JD / 4];
 #pragma unroll
-                        for (int d = 0; d < 8; ++d) y[d] = __ldcg(reinterpret_cast<const float4 *>(q) + (half * (HALF / 4) + d0 + d) * BM + row);
-                        if (mb == -INFINITY && lb == 0.0f) continue;  // saw nothing
-                        const float f = ex2_approx(mb - M);
-                        L = fmaf(lb, f, L);
+                        for (int d = 0; d < JD / 4; ++d) x[d] = __ldcg(reinterpret_cast<const float4 *>(q) + ((half * HALF + d0) / 4 + d) * BM + row);
+                        const bool none = mb == -INFINITY && lb == 0.0f;  // saw nothing, whatever it holds
+                        const float f = none ? 0.0f : ex2_approx(mb - M);
+                        L = fmaf(none ? 0.0f : lb, f, L);
 #pragma unroll
-                        for (int d = 0; d < 8; ++d) {
-                            acc[d].x = fmaf(y[d].x, f, acc[d].x);
-                            acc[d].y = fmaf(y[d].y, f, acc[d].y);
-                            acc[d].z = fmaf(y[d].z, f, acc[d].z);
-                            acc[d].w = fmaf(y[d].w, f, acc[d].w);
+                        for (int d = 0; d < JD / 4; ++d) {
+                            y[4 * d] = none ? y[4 * d] : fmaf(x[d].x, f, y[4 * d]);
+                            y[4 * d + 1] = none ? y[4 * d + 1] : fmaf(x[d].y, f, y[4 * d + 1]);
+                            y[4 * d + 2] = none ? y[4 * d + 2] : fmaf(x[d].z, f, y[4 * d + 2]);
+                            y[4 * d + 3] = none ? y[4 * d + 3] : fmaf(x[d].w, f, y[4 * d + 3]);
                         }
                     }
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-                    for (int d = 0; d < 8; ++d) {
-                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (L != 0.0f) y = make_float4(acc[d].x * inv, acc[d].y * inv, acc[d].z * inv, acc[d].w * inv);
-                        odd |= !(fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY && fabsf(y.w) < INFINITY);
-                        reinterpret_cast<float4 *>(out)[d0 + d] = y;
+                    for (int d = 0; d < JD; ++d) {
+                        y[d] = L == 0.0f ? 0.0f : y[d] * inv;
+                        odd |= !(fabsf(y[d]) < INFINITY);
                     }
+                    put(y, d0);
+                    put(y + 16, d0 + 16);
                 }
             }
         }
         if (finish) {
+            odd = odd && live;
             if (odd) sm.odd[row] = 1;
-            named_sync(1, kRowThreads);
             // rows that are not finite: by the definition, a row a warp
-            for (int r = warp; r < rows; r += kRowThreads / 32) {
-                if (!sm.odd[r]) continue;
-                RowJob job;
-                const long long t = w.lo + w.t0 + r / g;
-                job.q = p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd;
-                job.out = p.a.out + (t * p.a.nh + w.head * g + r % g) * HD;
-                job.rows = w.rows;
-                job.p = w.past + w.t0 + r / g;
-                job.hk = w.head;
-                attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
-            }
+            if (!named_all(1, kRowThreads, !odd))
+                for (int r = warp; r < rows; r += kRowThreads / 32) {
+                    if (!sm.odd[r]) continue;
+                    RowJob job;
+                    const long long at = static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g;
+                    job.q = p.a.q + at * p.a.hd;
+                    job.out = p.a.out + at * HD;
+                    job.rows = w.rows;
+                    job.p = walk_pos(w, p) + r / g;
+                    job.hk = w.head;
+                    attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
+                }
         }
         tc_before();
         named_sync(1, kRowThreads);  // sm.odd and sm.sum are free for the next segment
@@ -877,7 +884,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const TileParams &p, ui
 template <int HD, typename T>
 __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     chunk_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ TileParams p) {
+                       const __grid_constant__ AttnParams p) {
     using C = Cfg<HD, T>;
     extern __shared__ unsigned char smem_raw[];
     Smem<HD, T> &sm = *reinterpret_cast<Smem<HD, T> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             prefetch_tensormap(&tm_v);
         }
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sm.tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
@@ -924,29 +931,29 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     if (warp < kRowThreads / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRowRegs));
         do_rows<HD, T>(sm, p, tmem, total, ctas);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        if (warp == kMmaWarp) {
-            if (lane == 0) issue_mmas<HD, T>(sm, p, tmem, total, ctas);
+    } else if (!C::HL || warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+        if (warp == kScoreWarp) {
+            if (lane == 0) issue_scores<HD, T>(sm, p, tmem, total, ctas);
             __syncwarp();
-        } else if (warp == kMmaWarp + 3) {
-            copy_q<HD, T>(sm, p, total, ctas);
+        } else if (warp == kValueWarp) {
+            if (lane == 0) issue_values<HD, T>(sm, p, tmem, total, ctas);
+            __syncwarp();
         } else if constexpr (C::HL) {
-            if (warp >= 16)
-                split_tiles<HD, T, true>(sm, p, warp - 16, total, ctas);
-            else if (warp >= 12)
-                split_tiles<HD, T, false>(sm, p, warp - 12, total, ctas);
+            if (warp == kQueryWarp) copy_q<HD, T>(sm, p, total, ctas);
+        } else if (warp == kKeyWarp) {
+            copy_tiles<HD, T, false>(sm, tm_k, p, total, ctas);
         } else {
-            if (warp == kMmaWarp + 1)
-                copy_tiles<HD, T, false>(sm, tm_k, p, total, ctas);
-            else if (warp == kMmaWarp + 2)
-                copy_tiles<HD, T, true>(sm, tm_v, p, total, ctas);
+            copy_tiles<HD, T, true>(sm, tm_v, p, total, ctas);
         }
+    } else if constexpr (C::HL) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSplitRegs));
+        split_tiles<HD, T>(sm, p, warp - 12, total, ctas);
     }
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         if (*static_cast<volatile int *>(&sm.abort_flag)) {
             // a wait ran out: let copies and MMAs in flight finish before TMEM and shared memory go away
             const unsigned long long t0 = gtimer();
@@ -959,7 +966,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
 }
 
 template <int HD, typename T>
-int launch(const TileParams &p, int grid, cudaStream_t s) {
+int launch(const AttnParams &p, int grid, cudaStream_t s) {
     using C = Cfg<HD, T>;
     CUtensorMap tk = {}, tv = {};
     if constexpr (!C::HL) {
@@ -1000,36 +1007,15 @@ size_t chunk_tiles_workspace(int nt, int n_seq, int nh, int nk, int hd_kv) {
 int launch_chunk_tiles(const ChunkAttnArgs &a, void *workspace, int least, cudaStream_t s) {
     const int sms = sm_count();
     const PlanLayout lay = tiles_layout(a.sq.nt, a.sq.n_seq, a.nh, a.nk, a.hd_kv);
-    char *ws = static_cast<char *>(workspace);
-    TileParams p = {};
+    AttnParams p = {};
     p.a = a;
     p.tt = BM / (a.nh / a.nk);
+    p.kt = KT;
     p.least = least;
-    p.head = reinterpret_cast<const PlanHead *>(ws + lay.head);
-    p.starts = reinterpret_cast<const PlanStart *>(ws + lay.starts);
-    p.tickets = reinterpret_cast<int *>(ws + lay.tickets);
-    p.parts = reinterpret_cast<float *>(ws + lay.parts);
+    p.most = 0x7fffffff;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    PlanArgs pl = {};
-    pl.c = a.c;
-    pl.sq = a.sq;
-    pl.nk = a.nk;
-    pl.tt = p.tt;
-    pl.kt = KT;
-    pl.window = a.window;
-    pl.n_sink = a.n_sink;
-    pl.max_ctas = sms;
-    pl.min_units = 1;
-    pl.least = least;
-    pl.most = 0x7fffffff;
-    pl.head = const_cast<PlanHead *>(p.head);
-    pl.starts = const_cast<PlanStart *>(p.starts);
-    pl.tickets = p.tickets;
-    pl.seq_units = reinterpret_cast<long long *>(ws + lay.seq_units);
-    pl.tile_units = reinterpret_cast<long long *>(ws + lay.tile_units);
-    pl.err = a.err;
-    const int st = launch_chunk_plan(pl, s);
+    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms, 1), s);
     if (st != MINF_OK) return st;
     if (a.hd_kv == 64)
         return a.c.kv == kKvQ8    ? launch<64, Q8>(p, sms, s)
