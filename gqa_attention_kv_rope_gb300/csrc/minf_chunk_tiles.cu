@@ -24,12 +24,16 @@
 // V_j = V'_j 2^e_j, and the softmax runs on t_j = s_j + e_j, so P'_j = 2^(t_j - M) weighs V'_j and
 // P'_j 2^-e_j is the term of the sum: a large row cannot push the others out of binary16's range for
 // the rows that do not see it.  (Rows below 2^-46 keep the scale 2^60: what they lose is below 2^-70.)
+// Where a tile's rows are within 2^16 of its largest, as they nearly always are, one factor serves the
+// whole tile (its small rows still have all their 22 bits) and the row threads need no factor a key:
+// those would take half of the shared-memory bandwidth.
 //
 // Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues S, warp 10 issues P V (two threads, so
 // that neither's waits hold up the other's products), warp 11 copies the next item's Q rows in; then
 // the producers: for binary16 warps 9 (K) and 11 (V) issue TMA copies straight into the swizzled
-// layout that the tensor cores read, a block or a stretch of rows a copy; otherwise warps 12-15 load,
-// split and write K and V in turn (K of the next tile while P V runs, V while S does).
+// layout that the tensor cores read, a block or a stretch of rows a copy; otherwise warp 9
+// resolves the tiles' rows ahead, warps 12-15 load, split and write K and warps 16-19 V (K of the next
+// tile while P V runs, V while S does).
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
 // not); rows that only some tokens see can still carry infinities or NaN into the sums of those that
@@ -48,6 +52,7 @@ namespace {
 
 constexpr int BM = 128, KT = 128;
 constexpr int kRowThreads = 256;  // warps 0-7: two threads a query row
+constexpr int kSplitWarps = 4, kSplitRows = KT / kSplitWarps;  // for K and for V each; rows of a tile a warp takes
 constexpr int kScoreWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^(shift + slack) = 2^15
 // TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
@@ -60,12 +65,12 @@ struct Cfg {
     static constexpr int SLABS = HD / 64;                        // 128-byte-wide slabs of a tile
     static constexpr int TERMS = HL ? 2 : 1;
     static constexpr int NS = HL ? (HD == 64 ? 2 : 1) : (HD == 64 ? 4 : 2);  // K and V stages
-    // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3).  The rows'
-    // threads hold 64 scores and their halves and the producers a tile's rows, so registers move to
-    // them; the shares add up to no more than the launch's: 256 * 208 + 128 * 88 = 384 * 168, and
-    // 256 * 152 + 128 * 56 + 128 * 144 < 512 * 128.
-    static constexpr int kThreads = HL ? 512 : 384;
-    static constexpr int kRowRegs = HL ? 152 : 208, kIssueRegs = HL ? 56 : 88, kSplitRegs = 144;
+    // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3, 4).  The rows'
+    // threads hold 64 scores and their halves, so registers move to them; the shares add up to the
+    // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
+    static constexpr int kThreads = HL ? 640 : 384;
+    static constexpr int kRowRegs = HL ? 144 : 208, kIssueRegs = HL ? 48 : 88;
+    static constexpr int kSplitRegs = 72;  // (HL)
     static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
@@ -77,13 +82,27 @@ struct Smem {
     unsigned char q[BM * C::kQRow];                    // the item's Q rows, fp32
     unsigned long long q_in, q_free, q_full, p_ready[2], o_done[2], s_full[2], k_full[C::NS], k_empty[C::NS], v_full[C::NS], v_empty[C::NS];
     unsigned long long k_stat[4], v_stat[4];           // hi + lo kinds: factors of a tile written
+    unsigned long long row_full[4], row_free[4];       // and its rows resolved, taken
     alignas(16) float out[BM][36];                     // 32 dims of the output rows on their way out
     float mx[2][2][BM], sum[2][BM];
     int odd[BM];                                       // rows whose result is not finite
-    alignas(16) float k_fac[C::HL ? 4 : 1][KT];        // K row factors, V row exponents and 2^-e
+    // hi + lo kinds, tile n in slot n % 4: K row factors, V row exponents and 2^-e; the smallest and the
+    // largest shifts of each splitting warp's rows (K, V); what the row threads go by
+    alignas(16) float k_fac[C::HL ? 4 : 1][KT];
     alignas(16) float v_exp[C::HL ? 4 : 1][KT], v_inv[C::HL ? 4 : 1][KT];
+    int rows[C::HL ? 4 : 1][KT];                       // rows of the pool (-1: zeros)
+    int row_head[C::HL ? 4 : 1];                       // their kv head (-1: no more tiles)
+    int2 shifts[2][C::HL ? 4 : 1][kSplitWarps];
+    struct TileFactors {
+        float exp, fac;  // the tile's: V's e and 2^-e; K's factor in fac
+        int by_row;      // its rows have their own
+    } k_tile[C::HL ? 4 : 1], v_tile[C::HL ? 4 : 1];
     uint32_t tmem_base;
     int abort_flag, last;
+    // the row threads lead the two issuing threads (which would need registers to walk on their own):
+    // tiles of the segment whose Q is ready (0: no more), and of a tile whose P is: 1 the segment's
+    // first, 2 the last of all
+    int seg_tiles, p_flag[2];
 };
 
 // ----------------------------------------------------------------------------- tensor-core wrappers
@@ -145,6 +164,10 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *u) {
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint32_t (&u)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
+}
 
 // Byte offset of the 16-byte chunk c of a row in a 128-byte-swizzled slab.
 __device__ __forceinline__ uint32_t sw16(int row, int c) {
@@ -244,244 +267,325 @@ __device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, lon
     }
 }
 
-// Four warps: the stretch's K and V tiles as scaled hi + lo halves; a warp takes 32 of a tile's rows.
-// Lane r resolves row r of the tile ahead (its block, and an L2 prefetch).  The values are loaded by
-// eight lanes a row, eight values of each slab a lane, four rows a step; Q8_0 rows of a whole tile are
-// held as they are stored, so that K's are in flight while V is split and the other way round.  V's
-// row exponents go out one tile ahead of its values: the row threads need them with S, while the V
-// stage may still be in use.
-template <int HD, typename T>
-struct Splitter {
-    using C = Cfg<HD, T>;
-    static constexpr bool Q = std::is_same<T, Q8>::value;
-    static constexpr int STEP = Q ? 8 : 4;  // four-row steps held at a time
-    Smem<HD, T> &sm;
-    const AttnParams &p;
-    int warp, lane, l8, sub;
-    uint2 raw[Q ? STEP : 1][C::SLABS];
-    __half2 sc[Q ? STEP : 1];  // the slabs' blocks' scales
-    float x[Q ? 1 : STEP][C::SLABS][8];
+// Four warps each: the stretch's K and V tiles as scaled hi + lo halves; a warp takes 32 of a tile's
+// rows.  V's exponents go out a tile ahead (the row threads need them with S, while the V stage may
+// still be in use); fp32 rows are prefetched into L2.  Eight lanes load, split and write a row, four
+// rows a step.  (The rows come resolved from warp 9: a walk of their own would take the registers
+// that the splitting warps hold rows in.)
 
-    __device__ __forceinline__ Splitter(Smem<HD, T> &s, const AttnParams &pp, int wp)
-        : sm(s), p(pp), warp(wp), lane(threadIdx.x & 31), l8(lane & 7), sub(lane >> 3) {}
-
-    // Rows r0 .. of the tile; `at`: this lane's row's byte offset in the pool (negative: zeros).
-    __device__ __forceinline__ void load(const void *base, long long at, int head, int r0) {
+// Eight lanes a row: VPL consecutive values a lane, a warp's rows of a whole tile held as they
+// are stored, loaded as soon as the last tile's have been written.
+template <int HD>
+struct SplitQ8 {
+    static constexpr int VPL = HD / 8, CH = VPL / 8;  // values and 16-byte chunks of halves a lane
+    static constexpr int STEPS = kSplitRows / 4;
+    uint2 raw[STEPS][CH];
+    // Values of hidden rows are whatever row 0 holds times a scale of zero.
+    static __device__ __forceinline__ uint2 load_scales(const void *base, const ChunkKv &c, int row, int head) {
+        uint2 d = make_uint2(0, 0);
+        if (row < 0) return d;
+        const unsigned char *q = static_cast<const unsigned char *>(base) + row * c.row_bytes + c.W + head * (HD / 16);
+        if constexpr (HD == 128)
+            d = __ldg(reinterpret_cast<const uint2 *>(q));
+        else
+            d.x = __ldg(reinterpret_cast<const uint32_t *>(q));
+        return d;
+    }
+    static __device__ __forceinline__ float most(uint2 d) {  // no value is above 127 scales
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&d.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&d.y));
+        return 127.0f * fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
+    }
+    // scale * 2^sh is a binary16 value (2^sh is exact; what a far smaller block's scale loses is below
+    // 2^-33 of the row's largest value).
+    static __device__ __forceinline__ uint32_t times(uint32_t d, float f) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&d));
+        const __half2 y = __floats2half2_rn(a.x * f, a.y * f);
+        return *reinterpret_cast<const uint32_t *>(&y);
+    }
+    __device__ __forceinline__ void load(const void *pool, const ChunkKv &c, int row, int head, int sub, int l8) {
+        const unsigned char *base = static_cast<const unsigned char *>(pool) + head * HD + l8 * VPL;
 #pragma unroll
-        for (int i = 0; i < STEP; ++i) {
-            const long long o = __shfl_sync(0xffffffffu, at, r0 + 4 * i + sub);
-            const unsigned char *row = static_cast<const unsigned char *>(base) + o;
-            if constexpr (Q) {
-#pragma unroll
-                for (int s = 0; s < C::SLABS; ++s) raw[i][s] = make_uint2(0, 0);
-                sc[i] = __floats2half2_rn(0.0f, 0.0f);
-                if (o >= 0) {
-                    const __half *d = reinterpret_cast<const __half *>(row + p.a.c.W) + head * (HD / 32) + (l8 >> 2);
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s) raw[i][s] = __ldg(reinterpret_cast<const uint2 *>(row) + head * (HD / 8) + s * 8 + l8);
-                    sc[i] = __halves2half2(d[0], C::SLABS == 2 ? d[2] : d[0]);
-                }
+        for (int i = 0; i < STEPS; ++i) {
+            const int r = max(__shfl_sync(0xffffffffu, row, 4 * i + sub), 0);
+            const unsigned char *q = base + r * c.row_bytes;
+            if constexpr (CH == 2) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(q));
+                raw[i][0] = make_uint2(x.x, x.y);
+                raw[i][1] = make_uint2(x.z, x.w);
             } else {
-#pragma unroll
-                for (int s = 0; s < C::SLABS; ++s) {
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                    if (o >= 0) {
-                        const float4 *f = reinterpret_cast<const float4 *>(row) + head * (HD / 4) + s * 16 + 2 * l8;
-                        a = __ldg(f);
-                        b = __ldg(f + 1);
-                    }
-                    x[i][s][0] = a.x, x[i][s][1] = a.y, x[i][s][2] = a.z, x[i][s][3] = a.w;
-                    x[i][s][4] = b.x, x[i][s][5] = b.y, x[i][s][6] = b.z, x[i][s][7] = b.w;
-                }
+                raw[i][0] = __ldg(reinterpret_cast<const uint2 *>(q));
             }
         }
     }
-    // The loaded rows, scaled, split and written (K: with their factors).
-    template <bool kV>
-    __device__ __forceinline__ void put(int n, int r0) {
-        const int st = n % C::NS;
+    // hi is the rounded product of a scaled scale and a quant, two binary16 values; the rest, at most 7 bits,
+    // comes exactly out of a fused multiply-add.
+    // d: this lane's row's scales, scaled.
+    __device__ __forceinline__ void put(uint32_t hi0, uint32_t lo0, uint2 d, int warp, int sub, int l8) {
 #pragma unroll
-        for (int i = 0; i < STEP; ++i) {
-            const int r = warp * 32 + r0 + 4 * i + sub;
-            float f;
-            if constexpr (kV) {
-                f = sm.v_inv[n & 3][r];
-            } else {
-                float am;
-                if constexpr (Q) {  // no value is above 127 scales; four lanes share a block
-                    const float2 d = __half22float2(sc[i]);
-                    am = 127.0f * fmaxf(fabsf(d.x), fabsf(d.y));
-                    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 4));
-                } else {
-                    am = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(x[i][s][e]));
-#pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-                }
-                const int sh = row_shift(am, 126);
-                f = pow2i(sh);
-                if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-sh);
+        for (int i = 0; i < STEPS; ++i) {
+            const int r = warp * kSplitRows + 4 * i + sub;
+            uint32_t dd = __shfl_sync(0xffffffffu, d.x, 4 * i + sub);
+            int b = l8 * VPL / 32;  // the lane's block of the row
+            if constexpr (HD == 128) {
+                const uint32_t dy = __shfl_sync(0xffffffffu, d.y, 4 * i + sub);
+                dd = b & 2 ? dy : dd;
             }
+            dd = __byte_perm(dd, dd, b & 1 ? 0x3232 : 0x1010);
+            const __half2 s = *reinterpret_cast<const __half2 *>(&dd);
 #pragma unroll
-            for (int s = 0; s < C::SLABS; ++s) {
+            for (int c = 0; c < CH; ++c) {
+                // lanes 4-7 (the second slab) take their chunks in the other order: no bank twice
+                const int cc = CH == 2 ? (c ^ (l8 >> 2)) : 0;
+                const uint2 q2 = CH == 2 ? (cc ? raw[i][CH - 1] : raw[i][0]) : raw[i][0];
+                const uint32_t u[2] = {q2.x ^ 0x80808080u, q2.y ^ 0x80808080u};
                 uint32_t hi[4], lo[4];
-                if constexpr (Q) {
-                    // scale * 2^sh is a binary16 value (2^sh is exact; what a far smaller block's scale loses
-                    // is below 2^-33 of the row's largest value), a quant another; hi is their rounded product,
-                    // and the rest, at most 7 bits, comes exactly out of a fused multiply-add
-                    const __half d = __float2half_rn((s == 0 ? __low2float(sc[i]) : __high2float(sc[i])) * f);
-                    const __half2 dd = __halves2half2(d, d);
-                    const uint32_t u[2] = {raw[i][s].x ^ 0x80808080u, raw[i][s].y ^ 0x80808080u};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t b = __byte_perm(u[e >> 1], 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
-                        const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&b), __floats2half2_rn(1152.0f, 1152.0f));
-                        const __half2 h = __hmul2_rn(q, dd), l = __hfma2(q, dd, __hneg2(h));
-                        hi[e] = *reinterpret_cast<const uint32_t *>(&h);
-                        lo[e] = *reinterpret_cast<const uint32_t *>(&l);
-                    }
-                } else {
-                    const float2 ff = make_float2(f, f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = mul2(make_float2(x[i][s][2 * e], x[i][s][2 * e + 1]), ff);
-                        split2(y.x, y.y, hi[e], lo[e]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = __byte_perm(u[e >> 1], 0x64646464u, (e & 1) ? 0x4342 : 0x4140);
+                    const __half2 q = __hsub2(*reinterpret_cast<const __half2 *>(&w), __floats2half2_rn(1152.0f, 1152.0f));
+                    const __half2 h = __hmul2_rn(q, s), l = __hfma2(q, s, __hneg2(h));
+                    hi[e] = *reinterpret_cast<const uint32_t *>(&h);
+                    lo[e] = *reinterpret_cast<const uint32_t *>(&l);
                 }
-                unsigned char *h = kV ? sm.v[st][0][s] : sm.k[st][0][s], *l = kV ? sm.v[st][C::TERMS - 1][s] : sm.k[st][C::TERMS - 1][s];
-                *reinterpret_cast<uint4 *>(h + sw16(r, l8)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(l + sw16(r, l8)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                const int chunk = l8 * CH + cc;  // of the row; eight a slab
+                const uint32_t at = (chunk >> 3) * (KT * 128) + sw16(r, chunk & 7);
+                st_shared(hi0 + at, hi);
+                st_shared(lo0 + at, lo);
             }
         }
     }
-    // V's row exponents of tile n.
-    __device__ __forceinline__ void exponents(int n, long long at, int head) {
-        const int r = warp * 32 + lane;
-        float am = 0.0f;
-        if constexpr (Q) {  // no value is above 127 scales
-            if (at >= 0) {
-                const __half *d = reinterpret_cast<const __half *>(static_cast<const unsigned char *>(p.a.c.v) + at + p.a.c.W) + head * (HD / 32);
+};
+
+// fp32 rows: eight values of each slab a lane, eight rows in flight.
+template <int HD>
+struct SplitF32 {
+    static constexpr int SLABS = HD / 64, STEP = 2;  // (two four-row steps)
+    float x[STEP][SLABS][8];
+
+    __device__ __forceinline__ void load(const void *base, const ChunkKv &c, int row, int head, int r0, int sub, int l8) {
 #pragma unroll
-                for (int b = 0; b < HD / 32; ++b) am = fmaxf(am, 127.0f * fabsf(__half2float(d[b])));
+        for (int i = 0; i < STEP; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, r0 + 4 * i + sub);
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const unsigned char *>(base) + max(r, 0) * c.row_bytes) + head * (HD / 4) + 2 * l8;
+#pragma unroll
+            for (int s = 0; s < SLABS; ++s) {
+                float4 a = __ldg(q + s * 16), b = __ldg(q + s * 16 + 1);
+                if (r < 0) a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+                x[i][s][0] = a.x, x[i][s][1] = a.y, x[i][s][2] = a.z, x[i][s][3] = a.w;
+                x[i][s][4] = b.x, x[i][s][5] = b.y, x[i][s][6] = b.z, x[i][s][7] = b.w;
             }
+        }
+    }
+    __device__ __forceinline__ float amax(int i) const {  // of step i's row, in all of its lanes
+        float m = 0.0f;
+#pragma unroll
+        for (int s = 0; s < SLABS; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][s][e]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
+    __device__ __forceinline__ void put(uint32_t hi0, uint32_t lo0, int i, int r, int l8, float f) {
+        const float2 ff = make_float2(f, f);
+#pragma unroll
+        for (int s = 0; s < SLABS; ++s) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = mul2(make_float2(x[i][s][2 * e], x[i][s][2 * e + 1]), ff);
+                split2(y.x, y.y, hi[e], lo[e]);
+            }
+            const uint32_t at = s * (KT * 128) + sw16(r, l8);
+            st_shared(hi0 + at, hi);
+            st_shared(lo0 + at, lo);
+        }
+    }
+};
+
+// Warp 9: the rows of every tile of the stretch, up to four tiles ahead.
+template <int HD, typename T>
+__device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &p, long long total, int ctas) {
+    const int lane = threadIdx.x & 31;
+    const ChunkKv &c = p.a.c;
+    volatile int *abort_flag = &sm.abort_flag;
+    int n = 0;
+    Walk w;
+    bool more = walk_begin<KT>(w, p, total, ctas);
+    int u = more ? w.u0 : 0;
+    for (bool on = more; on; ++n) {
+        const int slot = n & 3;
+        if (n >= 4 && !__all_sync(0xffffffffu, mbar_wait(&sm.row_free[slot], ((n >> 2) - 1) & 1, abort_flag, p.a.err))) return;
+        on = more;
+        if (on) {
+            const int j0 = unit_tile(w.keys, u) * KT + lane;
+            long long row[KT / 32];
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i) row[i] = item_sees(w.keys, j0 + 32 * i) ? seq_row(c, w.rows, j0 + 32 * i) : -2;
+#pragma unroll
+            for (int i = 0; i < KT / 32; ++i) {
+                if (row[i] == -1) flag_error(p.a.err, MINF_ERRBIT_BLOCK);
+                sm.rows[slot][32 * i + lane] = row[i] < 0 ? -1 : static_cast<int>(row[i]);
+            }
+            if (lane == 0) sm.row_head[slot] = w.head;
+            if (++u == w.u1) {
+                more = walk_next<KT>(w, p);
+                u = w.u0;
+            }
+        } else if (lane == 0) {
+            sm.row_head[slot] = -1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.row_full[slot]);
+    }
+}
+
+template <int HD, typename T, bool kV>
+__device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p, int warp) {
+    using C = Cfg<HD, T>;
+    constexpr bool Q = std::is_same<T, Q8>::value;
+    constexpr int kMostShift = kV ? 60 : 126;
+    const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
+    const int my_row = warp * kSplitRows + lane;
+    const ChunkKv &c = p.a.c;
+    const void *pool = kV ? c.v : c.k;
+    volatile int *abort_flag = &sm.abort_flag;
+    std::conditional_t<Q, SplitQ8<HD>, SplitF32<HD>> sp;
+    uint2 scales = make_uint2(0, 0);
+    int row = -1, head = -1;  // the rows taken last
+    // The rows of tile n; false once a wait has run out.
+    auto take_rows = [&](int n) -> bool {
+        const int slot = n & 3;
+        const bool ok = mbar_wait(&sm.row_full[slot], (n >> 2) & 1, abort_flag, p.a.err);
+        head = ok ? sm.row_head[slot] : -1;
+        row = head < 0 ? -1 : sm.rows[slot][my_row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.row_free[slot]);
+        if constexpr (Q) {
+            scales = sp.load_scales(pool, c, row, max(head, 0));
+        } else if (row >= 0) {
+            const unsigned char *q = static_cast<const unsigned char *>(pool) + row * c.row_bytes + head * (HD * 4);
+#pragma unroll
+            for (int b = 0; b < HD * 4; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + b));
+        }
+        return ok;
+    };
+    // This lane's row's shift in the tile whose rows were taken last, agreed on by the four warps: the tile's
+    // where its rows are within 2^16 of its largest, else the row's own.  False, in all four, once a wait
+    // has run out in one of them: they leave together.
+    auto agree = [&](int slot, bool ok, int &sh, int &by_row) -> bool {
+        float am = 0.0f;
+        if constexpr (Q) {
+            am = sp.most(scales);
         } else {
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 4 * STEP) {
-                load(p.a.c.v, at, head, r0);
+            for (int r0 = 0; r0 < kSplitRows; r0 += 8) {
+                sp.load(pool, c, row, max(head, 0), r0, sub, l8);
 #pragma unroll
-                for (int i = 0; i < STEP; ++i) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][s][e]));
-#pragma unroll
-                    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    // to the lane of this row
-                    const float y = __shfl_sync(0xffffffffu, m, (lane & 3) * 8);
+                for (int i = 0; i < 2; ++i) {
+                    const float y = __shfl_sync(0xffffffffu, sp.amax(i), (lane & 3) * 8);  // to the row's lane
                     if ((lane >> 2) == (r0 >> 2) + i) am = y;
                 }
             }
         }
-        const int sh = row_shift(am, 60);
-        sm.v_exp[n & 3][r] = static_cast<float>(-sh);
-        sm.v_inv[n & 3][r] = pow2i(sh);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_stat[n & 3]);
-    }
-};
-
-template <int HD, typename T>
-__device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p, int warp, long long total, int ctas) {
-    using S = Splitter<HD, T>;
-    using C = Cfg<HD, T>;
-    S sp(sm, p, warp);
-    const int lane = sp.lane;
-    volatile int *abort_flag = &sm.abort_flag;
-    Walk w;  // of the tile ahead
-    bool more = walk_begin<KT>(w, p, total, ctas);
-    if (!more) return;
-    int u = w.u0, ahead = 0, nxt_head = 0;
-    long long nxt = -1;  // this lane's row of the tile ahead, as a byte offset (negative: hidden or missing)
-    auto look_ahead = [&]() {
-        nxt = -1;
-        nxt_head = w.head;
-        const int j = unit_tile(w.keys, u) * KT + warp * 32 + lane;
-        if (item_sees(w.keys, j)) {
-            const long long row = seq_row(p.a.c, w.rows, j);
-            if (row >= 0)
-                nxt = row * p.a.c.row_bytes;
-            else
-                flag_error(p.a.err, MINF_ERRBIT_BLOCK);
-        }
-        constexpr int kBytes = HD * (S::Q ? 1 : 4);
-        if (nxt >= 0) {
-            const unsigned char *k = static_cast<const unsigned char *>(p.a.c.k) + nxt + w.head * kBytes;
-            const unsigned char *v = static_cast<const unsigned char *>(p.a.c.v) + nxt + w.head * kBytes;
+        sh = row_shift(am, kMostShift);
+        const int none = 1 << 20;  // rows of zeros go by whatever the others do
+        const int2 mine = make_int2(__reduce_min_sync(0xffffffffu, am > 0.0f ? sh : none), __reduce_max_sync(0xffffffffu, am > 0.0f ? sh : -none));
+        if (lane == 0) sm.shifts[kV][slot][warp] = mine;
+        if (!named_all(kV ? 3 : 2, kSplitWarps * 32, ok)) return false;
+        int2 all = sm.shifts[kV][slot][0];
 #pragma unroll
-            for (int b = 0; b < kBytes; b += 128) {
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(k + b));
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + b));
+        for (int k = 1; k < kSplitWarps; ++k) {
+            const int2 o = sm.shifts[kV][slot][k];
+            all = make_int2(min(all.x, o.x), max(all.y, o.y));
+        }
+        by_row = all.y - all.x > 16;  // (no row at all: not row by row)
+        if (!by_row) sh = all.x == none ? 0 : all.x;
+        return true;
+    };
+    auto scaled = [&](int sh) {
+        return make_uint2(SplitQ8<HD>::times(scales.x, pow2i(sh)), SplitQ8<HD>::times(scales.y, pow2i(sh)));
+    };
+    bool ok = take_rows(0);
+    if constexpr (Q) sp.load(pool, c, row, max(head, 0), sub, l8);
+    uint2 d = make_uint2(0, 0), d_next = d;  // Q8_0: the scaled scales
+    int sh = 0, by_row = 0;
+    // V: exponents of tile n out.
+    auto publish = [&](int n) {
+        const int slot = n & 3;
+        if (by_row) sm.v_exp[slot][my_row] = static_cast<float>(-sh);
+        if (by_row || !Q) sm.v_inv[slot][my_row] = pow2i(sh);
+        if (warp == 0 && lane == 0) sm.v_tile[slot] = {by_row ? 0.0f : static_cast<float>(-sh), by_row ? 1.0f : pow2i(sh), by_row};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_stat[slot]);
+    };
+    if constexpr (kV) {
+        if (!agree(0, ok, sh, by_row)) return;
+        publish(0);
+        if constexpr (Q) d = scaled(sh);
+    }
+    for (int n = 0;; ++n) {
+        if constexpr (!kV && Q) {
+            if (!agree(n & 3, ok, sh, by_row)) return;
+            d = scaled(sh);
+        } else if constexpr (!kV) {
+            if (!named_all(2, kSplitWarps * 32, ok)) return;
+        }
+        if (head < 0) return;
+        const int st = n % C::NS, cur = row, cur_head = head, phase = ((n / C::NS) - 1) & 1;
+        const uint32_t hi = su32(kV ? sm.v[st][0][0] : sm.k[st][0][0]), lo = hi + C::SLABS * KT * 128;
+        ok = take_rows(n + 1);
+        if constexpr (kV) {
+            int sh1 = 0, by1 = 0;
+            if (!agree((n + 1) & 3, ok, sh1, by1)) return;
+            if (head >= 0) {
+                sh = sh1, by_row = by1;
+                publish(n + 1);
+                if constexpr (Q) d_next = scaled(sh);
             }
         }
-        ++ahead;
-        if (++u == w.u1) {
-            more = walk_next<KT>(w, p);
-            u = w.u0;
-        }
-    };
-    look_ahead();
-    sp.exponents(0, nxt, nxt_head);
-    if constexpr (S::Q) sp.load(p.a.c.k, nxt, nxt_head, 0);
-    for (int n = 0; n < ahead; ++n) {
-        const int st = n % C::NS, head = nxt_head, phase = ((n / C::NS) - 1) & 1;
-        const long long cur = nxt;
-        if (more) look_ahead();
-        const bool next = ahead > n + 1;
-        // K of tile n
-        auto wait_empty = [&](unsigned long long *bar) -> bool {
-            return n < C::NS || __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, p.a.err));
+        auto wait_empty = [&]() {  // (one that runs out shows in the next take_rows)
+            if (n >= C::NS) mbar_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], phase, abort_flag, p.a.err);
+            __syncwarp();
         };
-        if constexpr (S::Q) {
-            if (!wait_empty(&sm.k_empty[st])) return;
-            sp.template put<false>(n, 0);
+        if constexpr (Q) {
+            wait_empty();
+            if constexpr (!kV) {
+                if (by_row) sm.k_fac[n & 3][my_row] = pow2i(-sh);
+                if (warp == 0 && lane == 0) sm.k_tile[n & 3] = {0.0f, by_row ? 1.0f : pow2i(-sh), by_row};
+            }
+            sp.put(hi, lo, d, warp, sub, l8);
         } else {
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 4 * S::STEP) {
-                sp.load(p.a.c.k, cur, head, r0);
-                if (r0 == 0 && !wait_empty(&sm.k_empty[st])) return;
-                sp.template put<false>(n, r0);
+            for (int r0 = 0; r0 < kSplitRows; r0 += 8) {
+                sp.load(pool, c, cur, cur_head, r0, sub, l8);
+                if (r0 == 0) {
+                    wait_empty();
+                    if (!kV && warp == 0 && lane == 0) sm.k_tile[n & 3] = {0.0f, 1.0f, 1};
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = warp * kSplitRows + r0 + 4 * i + sub;
+                    float f;
+                    if constexpr (kV) {
+                        f = sm.v_inv[n & 3][r];
+                    } else {
+                        const int s = row_shift(sp.amax(i), kMostShift);
+                        if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-s);
+                        f = pow2i(s);
+                    }
+                    sp.put(hi, lo, i, r, l8, f);
+                }
             }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(&sm.k_stat[n & 3]);
-            mbar_arrive(&sm.k_full[st]);
+            if (!kV) mbar_arrive(&sm.k_stat[n & 3]);
+            mbar_arrive(kV ? &sm.v_full[st] : &sm.k_full[st]);
         }
-        if constexpr (S::Q) sp.load(p.a.c.v, cur, head, 0);
-        if (next) sp.exponents(n + 1, nxt, nxt_head);
-        // V of tile n
-        if constexpr (S::Q) {
-            if (!wait_empty(&sm.v_empty[st])) return;
-            sp.template put<true>(n, 0);
-        } else {
-#pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 4 * S::STEP) {
-                sp.load(p.a.c.v, cur, head, r0);
-                if (r0 == 0 && !wait_empty(&sm.v_empty[st])) return;
-                sp.template put<true>(n, r0);
-            }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_full[st]);
-        if constexpr (S::Q) {
-            if (next) sp.load(p.a.c.k, nxt, nxt_head, 0);
-        }
+        if constexpr (Q) sp.load(pool, c, row, max(head, 0), sub, l8);
+        d = d_next;
     }
 }
 
@@ -496,32 +600,35 @@ struct Desc {
 };
 
 template <int HD, typename T>
-__device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
+__device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, uint32_t tmem, int32_t *err) {
     using C = Cfg<HD, T>;
     using D = Desc<HD, T>;
     volatile int *abort_flag = &sm.abort_flag;
     constexpr uint32_t kId = idesc_f16(BM, KT, false);
     const uint64_t dk = desc128(su32(sm.k), 16);
     const uint32_t qh = tmem + kColQ, ql = qh + HD / 2;
-    int n = 0, seg = 0;
-    Walk w;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
-        if (!mbar_wait(&sm.q_full, seg & 1, abort_flag, p.a.err)) return;
-        const int tiles = w.u1 - w.u0;
+    for (int n = 0, seg = 0;; ++seg) {
+        if (!mbar_wait(&sm.q_full, seg & 1, abort_flag, err)) return;
+        const int tiles = *static_cast<volatile int *>(&sm.seg_tiles);
+        if (tiles == 0) return;
         for (int i = 0; i < tiles; ++i, ++n) {
             const int st = n % C::NS;
-            if (!mbar_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, p.a.err)) return;
+            if (!mbar_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, err)) return;
             // this buffer's last P: its product must be done (the item's first two tiles: with the last item)
-            if (i >= 2 && !mbar_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, p.a.err)) return;
+            if (i >= 2 && !mbar_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, err)) return;
             tc_after();
             const uint32_t d = tmem + kColS + static_cast<uint32_t>(n & 1) * KT;
             const uint64_t k0 = dk + st * D::kStage;
+            // (a slab at a time: all descriptors at once would go through local memory)
+#pragma unroll 1
+            for (int s = 0; s < C::SLABS; ++s) {
+                const uint64_t ks = k0 + s * (D::kSlab >> 4);
 #pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint64_t o = static_cast<uint64_t>(kk >> 2) * (D::kSlab >> 4) + 2 * (kk & 3);
-                mma_ts(d, qh + kk * 8, k0 + o, kId, kk > 0);
-                mma_ts(d, ql + kk * 8, k0 + o, kId, true);
-                if constexpr (C::HL) mma_ts(d, qh + kk * 8, k0 + D::kTerm + o, kId, true);
+                for (int kk = 0; kk < 4; ++kk) {
+                    mma_ts(d, qh + s * 32 + kk * 8, ks + 2 * kk, kId, s > 0 || kk > 0);
+                    mma_ts(d, ql + s * 32 + kk * 8, ks + 2 * kk, kId, true);
+                    if constexpr (C::HL) mma_ts(d, qh + s * 32 + kk * 8, ks + D::kTerm + 2 * kk, kId, true);
+                }
             }
             commit(&sm.s_full[n & 1]);
             commit(&sm.k_empty[st]);
@@ -530,33 +637,30 @@ __device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, const AttnParams &
 }
 
 template <int HD, typename T>
-__device__ __forceinline__ void issue_values(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
+__device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int32_t *err) {
     using C = Cfg<HD, T>;
     using D = Desc<HD, T>;
     volatile int *abort_flag = &sm.abort_flag;
     constexpr uint32_t kId = idesc_f16(BM, HD, true);
     const uint64_t dv = desc128(su32(sm.v), D::kSlab);
-    int n = 0;
-    Walk w;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
-        const int tiles = w.u1 - w.u0;
-        for (int i = 0; i < tiles; ++i, ++n) {
-            const int st = n % C::NS;
-            if (!mbar_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, p.a.err)) return;
-            if (!mbar_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, p.a.err)) return;
-            tc_after();
-            const uint64_t v0 = dv + st * D::kStage;
-            const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk) {
-                const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
-                mma_ts(tmem + kColO, ph + kk * 8, v0 + o, kId, i > 0 || kk > 0);
-                mma_ts(tmem + kColO, pl + kk * 8, v0 + o, kId, true);
-                if constexpr (C::HL) mma_ts(tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
-            }
-            commit(&sm.o_done[n & 1]);
-            commit(&sm.v_empty[st]);
+    for (int n = 0;; ++n) {
+        const int st = n % C::NS;
+        if (!mbar_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
+        const int flag = *static_cast<volatile int *>(&sm.p_flag[n & 1]);
+        if (!mbar_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
+        tc_after();
+        const uint64_t v0 = dv + st * D::kStage;
+        const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
+#pragma unroll 4
+        for (int kk = 0; kk < KT / 16; ++kk) {
+            const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
+            mma_ts(tmem + kColO, ph + kk * 8, v0 + o, kId, !(flag & 1) || kk > 0);
+            mma_ts(tmem + kColO, pl + kk * 8, v0 + o, kId, true);
+            if constexpr (C::HL) mma_ts(tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
         }
+        commit(&sm.o_done[n & 1]);
+        commit(&sm.v_empty[st]);
+        if (flag & 2) return;
     }
 }
 
@@ -614,6 +718,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             }
             tm_wait_st();
             tc_before();
+            if (tid == 0) sm.seg_tiles = tiles;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full);
         }
@@ -644,24 +749,39 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 uint32_t x[64];  // scores, as bits
                 tm_ld32(lanes + kColS + (q & 1) * KT + half * 64, x);
                 tm_ld32(lanes + kColS + (q & 1) * KT + half * 64 + 32, x + 32);
+                float cc = c, ve = 0.0f, vi = 1.0f;
+                bool k_rows = false, v_rows = false;
                 if constexpr (C::HL) {
                     mbar_wait(&sm.k_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     mbar_wait(&sm.v_stat[q & 3], (q >> 2) & 1, abort_flag, err);
+                    const auto fk = sm.k_tile[q & 3], fv = sm.v_tile[q & 3];
+                    k_rows = fk.by_row, v_rows = fv.by_row;
+                    cc = c * fk.fac;  // (1, 0 and 1 where they are row by row)
+                    ve = fv.exp;
+                    vi = fv.fac;
                 }
                 tm_wait_ld();
                 const bool mask = !(j0 >= all_lo && j0 + KT <= all_hi) && !(j0 + KT <= p.a.n_sink && j0 + KT <= all_hi);
-                const float2 cc = make_float2(c, c);
+                if (!C::HL || !(k_rows || v_rows)) {
+                    const float2 c2 = make_float2(cc, cc), e2 = make_float2(ve, ve);
 #pragma unroll
-                for (int e = 0; e < 64; e += 4) {
-                    float2 a = mul2(bits2(x[e], x[e + 1]), cc), b = mul2(bits2(x[e + 2], x[e + 3]), cc);
-                    if constexpr (C::HL) {
-                        const float4 kf = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][half * 64 + e]);
-                        const float4 ve = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][half * 64 + e]);
-                        a = fma2(a, lo2(kf), lo2(ve));
-                        b = fma2(b, hi2(kf), hi2(ve));
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 a = C::HL ? fma2(bits2(x[e], x[e + 1]), c2, e2) : mul2(bits2(x[e], x[e + 1]), c2);
+                        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
                     }
-                    x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
-                    x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        float4 kf = make_float4(cc, cc, cc, cc), vv = make_float4(ve, ve, ve, ve);
+                        if (k_rows) {
+                            const float4 f = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][half * 64 + e]);
+                            kf = make_float4(f.x * cc, f.y * cc, f.z * cc, f.w * cc);
+                        }
+                        if (v_rows) vv = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][half * 64 + e]);
+                        const float2 a = fma2(bits2(x[e], x[e + 1]), lo2(kf), lo2(vv)), b = fma2(bits2(x[e + 2], x[e + 3]), hi2(kf), hi2(vv));
+                        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
+                        x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
+                    }
                 }
                 if (mask) {
                     const int jb = j0 + half * 64, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
@@ -712,21 +832,24 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         float2 a = add2(bits2(x[e0 + e], x[e0 + e + 1]), nb), b = add2(bits2(x[e0 + e + 2], x[e0 + e + 3]), nb);
                         a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         b = make_float2(ex2_approx(b.x), ex2_approx(b.y));
-                        if constexpr (C::HL) {
-                            const float4 vi = *reinterpret_cast<const float4 *>(&sm.v_inv[q & 3][half * 64 + e0 + e]);
-                            s2 = fma2(a, lo2(vi), s2);
-                            s3 = fma2(b, hi2(vi), s3);
-                        } else {
-                            s2 = add2(s2, a);
-                            s3 = add2(s3, b);
-                        }
+                        s2 = add2(s2, a);
+                        s3 = add2(s3, b);
                         split2(a.x, a.y, ph[e >> 1], pl[e >> 1]);
                         split2(b.x, b.y, ph[(e >> 1) + 1], pl[(e >> 1) + 1]);
                     }
                     tm_st16(lanes + kColS + (q & 1) * KT + half * 32 + (e0 >> 1), ph);
                     tm_st16(lanes + kColS + (q & 1) * KT + 64 + half * 32 + (e0 >> 1), pl);
                 }
-                l = l * corr + ((s2.x + s2.y) + (s3.x + s3.y));
+                float sum = (s2.x + s2.y) + (s3.x + s3.y);
+                if constexpr (C::HL) {
+                    sum *= vi;
+                    if (v_rows) {  // each key's own 2^-e
+                        sum = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) sum = fmaf(ex2_approx(__uint_as_float(x[e]) - base), sm.v_inv[q & 3][half * 64 + e], sum);
+                    }
+                }
+                l = l * corr + sum;
                 tm_wait_st();
             }
             if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
@@ -742,6 +865,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 fence_async_smem();
             }
             tc_before();
+            if (tid == 0) sm.p_flag[q & 1] = (i == 0 ? 1 : 0) | (i + 1 == tiles && tiles == w.left ? 2 : 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
         }
@@ -830,7 +954,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     float y[JD];
 #pragma unroll
                     for (int d = 0; d < JD; ++d) y[d] = 0.0f;
-#pragma unroll(C::HL ? 2 : 3)
+#pragma unroll(C::HL ? 1 : 3)
                     for (int b = b0; b <= b1; ++b) {
                         const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                         const float mb = __ldcg(q + BM * HD + row), lb = __ldcg(q + BM * (HD + 1) + row);
@@ -879,6 +1003,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         tc_before();
         named_sync(1, kRowThreads);  // sm.odd and sm.sum are free for the next segment
     }
+    if (tid == 0) sm.seg_tiles = 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full);
 }
 
 template <int HD, typename T>
@@ -899,14 +1026,16 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             mbar_init(&sm.s_full[i], 1);
         }
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&sm.k_full[i], C::HL ? 4 : 1);
-            mbar_init(&sm.v_full[i], C::HL ? 4 : 1);
+            mbar_init(&sm.k_full[i], C::HL ? kSplitWarps : 1);
+            mbar_init(&sm.v_full[i], C::HL ? kSplitWarps : 1);
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_empty[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm.k_stat[i], 4);
-            mbar_init(&sm.v_stat[i], 4);
+            mbar_init(&sm.k_stat[i], kSplitWarps);
+            mbar_init(&sm.v_stat[i], kSplitWarps);
+            mbar_init(&sm.row_full[i], 1);
+            mbar_init(&sm.row_free[i], 2 * kSplitWarps);
         }
         sm.abort_flag = 0;
         mbar_init_fence();
@@ -928,27 +1057,36 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     gdc_wait();  // the plan, and everything before it
     const long long total = p.head->total;
     const int ctas = p.head->ctas;
+    const bool idle = static_cast<int>(blockIdx.x) >= ctas;  // no stretch
     if (warp < kRowThreads / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRowRegs));
-        do_rows<HD, T>(sm, p, tmem, total, ctas);
+        if (!idle) do_rows<HD, T>(sm, p, tmem, total, ctas);
     } else if (!C::HL || warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
         if (warp == kScoreWarp) {
-            if (lane == 0) issue_scores<HD, T>(sm, p, tmem, total, ctas);
+            if (lane == 0 && !idle) issue_scores<HD, T>(sm, tmem, p.a.err);
             __syncwarp();
         } else if (warp == kValueWarp) {
-            if (lane == 0) issue_values<HD, T>(sm, p, tmem, total, ctas);
+            if (lane == 0 && !idle) issue_values<HD, T>(sm, tmem, p.a.err);
             __syncwarp();
         } else if constexpr (C::HL) {
-            if (warp == kQueryWarp) copy_q<HD, T>(sm, p, total, ctas);
+            if (warp == kQueryWarp)
+                copy_q<HD, T>(sm, p, total, ctas);
+            else
+                resolve_rows<HD, T>(sm, p, total, ctas);
         } else if (warp == kKeyWarp) {
             copy_tiles<HD, T, false>(sm, tm_k, p, total, ctas);
         } else {
             copy_tiles<HD, T, true>(sm, tm_v, p, total, ctas);
         }
     } else if constexpr (C::HL) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSplitRegs));
-        split_tiles<HD, T>(sm, p, warp - 12, total, ctas);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSplitRegs));
+        if (idle) {
+        } else if (warp < 16) {
+            split_tiles<HD, T, false>(sm, p, warp - 12);
+        } else {
+            split_tiles<HD, T, true>(sm, p, warp - 16);
+        }
     }
     tc_before();
     __syncthreads();
