@@ -86,6 +86,11 @@ struct Smem {
     alignas(16) float out[BM][36];                     // 32 dims of the output rows on their way out
     float mx[2][2][BM], sum[2][BM];
     int odd[BM];                                       // rows whose result is not finite
+    int token[BM];                                     // of each row (a division otherwise)
+    // the row threads' walk (here, not in every thread's registers): segment n in walk[n % 2]
+    Walk walk[2];
+    int more[2];
+    int2 all;                                          // keys that every row of the item sees
     // hi + lo kinds, tile n in slot n % 4: K row factors, V row exponents and 2^-e; the smallest and the
     // largest shifts of each splitting warp's rows (K, V); what the row threads go by
     alignas(16) float k_fac[C::HL ? 4 : 1][KT];
@@ -321,9 +326,16 @@ struct SplitQ8 {
     // comes exactly out of a fused multiply-add.
     // d: this lane's row's scales, scaled.
     __device__ __forceinline__ void put(uint32_t hi0, uint32_t lo0, uint2 d, int warp, int sub, int l8) {
+        // where the lane's chunks go in even and odd steps (four rows on, the swizzle differs in one bit)
+        uint32_t at[2][CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int chunk = l8 * CH + (CH == 2 ? (c ^ (l8 >> 2)) : 0);  // of the row; eight a slab
+            at[0][c] = hi0 + (chunk >> 3) * (KT * 128) + sw16(warp * kSplitRows + sub, chunk & 7);
+            at[1][c] = at[0][c] ^ 64u;
+        }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            const int r = warp * kSplitRows + 4 * i + sub;
             uint32_t dd = __shfl_sync(0xffffffffu, d.x, 4 * i + sub);
             int b = l8 * VPL / 32;  // the lane's block of the row
             if constexpr (HD == 128) {
@@ -347,11 +359,10 @@ struct SplitQ8 {
                     hi[e] = *reinterpret_cast<const uint32_t *>(&h);
                     lo[e] = *reinterpret_cast<const uint32_t *>(&l);
                 }
-                const int chunk = l8 * CH + cc;  // of the row; eight a slab
-                const uint32_t at = (chunk >> 3) * (KT * 128) + sw16(r, chunk & 7);
-                st_shared(hi0 + at, hi);
-                st_shared(lo0 + at, lo);
+                st_shared(at[i & 1][c] + i * 512, hi);
+                st_shared(at[i & 1][c] + i * 512 + (lo0 - hi0), lo);
             }
+            asm volatile("" ::: "memory");  // a step at a time: more in flight would go through local memory
         }
     }
 };
@@ -675,16 +686,12 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
     const int g = p.a.nh / p.a.nk;
     volatile int *abort_flag = &sm.abort_flag;
     int32_t *err = p.a.err;
-    // where this thread's four rows of an output pass lie in an item (32 bits: an item spans 128 / g tokens)
-    int out_at[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int r = k * 32 + (tid >> 3), q = tid & 7;
-        out_at[k] = ((r / g) * p.a.nh + r % g) * HD + (q >> 2) * HALF + (q & 3) * 4;
-    }
-    int n = 0, seg = 0;
-    Walk w;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
+    if (half == 0) sm.token[row] = row / g;
+    if (tid == 0) sm.more[0] = walk_begin<KT>(sm.walk[0], p, total, ctas);
+    named_sync(1, kRowThreads);
+    int n = 0;
+    for (int seg = 0; sm.more[seg & 1]; ++seg) {
+        const Walk &w = sm.walk[seg & 1];
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
         // this half row of Q, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
         float c;
@@ -723,21 +730,18 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             if (lane == 0) mbar_arrive(&sm.q_full);
         }
         const bool warp_live = (row & ~31) < rows, live = row < rows;
-        // this row's window: keys [r_lo, r_hi) and [0, r_sink)
-        const long long pos = walk_pos(w, p) + row / g;
-        int r_hi = 0, r_lo = 0, r_sink = 0;
-        if (live && pos >= 0) {
-            r_hi = pos + 1 < w.rows.cap ? static_cast<int>(pos + 1) : w.rows.cap;
-            if (p.a.window) {
-                const long long lo = pos - p.a.window + 1;
-                r_lo = lo <= 0 ? 0 : (lo < r_hi ? static_cast<int>(lo) : r_hi);
-                r_sink = min(p.a.n_sink, r_hi);
-            }
+        if (tid == 0) {
+            // keys in [x, y) are seen by every row: their tiles need no mask
+            const long long first = walk_pos(w, p), last = first + w.cnt - 1;
+            const long long lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
+            const long long hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
+            sm.all = make_int2(lo < 0x7fffffff ? static_cast<int>(lo) : 0x7fffffff, hi > 0 ? static_cast<int>(hi) : 0);
+            // the next segment
+            Walk next = w;
+            sm.more[(seg + 1) & 1] = walk_next<KT>(next, p);
+            sm.walk[(seg + 1) & 1] = next;
         }
-        // tiles in [all_lo, all_hi) (rows) are seen whole by every row: no mask
-        const long long first = walk_pos(w, p), last = first + w.cnt - 1;
-        const long long all_hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
-        const long long all_lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
+        named_sync(1, kRowThreads);
         float m = -INFINITY, l = 0.0f;
         for (int i = 0; i < tiles; ++i) {
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
@@ -761,7 +765,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     vi = fv.fac;
                 }
                 tm_wait_ld();
-                const bool mask = !(j0 >= all_lo && j0 + KT <= all_hi) && !(j0 + KT <= p.a.n_sink && j0 + KT <= all_hi);
+                const int2 all = sm.all;
+                const bool mask = j0 + KT > all.y || (j0 < all.x && j0 + KT > p.a.n_sink);
                 if (!C::HL || !(k_rows || v_rows)) {
                     const float2 c2 = make_float2(cc, cc), e2 = make_float2(ve, ve);
 #pragma unroll
@@ -784,6 +789,17 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     }
                 }
                 if (mask) {
+                    // this row's window: keys [r_lo, r_hi) and [0, r_sink)
+                    const long long pos = walk_pos(w, p) + sm.token[row];
+                    int r_hi = 0, r_lo = 0, r_sink = 0;
+                    if (pos >= 0) {
+                        r_hi = pos + 1 < w.rows.cap ? static_cast<int>(pos + 1) : w.rows.cap;
+                        if (p.a.window) {
+                            const long long lo = pos - p.a.window + 1;
+                            r_lo = lo <= 0 ? 0 : (lo < r_hi ? static_cast<int>(lo) : r_hi);
+                            r_sink = min(p.a.n_sink, r_hi);
+                        }
+                    }
                     const int jb = j0 + half * 64, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
 #pragma unroll
                     for (int e = 0; e < 64; ++e) {
@@ -889,8 +905,11 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = k * 32 + (tid >> 3);  // eight lanes a row: four of each half
-                if (r < rows)
-                    *reinterpret_cast<float4 *>(item_out + out_at[k] + d) = *reinterpret_cast<const float4 *>(&sm.out[r][(tid & 7) * 4]);
+                if (r < rows) {
+                    const int t = sm.token[r];
+                    *reinterpret_cast<float4 *>(item_out + (t * p.a.nh + r - t * g) * HD + ((tid & 7) >> 2) * HALF + (tid & 3) * 4 + d) =
+                        *reinterpret_cast<const float4 *>(&sm.out[r][(tid & 7) * 4]);
+                }
             }
             named_sync(1, kRowThreads);
         };
