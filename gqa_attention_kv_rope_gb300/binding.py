@@ -177,8 +177,14 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+# The current stream's handle without a Stream object around it (which takes 3 us of a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -583,14 +589,23 @@ def minf_layer_attn_step_qkv(xn, h, gain, eps, w_qkv, b_qkv, pos, q, k, v, k_reg
 # pair_axis: the axis of each of the hd/2 pairs, as bytes or a sequence of ints (None: one axis).
 # These check sizes too (the library sees only pointers), and that every tensor is on the current
 # device, whose stream the call goes to.
+_F32, _I32 = torch.float32, torch.int32
 _CHUNK_DTYPE = {"": torch.float32, "_f16": torch.float16, "_q8": torch.uint8}
 
 
-def _on_current_device(*tensors):
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"every tensor must be on the current device (cuda:{here}), got one on {t.device}")
+def _ptr(t, dtype, name, here):
+    """Address of a contiguous tensor of this type on the current device (None stays None)."""
+    if t is None:
+        return None
+    if t.__class__ is not torch.Tensor and not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on the current device (cuda:{here}), it is on {t.device}")
+    return t.data_ptr()
 
 
 def _size(name, t, n):
@@ -622,9 +637,9 @@ def _chunk_pool(end, k_pool, v_pool, block_table, n_seq, row_width):
         if row_width % 32:
             raise ValueError("Q8_0 rows hold whole 32-value blocks")
         cols = row_width + ((row_width // 32) * 2 + 15) // 16 * 16
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] != k_pool.shape[0]:
-            raise ValueError(f"{name} must be [pool_rows, {cols}], the same rows for both, got {tuple(t.shape)}")
+    shape = k_pool.shape
+    if len(shape) != 2 or shape[1] != cols or v_pool.shape != shape:
+        raise ValueError(f"the pools (regions) must both be [rows, {cols}], got {tuple(shape)} and {tuple(v_pool.shape)}")
     if block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != n_seq):
         raise ValueError(f"block_table must be [{n_seq}, max_blocks], got {tuple(block_table.shape)}")
 
@@ -632,12 +647,12 @@ def _chunk_pool(end, k_pool, v_pool, block_table, n_seq, row_width):
 def minf_rope_axes(y, x, pos, pair_axis, n_head, hd, theta, freq_scale, style, err, stream=None):
     """pos: int32 [n_axis, nt] (or [nt] for one axis); y may be x."""
     n_axis, nt = pos.shape if pos.dim() == 2 else (1, pos.numel())
-    _on_current_device(y, x, pos, err)
+    here = torch.cuda.current_device()
     _size("x", x, nt * n_head * hd)
     _size("y", y, nt * n_head * hd)
-    _check(lib().minf_rope_axes(_dev(y, name="y"), _dev(x, name="x"), _dev(pos, torch.int32, "pos"), nt, n_axis,
+    _check(lib().minf_rope_axes(_ptr(y, _F32, "y", here), _ptr(x, _F32, "x", here), _ptr(pos, _I32, "pos", here), nt, n_axis,
                                 _axis_bytes(pair_axis, hd), n_head, hd, theta, freq_scale, style,
-                                _dev(err, torch.int32, "err"), _stream(stream)), "minf_rope_axes")
+                                _ptr(err, _I32, "err", here), _stream(stream)), "minf_rope_axes")
 
 
 def _rope_kv_append_chunk_paged(end, q_out, k_out, q, k, v, rope_pos, pair_axis, chunk_off, n_past, n_head, n_kv_head,
@@ -646,7 +661,7 @@ def _rope_kv_append_chunk_paged(end, q_out, k_out, q, k, v, rope_pos, pair_axis,
     dt, w = _CHUNK_DTYPE[end], n_kv_head * hd_kv
     nt = v.numel() // w
     n_axis = 1 if rope_pos is None or rope_pos.dim() == 1 else rope_pos.shape[0]
-    _on_current_device(q_out, k_out, q, k, v, rope_pos, chunk_off, n_past, k_pool, v_pool, block_table, err)
+    here = torch.cuda.current_device()
     n_seq = _chunk_seqs(chunk_off, n_past, nt)
     _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
     for name, t, n in (("q", q, n_head * hd), ("q_out", q_out, n_head * hd), ("k", k, w), ("k_out", k_out, w),
@@ -658,11 +673,11 @@ def _rope_kv_append_chunk_paged(end, q_out, k_out, q, k, v, rope_pos, pair_axis,
         axes = None
     name = "minf_rope_kv_append_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _dev(q_out, name="q_out"), _dev(k_out, name="k_out"), _dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"),
-        _dev(rope_pos, torch.int32, "rope_pos"), n_axis, axes, _dev(chunk_off, torch.int32, "chunk_off"),
-        _dev(n_past, torch.int32, "n_past"), nt, n_seq, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
-        _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"), k_pool.shape[0],
-        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows, _dev(err, torch.int32, "err"),
+        _ptr(q_out, _F32, "q_out", here), _ptr(k_out, _F32, "k_out", here), _ptr(q, _F32, "q", here), _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here),
+        _ptr(rope_pos, _I32, "rope_pos", here), n_axis, axes, _ptr(chunk_off, _I32, "chunk_off", here),
+        _ptr(n_past, _I32, "n_past", here), nt, n_seq, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
+        _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0],
+        _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows, _ptr(err, _I32, "err", here),
         _stream(stream)), name)
 
 
@@ -693,17 +708,17 @@ def minf_rope_kv_append_chunk_paged_q8(q_out, k_out, q, k, v, rope_pos, pair_axi
 def _kv_read_chunk_paged(end, k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err, stream):
     dt, w = _CHUNK_DTYPE[end], k_rows.shape[-1]
     nt = k_rows.numel() // w
-    _on_current_device(k_rows, v_rows, k_pool, v_pool, block_table, chunk_off, n_past, err)
+    here = torch.cuda.current_device()
     n_seq = _chunk_seqs(chunk_off, n_past, nt)
     _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
     _size("v_rows", v_rows, nt * w)
     rows = torch.float16 if k_rows.dtype == torch.float16 else torch.float32
     name = "minf_kv_read_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _dev(k_rows, rows, "k_rows"), _dev(v_rows, rows, "v_rows"), rows == torch.float16, _dev(k_pool, dt, "k_pool"),
-        _dev(v_pool, dt, "v_pool"), k_pool.shape[0], w, _dev(block_table, torch.int32, "block_table"),
-        block_table.shape[1], block_rows, _dev(chunk_off, torch.int32, "chunk_off"),
-        _dev(n_past, torch.int32, "n_past"), nt, n_seq, _dev(err, torch.int32, "err"), _stream(stream)), name)
+        _ptr(k_rows, rows, "k_rows", here), _ptr(v_rows, rows, "v_rows", here), rows == torch.float16, _ptr(k_pool, dt, "k_pool", here),
+        _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0], w, _ptr(block_table, _I32, "block_table", here),
+        block_table.shape[1], block_rows, _ptr(chunk_off, _I32, "chunk_off", here),
+        _ptr(n_past, _I32, "n_past", here), nt, n_seq, _ptr(err, _I32, "err", here), _stream(stream)), name)
 
 
 def minf_kv_read_chunk_paged(k_rows, v_rows, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, err,
@@ -739,16 +754,16 @@ def _gqa_attn_chunk_paged(end, out, q, k_pool, v_pool, block_table, block_rows, 
                           n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream):
     dt = _CHUNK_DTYPE[end]
     nt = _attn_rows(out, q, n_head, hd, hd_kv)
-    _on_current_device(out, q, k_pool, v_pool, block_table, chunk_off, n_past, ws, err)
+    here = torch.cuda.current_device()
     n_seq = _chunk_seqs(chunk_off, n_past, nt)
     _chunk_pool(end, k_pool, v_pool, block_table, n_seq, n_kv_head * hd_kv)
     name = "minf_gqa_attn_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _dev(out, name="out"), _dev(q, name="q"), _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"),
-        k_pool.shape[0], _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows,
-        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk, n_head,
-        n_kv_head, hd, hd_kv, scale, window, n_sink, _dev(ws, torch.uint8, "ws"), _nbytes(ws),
-        _dev(err, torch.int32, "err"), _stream(stream)), name)
+        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here),
+        k_pool.shape[0], _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows,
+        _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk, n_head,
+        n_kv_head, hd, hd_kv, scale, window, n_sink, _ptr(ws, _U8, "ws", here), _nbytes(ws),
+        _ptr(err, _I32, "err", here), _stream(stream)), name)
 
 
 def minf_gqa_attn_chunk_paged(out, q, k_pool, v_pool, block_table, block_rows, chunk_off, n_past, max_chunk, n_head,
@@ -773,7 +788,7 @@ def _gqa_attn_window(end, out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, c
                      n_kv_head, hd, hd_kv, scale, window, n_sink, ws, err, stream):
     dt = _CHUNK_DTYPE[end]
     nt = _attn_rows(out, q, n_head, hd, hd_kv)
-    _on_current_device(out, q, k_reg, v_reg, seq_row_off, seq_cap, chunk_off, n_past, ws, err)
+    here = torch.cuda.current_device()
     n_seq = _chunk_seqs(chunk_off, n_past, nt)
     _chunk_pool(end, k_reg, v_reg, None, n_seq, n_kv_head * hd_kv)
     for name, t in (("seq_row_off", seq_row_off), ("seq_cap", seq_cap)):
@@ -783,11 +798,11 @@ def _gqa_attn_window(end, out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, c
         raise ValueError(f"the regions have {k_reg.shape[0]} rows, max_cap is {max_cap}")
     name = "minf_gqa_attn_window" + end
     _check(getattr(lib(), name)(
-        _dev(out, name="out"), _dev(q, name="q"), _dev(k_reg, dt, "k_reg"), _dev(v_reg, dt, "v_reg"),
-        _dev(seq_row_off, torch.int64, "seq_row_off"), _dev(seq_cap, torch.int32, "seq_cap"), max_cap, k_reg.shape[0],
-        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk, n_head,
-        n_kv_head, hd, hd_kv, scale, window, n_sink, _dev(ws, torch.uint8, "ws"), _nbytes(ws),
-        _dev(err, torch.int32, "err"), _stream(stream)), name)
+        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_reg, dt, "k_reg", here), _ptr(v_reg, dt, "v_reg", here),
+        _ptr(seq_row_off, torch.int64, "seq_row_off", here), _ptr(seq_cap, _I32, "seq_cap", here), max_cap, k_reg.shape[0],
+        _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk, n_head,
+        n_kv_head, hd, hd_kv, scale, window, n_sink, _ptr(ws, _U8, "ws", here), _nbytes(ws),
+        _ptr(err, _I32, "err", here), _stream(stream)), name)
 
 
 def minf_gqa_attn_window(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, chunk_off, n_past, max_chunk, n_head,
@@ -815,7 +830,7 @@ def _layer_step_chunk_paged(end, xn, h, gain, eps, q, k, v, rope_pos, pair_axis,
     dt, w = _CHUNK_DTYPE[end], n_kv_head * hd_kv
     nt, n_embd = h.shape
     n_axis = 1 if rope_pos is None or rope_pos.dim() == 1 else rope_pos.shape[0]
-    _on_current_device(xn, h, gain, q, k, v, rope_pos, chunk_off, n_past, k_pool, v_pool, block_table, out, ws, err)
+    here = torch.cuda.current_device()
     n_seq = _chunk_seqs(chunk_off, n_past, nt)
     _chunk_pool(end, k_pool, v_pool, block_table, n_seq, w)
     for name, t, n in (("xn", xn, nt * n_embd), ("gain", gain, n_embd), ("q", q, nt * n_head * hd), ("k", k, nt * w),
@@ -827,13 +842,13 @@ def _layer_step_chunk_paged(end, xn, h, gain, eps, q, k, v, rope_pos, pair_axis,
         axes = None
     name = "minf_layer_attn_step_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd, _dev(q, name="q"),
-        _dev(k, name="k"), _dev(v, name="v"), _dev(rope_pos, torch.int32, "rope_pos"), n_axis, axes,
-        _dev(chunk_off, torch.int32, "chunk_off"), _dev(n_past, torch.int32, "n_past"), nt, n_seq, max_chunk,
-        _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"), k_pool.shape[0],
-        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], block_rows, n_head, n_kv_head, hd, hd_kv,
-        theta, freq_scale, style, window, n_sink, _dev(out, name="out"), _dev(ws, torch.uint8, "ws"), _nbytes(ws),
-        _dev(err, torch.int32, "err"), _stream(stream)), name)
+        _ptr(xn, _F32, "xn", here), _ptr(h, _F32, "h", here), _ptr(gain, _F32, "gain", here), eps, n_embd, _ptr(q, _F32, "q", here),
+        _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here), _ptr(rope_pos, _I32, "rope_pos", here), n_axis, axes,
+        _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk,
+        _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0],
+        _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows, n_head, n_kv_head, hd, hd_kv,
+        theta, freq_scale, style, window, n_sink, _ptr(out, _F32, "out", here), _ptr(ws, _U8, "ws", here), _nbytes(ws),
+        _ptr(err, _I32, "err", here), _stream(stream)), name)
 
 
 def minf_layer_attn_step_chunk_paged(xn, h, gain, eps, q, k, v, rope_pos, pair_axis, chunk_off, n_past, max_chunk,

@@ -7,18 +7,91 @@ namespace minf {
 namespace {
 
 constexpr int kPlanThreads = 512;
+constexpr int kHeld = 1024;     // sequences and token tiles whose sums are also held in shared memory
+constexpr int kFewTiles = 4;    // token tiles that a sequence's own thread adds up
 
+// A thread a sequence (its loads are the only ones that wait on memory), a warp for a sequence of many
+// token tiles; then a thread a stretch looks its start up in the sums.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     gdc_launch_dependents();  // the attention kernel sets itself up meanwhile
     __shared__ long long warp_sum[kPlanThreads / 32];
-    __shared__ long long s_total;
+    __shared__ long long held_seq[kHeld + 1], held_tile[kHeld];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int bad = 0;
-    for (int s = tid; a.sq.off && s <= a.sq.n_seq; s += kPlanThreads) {
-        const int o = __ldg(a.sq.off + s);
-        if (o < 0 || o > a.sq.nt || (s > 0 && o < __ldg(a.sq.off + s - 1))) bad = 1;
-    }
+    const size_t tiles_most = plan_tiles(a.sq.nt, a.sq.n_seq, a.tt);
+    long long *seq_units = a.sq.n_seq <= kHeld ? held_seq : a.seq_units;
+    long long *tile_units = tiles_most <= kHeld ? held_tile : a.tile_units;
     for (int b = tid; b < a.max_ctas; b += kPlanThreads) a.tickets[b] = 0;
+    long long before = 0;  // units of the sequences of earlier rounds
+    int bad = 0, reported = 0;
+    for (int s0 = 0; s0 < a.sq.n_seq; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int lo = s, n = 0, cap = 0, past = 0;
+        if (s < a.sq.n_seq) {
+            int hi = s + 1;
+            if (a.sq.off) {
+                lo = __ldg(a.sq.off + s);
+                hi = __ldg(a.sq.off + s + 1);
+            }
+            past = __ldg(a.sq.n_past + s);
+            cap = seq_rows(a.c, s).cap;
+            if (lo < 0 || hi < lo || hi > a.sq.nt) bad = 1;  // (nondecreasing within [0, nt])
+            lo = min(max(lo, 0), a.sq.nt);
+            hi = min(max(hi, lo), a.sq.nt);
+            n = hi - lo;
+        }
+        const int tiles = n < a.least || n > a.most ? 0 : (n + a.tt - 1) / a.tt;
+        if (tiles > 0 && (past < 0 || static_cast<long long>(past) + n > cap)) reported = 1;
+        auto units = [&](int t, int pst, int cnt, int cp) -> long long {
+            const long long p0 = static_cast<long long>(pst) + static_cast<long long>(t) * a.tt;
+            return item_keys(p0, p0 + min(a.tt, cnt - t * a.tt) - 1, cp, a.window, a.n_sink, a.kt).units;
+        };
+        long long total = 0;
+        if (tiles <= kFewTiles) {
+            for (int t = 0; t < tiles; ++t) {
+                total += units(t, past, n, cap);
+                tile_units[tile_base(lo, s, a.tt) + t] = total;
+            }
+        }
+        for (unsigned many = __ballot_sync(0xffffffffu, tiles > kFewTiles); many; many &= many - 1) {
+            const int l = __ffs(many) - 1;
+            const int t_n = __shfl_sync(0xffffffffu, tiles, l), t_lo = __shfl_sync(0xffffffffu, lo, l);
+            const int t_past = __shfl_sync(0xffffffffu, past, l), t_cnt = __shfl_sync(0xffffffffu, n, l), t_cap = __shfl_sync(0xffffffffu, cap, l);
+            const long long base = tile_base(t_lo, s0 + warp * 32 + l, a.tt);
+            long long run = 0;
+            for (int t0 = 0; t0 < t_n; t0 += 32) {
+                const int t = t0 + lane;
+                long long x = t < t_n ? units(t, t_past, t_cnt, t_cap) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (t < t_n) tile_units[base + t] = run + x;
+                run += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == l) total = run;
+        }
+        total *= a.nk;
+        // units before each sequence
+        long long inc = total;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        long long here = before + inc - total;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const long long y = warp_sum[w];
+            if (w < warp) here += y;
+            before += y;
+        }
+        if (s < a.sq.n_seq) seq_units[s] = here;
+        __syncthreads();  // warp_sum is free for the next round
+    }
+    if (reported) flag_error(a.err, MINF_ERRBIT_ATTN_POS);
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             flag_error(a.err, MINF_ERRBIT_CHUNK);
@@ -27,63 +100,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         }
         return;
     }
-    // a warp a sequence, a lane a token tile: running sums of the tiles' units
-    for (int s = warp; s < a.sq.n_seq; s += kPlanThreads / 32) {
-        int lo, hi;
-        chunk_rows(a.sq.off, a.sq.nt, s, lo, hi);
-        const long long past = __ldg(a.sq.n_past + s), base = tile_base(lo, s, a.tt);
-        const int cap = seq_rows(a.c, s).cap, n = hi - lo, tiles = n < a.least || n > a.most ? 0 : (n + a.tt - 1) / a.tt;
-        long long run = 0;
-        int reported = 0;
-        for (int t0 = 0; t0 < tiles; t0 += 32) {
-            const int t = t0 + lane;
-            int u = 0;
-            if (t < tiles) {
-                const long long p0 = past + static_cast<long long>(t) * a.tt;
-                const int cnt = min(a.tt, n - t * a.tt);
-                u = item_keys(p0, p0 + cnt - 1, cap, a.window, a.n_sink, a.kt).units;
-                if (p0 < 0 || p0 + cnt - 1 >= cap) reported = 1;
-            }
-            long long x = u;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
-            }
-            if (t < tiles) a.tile_units[base + t] = run + x;
-            run += __shfl_sync(0xffffffffu, x, 31);
-        }
-        if (reported) flag_error(a.err, MINF_ERRBIT_ATTN_POS);
-        if (lane == 0) a.seq_units[s] = run * a.nk;
-    }
-    __syncthreads();
-    // units before each sequence: a stretch of sequences a thread, then the threads' sums
-    const int per = (a.sq.n_seq + kPlanThreads - 1) / kPlanThreads;
-    const int s0 = min(tid * per, a.sq.n_seq), s1 = min(s0 + per, a.sq.n_seq);
-    long long sum = 0;
-    for (int s = s0; s < s1; ++s) sum += a.seq_units[s];
-    long long inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    long long before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    for (int s = s0; s < s1; ++s) {
-        const long long u = a.seq_units[s];
-        a.seq_units[s] = before;
-        before += u;
-    }
-    if (tid == kPlanThreads - 1) {  // (the last thread's running sum is the total)
-        a.seq_units[a.sq.n_seq] = before;
-        s_total = before;
-    }
-    __syncthreads();
-    const long long total = s_total;
-    long long want = (total + a.min_units - 1) / a.min_units;
+    const long long total = before;
+    const long long want = (total + a.min_units - 1) / a.min_units;
     const int ctas = static_cast<int>(want < a.max_ctas ? want : a.max_ctas);
     if (tid == 0) {
         a.head->total = total;
@@ -91,19 +109,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     for (int b = tid; b < ctas; b += kPlanThreads) {
         const long long x = stretch_start(total, ctas, b);
-        int l = 0, r = a.sq.n_seq;  // the last sequence that starts at or before x and has units
+        int l = 0, r = a.sq.n_seq;  // the last sequence that starts at or before x (it has units: x is below the total)
         while (r - l > 1) {
             const int mid = (l + r) >> 1;
-            if (a.seq_units[mid] <= x)
+            if (seq_units[mid] <= x)
                 l = mid;
             else
                 r = mid;
         }
         int lo, hi;
         chunk_rows(a.sq.off, a.sq.nt, l, lo, hi);
-        const long long *tu = a.tile_units + tile_base(lo, l, a.tt);
+        const long long *tu = tile_units + tile_base(lo, l, a.tt);
         const int tiles = (hi - lo + a.tt - 1) / a.tt;
-        const long long rest = x - a.seq_units[l];
+        const long long rest = x - seq_units[l];
         const long long per_head = tu[tiles - 1], in_head = rest % per_head;
         const int head = static_cast<int>(rest / per_head);
         int tl = -1, tr = tiles - 1;  // the first tile whose running sum passes in_head

@@ -81,7 +81,7 @@ struct PlanArgs {
 __device__ __forceinline__ long long tile_base(int chunk_lo, int s, int tt) {
     return static_cast<long long>(chunk_lo / tt) + s;
 }
-inline size_t plan_tiles(int nt, int n_seq, int tt) { return static_cast<size_t>(nt / tt) + n_seq + 1; }
+__host__ __device__ inline size_t plan_tiles(int nt, int n_seq, int tt) { return static_cast<size_t>(nt / tt) + n_seq + 1; }
 
 // Workspace offsets: the plan, then `parts` slots of `part_bytes`.
 struct PlanLayout {

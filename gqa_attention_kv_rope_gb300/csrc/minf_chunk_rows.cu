@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(kThreads) chunk_read_kernel(const ChunkReadArg
 int launch_chunk_store(const ChunkStoreArgs &a, float theta, float freq_scale, const unsigned char *pair_axis,
                        cudaStream_t s) {
     if (a.sq.nt == 0) return MINF_OK;
-    AxisTable tq, tk;
+    AxisTable tq, tk = {};
     axis_table(&tq, a.hd, theta, freq_scale, pair_axis);
-    axis_table(&tk, a.hd_kv, theta, freq_scale, pair_axis);
+    if (a.hd_kv != a.hd) axis_table(&tk, a.hd_kv, theta, freq_scale, pair_axis);  // (else k turns as q does)
     int tok;
     dim3 grid;
     row_grid(a.sq.nt, static_cast<long long>(a.nh) * (a.hd / 8) + a.nk * (a.hd_kv / 8) + a.c.W / 4, tok, grid);

@@ -3,8 +3,9 @@
 //
 // An item is up to 8*NT query rows (tokens x the g heads of one kv head).  One CTA an SM walks its
 // stretch of units (minf_chunk_plan.cuh), 64 keys a unit: a producer warp keeps a ring of K and V
-// tiles full with TMA copies of the rows as they are stored; eight warps compute, each on 16 keys of
-// every second tile with its own running maximum, sum and output, and are joined once an item.
+// tiles full with TMA copies of the rows as they are stored; groups of four warps compute, a group a
+// tile and a warp 16 of its keys, each with its own running maximum, sum and output; they are joined once
+// an item.
 //
 // The work per byte is small (8*NT rows), so what matters is that the products cost little and need
 // no barrier between warps: warp-level m16n8k16 products with the keys as the 16 rows and the
@@ -33,12 +34,7 @@ namespace minf {
 namespace {
 
 constexpr int KT = 64;              // keys of a tile
-constexpr int kWarps = 8;           // computing warps: two groups of four, a group a tile
-constexpr int kComputeThreads = kWarps * 32;
-// The third warp group holds the producer warp; registers move from it to the computing warps
-// (256 * 208 + 128 * 88 = 384 * 168, the launch's).
-constexpr int kThreads = kComputeThreads + 128;
-constexpr int kComputeRegs = 208, kOtherRegs = 88;
+constexpr int kMostWarps = 16;      // computing warps, four a tile
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^15
 
 template <int HD, typename T, int NT>
@@ -50,17 +46,25 @@ struct Cfg {
     static constexpr int kRow = HD * EB / SLABS;                     // bytes of a row in a slab
     static constexpr bool SW = kRow == 128;                          // 128-byte swizzle
     static constexpr int kTile = KT * HD * EB;                       // K or V of a stage
-    static constexpr int kScales = Q ? KT * 16 : 0;
-    static constexpr int kStage = 2 * (kTile + kScales);
+    static constexpr int kScale = HD / 32 * 2;                       // Q8_0: bytes of a row's scales
+    static constexpr int kScales = Q ? KT * kScale : 0;
+    static constexpr int kStage = (2 * (kTile + kScales) + 1023) / 1024 * 1024;
+    // Groups of four computing warps, a group a tile: four where a lane's registers allow it (the products of
+    // a tile are a chain of short steps, which more warps hide), else two.  The last warp group holds the
+    // producer warp; registers move from it to the computing warps (512 * 104 + 128 * 64 = 640 * 96 and
+    // 256 * 208 + 128 * 88 = 384 * 168, the launches').
+    static constexpr int G = NT == 1 && !F32 ? 4 : 2;
+    static constexpr int kWarps = 4 * G, kComputeThreads = 32 * kWarps, kThreads = kComputeThreads + 128;
+    static constexpr int kComputeRegs = G == 4 ? 104 : 208, kOtherRegs = G == 4 ? 64 : 88;
     static constexpr int TERMS = F32 ? 3 : 2;                        // of Q
     static constexpr int kQRow = HD * 2 + 16;                        // bytes of a Q row (spread over the banks)
     static constexpr int kQ = TERMS * R * kQRow;
     static constexpr int kRegs = NT * (HD / 16) * 4;                 // fp32 outputs a lane
-    static constexpr int kJoin = 4 * kRegs * 32 * 4;                 // four warps' outputs
+    static constexpr int kJoin = kWarps / 2 * kRegs * 32 * 4;        // half of the warps' outputs
     static constexpr int kRoom = 227 * 1024 - 1024 - kQ - kJoin - 6 * 1024;
-    // an even number of stages, so that a stage is always the same group's: its warps then wait on every
+    // a multiple of the groups, so that a stage is always the same group's: its warps then wait on every
     // phase of its barrier
-    static constexpr int NS = kRoom / kStage > 8 ? 8 : (kRoom / kStage) & ~1;
+    static constexpr int NS = kRoom / kStage > 8 ? 8 : kRoom / kStage / G * G;
     static constexpr int kOffQ = NS * kStage, kOffJoin = kOffQ + kQ, kOffMeta = kOffJoin + kJoin;
     static_assert(NS >= 2 && kStage % 1024 == 0 && kQ % 16 == 0, "ring");
 };
@@ -69,7 +73,7 @@ struct Meta {
     unsigned long long full[8], empty[8];
     float q_fac[32];
     int4 lim[32];                       // a row's window: hi, lo, sink
-    float m[kWarps][32], l[kWarps][32];
+    float m[kMostWarps][32], l[kMostWarps][32];
     int odd[32];
     int abort_flag, last;
 };
@@ -148,75 +152,114 @@ __device__ __forceinline__ uint32_t at16(int r, int c) {
 
 // ----------------------------------------------------------------------------- the producer
 struct Maps {
-    CUtensorMap k, v, ks, vs;  // ks, vs: Q8_0 scales
+    CUtensorMap k, v;
 };
 
+// A lane looks up two of a tile's rows (their block ids a tile ahead, so that no load is waited for), and
+// issues one of its TMA copies; Q8_0's scales come beside them, a few bytes a row, by cp.async (as TMA
+// boxes they would cost as many requests as the quants).
 template <int HD, typename T, int NT>
 __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const AttnParams &p,
                                         long long total, int ctas) {
     using C = Cfg<HD, T, NT>;
     const int lane = threadIdx.x & 31;
-    const int pieces = KT / p.box_rows;
-    constexpr int kPer = C::SLABS + (C::Q ? 1 : 0);  // copies of a piece of K (or V)
-    const int copies = 2 * kPer * pieces;            // at most 2 * 4 slabs * 4 pieces
-    const int is_v = lane / (kPer * pieces), rest = lane % (kPer * pieces), piece = rest / kPer, part = rest % kPer;
+    const ChunkKv &c = p.a.c;
+    const int pieces = KT / p.box_rows, copies = 2 * C::SLABS * pieces;  // at most 2 * 4 slabs * 4 pieces
+    const int is_v = lane / (C::SLABS * pieces), rest = lane % (C::SLABS * pieces), piece = rest / C::SLABS, part = rest % C::SLABS;
     volatile int *abort_flag = &mt.abort_flag;
-    Walk w;
-    int n = 0;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
-        for (int u = w.u0; u < w.u1; ++u, ++n) {
-            const int st = n % C::NS, j0 = unit_tile(w.keys, u) * KT, j = j0 + piece * p.box_rows;
-            long long row = p.a.c.rows;  // past the map's end: zeros
-            if (lane < copies) {
-                if (item_sees_some(w.keys, j, p.box_rows)) row = seq_row(p.a.c, w.rows, j);
-                if (row < 0) {
-                    if (!is_v) flag_error(p.a.err, MINF_ERRBIT_BLOCK);
-                    row = p.a.c.rows;
-                }
-            }
-            if (n >= C::NS && !__all_sync(0xffffffffu, mbar_wait(&mt.empty[st], ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
-            if (lane == 0) mbar_expect_tx(&mt.full[st], C::kStage);
-            __syncwarp();
-            if (lane < copies) {
-                unsigned char *stage = ring + st * C::kStage;
-                if (part < C::SLABS) {
-                    unsigned char *dst = stage + is_v * C::kTile + part * (KT * C::kRow) + piece * p.box_rows * C::kRow;
-                    tma_load_2d_stream(dst, is_v ? &maps.v : &maps.k, w.head * HD + part * (C::kRow / C::EB),
-                                       static_cast<int>(row), &mt.full[st]);
-                } else {  // 16 bytes of scales: this head's lie in them
-                    unsigned char *dst = stage + 2 * C::kTile + is_v * C::kScales + piece * p.box_rows * 16;
-                    tma_load_2d_stream(dst, is_v ? &maps.vs : &maps.ks, p.a.c.W + ((w.head * (HD / 32) * 2) & ~15),
-                                       static_cast<int>(row), &mt.full[st]);
-                }
-            }
-            __syncwarp();
+    Walk w;  // of the tile ahead
+    bool more = walk_begin<KT>(w, p, total, ctas);
+    int u = more ? w.u0 : 0;
+    int id[2], jj = 0, head = 0;  // the tile ahead: block ids (or the first row), -2: hidden
+    auto look_up = [&]() {
+        const int j0 = unit_tile(w.keys, u) * KT;
+        jj = j0 + lane;
+        head = w.head;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = j0 + lane + 32 * i;
+            // a row of a copy that some visible row lies in; rows past the capacity have no block
+            const int first = j / p.box_rows * p.box_rows;
+            id[i] = -2;
+            if (item_sees_some(w.keys, first, p.box_rows) && (j < w.rows.cap || !c.table))
+                id[i] = c.table ? __ldg(reinterpret_cast<const int32_t *>(w.rows.at) + (j >> c.block_shift)) : static_cast<int>(w.rows.at);
         }
+        if (++u == w.u1) {
+            more = walk_next<KT>(w, p);
+            u = w.u0;
+        }
+    };
+    if (!more) return;
+    look_up();
+    for (int n = 0, on = 1; on; ++n) {
+        const int st = n % C::NS, hd = head;
+        int row[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = jj + 32 * i;
+            row[i] = static_cast<int>(c.rows);  // past the map's end: zeros
+            if (id[i] == -2) continue;
+            if (!c.table)
+                row[i] = static_cast<int>(min(static_cast<long long>(id[i]) + j, c.rows));
+            else if (id[i] >= 0 && id[i] < c.pool_blocks)
+                row[i] = (id[i] << c.block_shift) + (j & ((1 << c.block_shift) - 1));
+            else
+                flag_error(p.a.err, MINF_ERRBIT_BLOCK);
+        }
+        on = more;
+        if (more) look_up();
+        const int key = piece * p.box_rows;
+        const int r0 = __shfl_sync(0xffffffffu, row[0], key & 31), r1 = __shfl_sync(0xffffffffu, row[1], key & 31);
+        if (n >= C::NS && !__all_sync(0xffffffffu, mbar_wait(&mt.empty[st], ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
+        if (lane == 0) mbar_expect_tx(&mt.full[st], 2 * C::kTile);
+        __syncwarp();
+        unsigned char *stage = ring + st * C::kStage;
+        if (lane < copies) {
+            unsigned char *dst = stage + is_v * C::kTile + part * (KT * C::kRow) + key * C::kRow;
+            tma_load_2d_stream(dst, is_v ? &maps.v : &maps.k, hd * HD + part * (C::kRow / C::EB), key < 32 ? r0 : r1, &mt.full[st]);
+        }
+        if constexpr (C::Q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = row[i & 1];
+                const bool there = r < c.rows;
+                const unsigned char *src = static_cast<const unsigned char *>(i < 2 ? c.k : c.v) +
+                                           (there ? r * c.row_bytes + c.W + hd * C::kScale : 0);
+                const uint32_t dst = su32(stage + 2 * C::kTile + (i < 2 ? 0 : C::kScales) + (lane + 32 * (i & 1)) * C::kScale);
+                // (a size of zero writes zeros)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(C::kScale),
+                             "r"(there ? C::kScale : 0)
+                             : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(su32(&mt.full[st])) : "memory");
+        }
+        __syncwarp();
     }
 }
 
 // ----------------------------------------------------------------------------- the computing warps
-// Sums the eight warps' outputs into warp 0's, always in the same order.
+// Sums the warps' outputs into warp 0's, always in the same order.
 template <typename C>
 __device__ __forceinline__ void join_warps(float (&acc)[C::kRegs], float *buf, int warp, int lane) {
 #pragma unroll
-    for (int step = 4; step > 0; step >>= 1) {
+    for (int step = C::kWarps / 2; step > 0; step >>= 1) {
         if (warp >= step && warp < 2 * step) {
 #pragma unroll
             for (int r = 0; r < C::kRegs; ++r) buf[((warp - step) * C::kRegs + r) * 32 + lane] = acc[r];
         }
-        named_sync(1, kComputeThreads);
+        named_sync(1, C::kComputeThreads);
         if (warp < step) {
 #pragma unroll
             for (int r = 0; r < C::kRegs; ++r) acc[r] += buf[(warp * C::kRegs + r) * 32 + lane];
         }
-        named_sync(1, kComputeThreads);
+        named_sync(1, C::kComputeThreads);
     }
 }
 
 template <int HD, typename T, int NT>
 __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const AttnParams &p, long long total, int ctas) {
     using C = Cfg<HD, T, NT>;
-    constexpr int R = C::R, MT = HD / 16, NB = HD / 32;
+    constexpr int R = C::R, MT = HD / 16, NB = HD / 32, kWarps = C::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n8 = lane >> 2, c4 = lane & 3;
     const int grp = warp >> 2, key0 = (warp & 3) * 16;
     const int g = p.a.nh / p.a.nk;
@@ -288,7 +331,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                 mt.odd[r] = 0;
             }
         }
-        named_sync(1, kComputeThreads);
+        named_sync(1, C::kComputeThreads);
         float c[NT][2], m[NT][2], l[NT][2];
         float acc[C::kRegs];  // [NT][MT][4]
 #pragma unroll
@@ -307,7 +350,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
         const long long all_lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
         for (int i = 0; i < tiles; ++i) {
             const int q = n + i;
-            if ((q & 1) != grp) continue;
+            if (q % C::G != grp) continue;
             const int st = q % C::NS, j0 = unit_tile(w.keys, w.u0 + i) * KT + key0;
             unsigned char *kst = smem + st * C::kStage, *vst = kst + C::kTile;
             mbar_wait(&mt.full[st], (q / C::NS) & 1, abort_flag, p.a.err);
@@ -334,8 +377,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
                 float ve[2] = {0.0f, 0.0f}, vw[2] = {1.0f, 1.0f}, vr[2][NB];  // Q8_0: V's exponents, 2^-e, relative scales
                 if constexpr (C::Q) {
-                    const int sub = (w.head * (HD / 32) * 2) & 15;  // of the 16 bytes of scales
-                    const unsigned char *ksc = kst + 2 * C::kTile + sub, *vsc = ksc + C::kScales;
+                    const unsigned char *ksc = kst + 2 * C::kTile, *vsc = ksc + C::kScales;
                     float kf[2][NB];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -343,9 +385,9 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                         float mx = 0.0f;
 #pragma unroll
                         for (int b = 0; b < NB; b += 2) {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(ksc + key * 16 + b * 2));
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(ksc + key * C::kScale + b * 2));
                             kf[h][b] = f.x, kf[h][b + 1] = f.y;
-                            float2 v = __half22float2(*reinterpret_cast<const __half2 *>(vsc + key * 16 + b * 2));
+                            float2 v = __half22float2(*reinterpret_cast<const __half2 *>(vsc + key * C::kScale + b * 2));
                             if (edge && !item_sees(w.keys, j0 + n8 + 8 * h)) v = make_float2(0.0f, 0.0f);
                             vr[h][b] = v.x, vr[h][b + 1] = v.y;
                             mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
@@ -577,7 +619,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     mt.l[warp][t * 8 + 2 * c4 + e] = l[t][e];
                 }
             }
-        named_sync(1, kComputeThreads);
+        named_sync(1, C::kComputeThreads);
         float M[NT][2], L[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -624,9 +666,9 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
             const int b0 = stretch_of(total, ctas, item0), b1 = stretch_of(total, ctas, item0 + w.keys.units - 1);
             __syncwarp();
             if (tid == 0) mt.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
-            named_sync(1, kComputeThreads);
+            named_sync(1, C::kComputeThreads);
             finish = mt.last != 0;
-            if (finish) {  // join the stretches' parts: every eighth one a warp, then the warps
+            if (finish) {  // join the stretches' parts, dealt out to the warps, then the warps
                 __threadfence();
                 auto part_of = [&](int b) { return p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart; };
 #pragma unroll
@@ -689,7 +731,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                         if (odd) mt.odd[r] = 1;
                     }
             }
-            named_sync(1, kComputeThreads);
+            named_sync(1, C::kComputeThreads);
             // rows that are not finite: by the definition, a row a warp
             for (int r = warp; r < rows; r += kWarps) {
                 if (!mt.odd[r]) continue;
@@ -703,12 +745,12 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                 attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
             }
         }
-        named_sync(1, kComputeThreads);  // Q, limits and the join buffer are free
+        named_sync(1, C::kComputeThreads);  // Q, limits and the join buffer are free
     }
 }
 
 template <int HD, typename T, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<HD, T, NT>::kThreads, 1)
     chunk_stream_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnParams p) {
     using C = Cfg<HD, T, NT>;
     extern __shared__ unsigned char smem_raw[];
@@ -717,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&mt.full[i], 1);
-            mbar_init(&mt.empty[i], 4);  // the warps of the group that takes the tile
+            mbar_init(&mt.full[i], C::Q ? 33 : 1);  // the copies' bytes, and each lane's scales
+            mbar_init(&mt.empty[i], 4);             // the warps of the group that takes the tile
         }
         mt.abort_flag = 0;
         mbar_init_fence();
@@ -729,12 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     gdc_wait();  // the plan, and everything before it
     const long long total = p.head->total;
     const int ctas = p.head->ctas;
-    if (warp < kWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kComputeRegs));
+    if (warp < C::kWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kComputeRegs));
         compute<HD, T, NT>(smem, mt, p, total, ctas);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kWarps) produce<HD, T, NT>(smem, mt, maps, p, total, ctas);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+        if (warp == C::kWarps) produce<HD, T, NT>(smem, mt, maps, p, total, ctas);
     }
     if (*static_cast<volatile int *>(&mt.abort_flag)) {
         // a wait ran out: let copies in flight land before shared memory goes away
@@ -755,18 +797,13 @@ int launch(const AttnParams &p, int grid, cudaStream_t s) {
     if (!make_tensor_map_2d(&maps.k, c.k, dt, C::EB, cols, rows, C::kRow / C::EB, p.box_rows, C::SW) ||
         !make_tensor_map_2d(&maps.v, c.v, dt, C::EB, cols, rows, C::kRow / C::EB, p.box_rows, C::SW))
         return MINF_ERR_CUDA;
-    maps.ks = maps.k;
-    maps.vs = maps.v;
-    if (C::Q && (!make_tensor_map_2d(&maps.ks, c.k, dt, 1, cols, rows, 16, p.box_rows, false) ||
-                 !make_tensor_map_2d(&maps.vs, c.v, dt, 1, cols, rows, 16, p.box_rows, false)))
-        return MINF_ERR_CUDA;
     constexpr int kSmem = C::kOffMeta + static_cast<int>(sizeof(Meta)) + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     auto kernel = chunk_stream_kernel<HD, T, NT>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return MINF_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -807,7 +844,7 @@ int launch_chunk_stream(const ChunkAttnArgs &a, void *workspace, int rows, int m
     p.most = most;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    // at least a tile for each group of warps in a stretch
+    // at least two tiles in a stretch: a stretch's own cost (its start, the join) is about one
     const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms, 2), s);
     if (st != MINF_OK) return st;
     if (a.hd_kv == 64)
