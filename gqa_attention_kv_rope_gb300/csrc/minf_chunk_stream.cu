@@ -2,7 +2,7 @@
 // tokens): a stream of the cached rows at memory speed.
 //
 // An item is up to 8*NT query rows (tokens x the g heads of one kv head).  One CTA an SM walks its
-// stretch of units (minf_chunk_plan.cuh), 64 keys a unit: a producer warp keeps a ring of K and V
+// stretch of units (minf_chunk_plan.cuh), 64 keys a unit: producer warps keep a ring of K and V
 // tiles full with TMA copies of the rows as they are stored; groups of four warps compute, a group a
 // tile and a warp 16 of its keys, each with its own running maximum, sum and output; they are joined once
 // an item.
@@ -34,7 +34,7 @@ namespace minf {
 namespace {
 
 constexpr int KT = 64;              // keys of a tile
-constexpr int kMostWarps = 16;      // computing warps, four a tile
+constexpr int kProducers = 4;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^15
 
 template <int HD, typename T, int NT>
@@ -49,13 +49,11 @@ struct Cfg {
     static constexpr int kScale = HD / 32 * 2;                       // Q8_0: bytes of a row's scales
     static constexpr int kScales = Q ? KT * kScale : 0;
     static constexpr int kStage = (2 * (kTile + kScales) + 1023) / 1024 * 1024;
-    // Groups of four computing warps, a group a tile: four where a lane's registers allow it (the products of
-    // a tile are a chain of short steps, which more warps hide), else two.  The last warp group holds the
-    // producer warp; registers move from it to the computing warps (512 * 104 + 128 * 64 = 640 * 96 and
-    // 256 * 208 + 128 * 88 = 384 * 168, the launches').
-    static constexpr int G = NT == 1 && !F32 ? 4 : 2;
+    // Groups of four computing warps, a group a tile.  The last warp group are the producers; registers move
+    // from it to the computing warps (256 * 208 + 128 * 88 = 384 * 168, the launch's).
+    static constexpr int G = 2;
     static constexpr int kWarps = 4 * G, kComputeThreads = 32 * kWarps, kThreads = kComputeThreads + 128;
-    static constexpr int kComputeRegs = G == 4 ? 104 : 208, kOtherRegs = G == 4 ? 64 : 88;
+    static constexpr int kComputeRegs = 208, kOtherRegs = 88;
     static constexpr int TERMS = F32 ? 3 : 2;                        // of Q
     static constexpr int kQRow = HD * 2 + 16;                        // bytes of a Q row (spread over the banks)
     static constexpr int kQ = TERMS * R * kQRow;
@@ -73,7 +71,7 @@ struct Meta {
     unsigned long long full[8], empty[8];
     float q_fac[32];
     int4 lim[32];                       // a row's window: hi, lo, sink
-    float m[kMostWarps][32], l[kMostWarps][32];
+    float m[8][32], l[8][32];
     int odd[32];
     int abort_flag, last;
 };
@@ -155,11 +153,13 @@ struct Maps {
     CUtensorMap k, v;
 };
 
-// A lane looks up two of a tile's rows (their block ids a tile ahead, so that no load is waited for), and
-// issues one of its TMA copies; Q8_0's scales come beside them, a few bytes a row, by cp.async (as TMA
-// boxes they would cost as many requests as the quants).
+// Producer warp `pw` of kProducers takes every kProducers-th tile (one warp's instructions for a tile take
+// longer than the tile's bytes).  A lane looks up two of the tile's rows (their block ids one of its
+// tiles ahead, so that no load is waited for), and issues one of its TMA copies; Q8_0's scales come
+// beside them, a few bytes a row, by cp.async (as TMA boxes they would cost as many requests as the
+// quants).
 template <int HD, typename T, int NT>
-__device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const AttnParams &p,
+__device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const AttnParams &p, int pw,
                                         long long total, int ctas) {
     using C = Cfg<HD, T, NT>;
     const int lane = threadIdx.x & 31;
@@ -170,28 +170,40 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
     Walk w;  // of the tile ahead
     bool more = walk_begin<KT>(w, p, total, ctas);
     int u = more ? w.u0 : 0;
-    int id[2], jj = 0, head = 0;  // the tile ahead: block ids (or the first row), -2: hidden
-    auto look_up = [&]() {
-        const int j0 = unit_tile(w.keys, u) * KT;
-        jj = j0 + lane;
-        head = w.head;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = j0 + lane + 32 * i;
-            // a row of a copy that some visible row lies in; rows past the capacity have no block
-            const int first = j / p.box_rows * p.box_rows;
-            id[i] = -2;
-            if (item_sees_some(w.keys, first, p.box_rows) && (j < w.rows.cap || !c.table))
-                id[i] = c.table ? __ldg(reinterpret_cast<const int32_t *>(w.rows.at) + (j >> c.block_shift)) : static_cast<int>(w.rows.at);
-        }
-        if (++u == w.u1) {
+    // `by` tiles on in the stretch
+    auto step = [&](int by) {
+        while (more && by > 0) {
+            const int left = w.u1 - u;
+            if (by < left) {
+                u += by;
+                return;
+            }
+            by -= left;
             more = walk_next<KT>(w, p);
             u = w.u0;
         }
     };
+    const int box_mask = -p.box_rows;  // (a power of two)
+    int id[2], jj = 0, head = 0;       // the tile ahead: block ids (or the first row), -2: hidden
+    auto look_up = [&]() {
+        const int j0 = unit_tile(w.keys, u) * KT;
+        jj = j0 + lane;
+        head = w.head;
+        // a row is copied where a visible one lies in its box; rows past the capacity have no block
+        const bool inside = j0 >= w.keys.lo && j0 + KT <= w.keys.hi;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = jj + 32 * i;
+            id[i] = -2;
+            if (inside || (item_sees_some(w.keys, j & box_mask, p.box_rows) && (j < w.rows.cap || !c.table)))
+                id[i] = c.table ? __ldg(reinterpret_cast<const int32_t *>(w.rows.at) + (j >> c.block_shift)) : static_cast<int>(w.rows.at);
+        }
+        step(kProducers);
+    };
+    step(pw);
     if (!more) return;
     look_up();
-    for (int n = 0, on = 1; on; ++n) {
+    for (int n = pw, on = 1; on; n += kProducers) {
         const int st = n % C::NS, hd = head;
         int row[2];
 #pragma unroll
@@ -677,7 +689,9 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     for (int e = 0; e < 2; ++e) {
                         const int r = t * 8 + 2 * c4 + e;
                         float mm = -INFINITY, ll = 0.0f;
+#pragma unroll 4
                         for (int b = b0; b <= b1; ++b) mm = fmaxf(mm, __ldcg(part_of(b) + R * HD + r));
+#pragma unroll 4
                         for (int b = b0; b <= b1; ++b) {
                             const float mb = __ldcg(part_of(b) + R * HD + r), lb = __ldcg(part_of(b) + R * HD + R + r);
                             if (mb != -INFINITY || lb != 0.0f) ll = fmaf(lb, ex2_approx(mb - mm), ll);
@@ -776,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<HD, T, NT>::kThreads, 1)
         compute<HD, T, NT>(smem, mt, p, total, ctas);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        if (warp == C::kWarps) produce<HD, T, NT>(smem, mt, maps, p, total, ctas);
+        produce<HD, T, NT>(smem, mt, maps, p, warp - C::kWarps, total, ctas);
     }
     if (*static_cast<volatile int *>(&mt.abort_flag)) {
         // a wait ran out: let copies in flight land before shared memory goes away
