@@ -6,7 +6,7 @@ namespace minf {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = kPlanMost;
 constexpr int kHeld = 1024;     // sequences and token tiles whose sums are also held in shared memory
 constexpr int kFewTiles = 4;    // token tiles that a sequence's own thread adds up
 
@@ -101,15 +101,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         return;
     }
     const long long total = before;
-    const long long want = (total + a.min_units - 1) / a.min_units;
-    const int ctas = static_cast<int>(want < a.max_ctas ? want : a.max_ctas);
-    if (tid == 0) {
-        a.head->total = total;
-        a.head->ctas = ctas;
+    const long long want = total / a.min_units;
+    const int ctas = static_cast<int>(want < 1 ? 1 : (want < a.max_ctas ? want : a.max_ctas));
+    if (total == 0) {  // nothing to do (no new token that this plan takes)
+        if (tid == 0) {
+            a.head->total = 0;
+            a.head->ctas = 0;
+        }
+        return;
     }
-    for (int b = tid; b < ctas; b += kPlanThreads) {
-        const long long x = stretch_start(total, ctas, b);
-        int l = 0, r = a.sq.n_seq;  // the last sequence that starts at or before x (it has units: x is below the total)
+    // a thread a stretch: its start, moved to an item's border that is near
+    __shared__ long long start[kPlanMost + 1];
+    __shared__ int first_lo[kPlanMost + 1], first_hi[kPlanMost + 1];
+    __shared__ int kept_warp[kPlanThreads / 32];
+    long long x = tid < ctas ? tid * total / ctas : total;
+    int l = 0, tile = 0, head = 0, tiles = 0;
+    long long in_tile = 0, item = 0;
+    const long long *tu = nullptr;
+    auto locate = [&]() {  // the item of unit x and its place there
+        int r = a.sq.n_seq;  // the last sequence that starts at or before x (it has units: x is below the total)
+        l = 0;
         while (r - l > 1) {
             const int mid = (l + r) >> 1;
             if (seq_units[mid] <= x)
@@ -119,11 +130,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         }
         int lo, hi;
         chunk_rows(a.sq.off, a.sq.nt, l, lo, hi);
-        const long long *tu = tile_units + tile_base(lo, l, a.tt);
-        const int tiles = (hi - lo + a.tt - 1) / a.tt;
-        const long long rest = x - seq_units[l];
-        const long long per_head = tu[tiles - 1], in_head = rest % per_head;
-        const int head = static_cast<int>(rest / per_head);
+        tu = tile_units + tile_base(lo, l, a.tt);
+        tiles = (hi - lo + a.tt - 1) / a.tt;
+        const long long rest = x - seq_units[l], per_head = tu[tiles - 1], in_head = rest % per_head;
+        head = static_cast<int>(rest / per_head);
         int tl = -1, tr = tiles - 1;  // the first tile whose running sum passes in_head
         while (tr - tl > 1) {
             const int mid = (tl + tr) >> 1;
@@ -132,13 +142,67 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
             else
                 tl = mid;
         }
+        tile = tr;
+        const long long tile0 = tr > 0 ? tu[tr - 1] : 0;
+        in_tile = in_head - tile0;
+        item = tu[tr] - tile0;
+    };
+    if (tid < ctas) {
+        locate();
+        if (in_tile <= a.snap) {
+            x -= in_tile;
+            in_tile = 0;
+        } else if (item - in_tile <= a.snap) {
+            x += item - in_tile;
+            if (x < total) locate();
+        }
+    }
+    // stretches that start where the one before them does are none
+    start[tid] = x;
+    __syncthreads();
+    const bool keep = tid < ctas && x < total && (tid == 0 || start[tid - 1] != x);
+    const unsigned kept = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) kept_warp[warp] = __popc(kept);
+    __syncthreads();
+    int at = __popc(kept & ((1u << lane) - 1)), n = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int y = kept_warp[w];
+        if (w < warp) at += y;
+        n += y;
+    }
+    if (keep) start[at] = x;
+    __syncthreads();
+    if (tid == 0) {
+        start[n] = total;
+        a.head->total = total;
+        a.head->ctas = n;
+    }
+    // the stretches of the item that this one starts inside of
+    int lo = at, hi = at;
+    if (keep && in_tile > 0) {
+        const long long item0 = x - in_tile, item1 = item0 + item;
+        while (start[lo] > item0) --lo;
+        while (hi + 1 < n && start[hi + 1] < item1) ++hi;
+    }
+    if (keep) {
+        first_lo[at] = lo;
+        first_hi[at] = hi;
+    }
+    __syncthreads();
+    if (keep) {
         PlanStart st;
         st.unit = x;
+        st.end = start[at + 1];
         st.seq = l;
         st.head = head;
-        st.tile = tr;
-        st.u = static_cast<int>(in_head - (tr > 0 ? tu[tr - 1] : 0));
-        a.starts[b] = st;
+        st.tile = tile;
+        st.u = static_cast<int>(in_tile);
+        st.first_lo = lo;
+        st.first_hi = hi;
+        st.last_hi = at + 1 < n ? first_hi[at + 1] : at;
+        st.pad = 0;
+        a.starts[at] = st;
     }
 }
 

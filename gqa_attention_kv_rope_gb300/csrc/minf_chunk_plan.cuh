@@ -4,7 +4,8 @@
 // kv head's query heads, and its units are the key tiles of `kt` rows that any of its tokens sees
 // (the sinks' tiles, then the window's).  All units in order (sequence, kv head, token tile, key
 // tile) are cut into equal stretches, one a CTA, so every CTA streams the same amount whatever the
-// lengths are.  An item that lies in one stretch is finished by its CTA; one that crosses
+// lengths are.  (A part of an item costs as much as several tiles to write and to join: a cut that would
+// fall within `snap` units of an item's border falls on it, and no stretch is shorter than min_units.)  An item that lies in one stretch is finished by its CTA; one that crosses
 // stretches is joined, in order, by the last of its CTAs to finish: two calls with the same
 // inputs add in the same order.
 //
@@ -50,10 +51,14 @@ __host__ __device__ __forceinline__ int unit_tile(const ItemKeys &k, int u) {
     return u < k.n_sink_tiles ? u : k.first_tile + (u - k.n_sink_tiles);
 }
 
-// Where a stretch starts: an item and a unit of it.
+// A stretch: where it starts (an item and a unit of it) and ends, and which stretches share its first
+// and its last item.
 struct PlanStart {
-    long long unit;  // of all units
+    long long unit, end;  // of all units
     int seq, head, tile, u;
+    int first_lo, first_hi;  // stretches of the first item (where u > 0)
+    int last_hi;             // last stretch of the item that the next stretch goes on with
+    int pad;
 };
 
 struct PlanHead {
@@ -62,11 +67,13 @@ struct PlanHead {
     int pad;
 };
 
+constexpr int kPlanMost = 512;  // stretches: a thread of the plan kernel each
+
 struct PlanArgs {
     ChunkKv c;
     ChunkSeqs sq;
     int nk, tt, kt, window, n_sink;
-    int max_ctas, min_units;  // stretches at most; units a stretch should have at least
+    int max_ctas, min_units, snap;  // stretches at most (kPlanMost at most); see above
     int least, most;          // chunk lengths that this plan takes (the others have no units)
     PlanHead *head;
     PlanStart *starts;        // [max_ctas]
@@ -100,14 +107,6 @@ inline PlanLayout plan_layout(int nt, int n_seq, int tt, int max_ctas, size_t pa
     return l;
 }
 
-// The first unit of stretch b, and the stretch that holds unit x.
-__host__ __device__ __forceinline__ long long stretch_start(long long total, int ctas, long long b) {
-    return b * total / ctas;
-}
-__host__ __device__ __forceinline__ int stretch_of(long long total, int ctas, long long x) {
-    return static_cast<int>(((x + 1) * ctas - 1) / total);
-}
-
 int launch_chunk_plan(const PlanArgs &a, cudaStream_t s);
 
 // What both attention kernels are launched with.
@@ -124,7 +123,7 @@ struct AttnParams {
 };
 
 // Fills the plan's arguments and the kernel's pointers for a workspace laid out as `lay`.
-inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int max_ctas, int min_units) {
+inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int max_ctas, int min_units, int snap) {
     PlanArgs pl = {};
     pl.c = p.a.c;
     pl.sq = p.a.sq;
@@ -135,6 +134,7 @@ inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int ma
     pl.n_sink = p.a.n_sink;
     pl.max_ctas = max_ctas;
     pl.min_units = min_units;
+    pl.snap = snap;
     pl.least = p.least;
     pl.most = p.most;
     pl.head = reinterpret_cast<PlanHead *>(ws + lay.head);
@@ -153,7 +153,6 @@ inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int ma
 // A CTA's way through its stretch, segment by segment: a segment is the stretch's part of one item.
 // Every role of a CTA walks the same segments on its own.
 struct Walk {
-    long long unit;       // of all units: the segment's first
     int left;             // units of the stretch from the segment's first on
     int seq, head, tile;  // the item
     int lo, n, past;      // its sequence: first packed row, new tokens, cached rows before them
@@ -186,11 +185,10 @@ __device__ __forceinline__ void walk_item(Walk &w, const AttnParams &p) {
 }
 // The first segment; false where the stretch is empty.
 template <int KT>
-__device__ __forceinline__ bool walk_begin(Walk &w, const AttnParams &p, long long total, int ctas) {
+__device__ __forceinline__ bool walk_begin(Walk &w, const AttnParams &p, int ctas) {
     if (static_cast<int>(blockIdx.x) >= ctas) return false;
     const PlanStart st = p.starts[blockIdx.x];
-    w.unit = st.unit;
-    w.left = static_cast<int>(stretch_start(total, ctas, blockIdx.x + 1LL) - st.unit);
+    w.left = static_cast<int>(st.end - st.unit);
     w.seq = st.seq;
     w.head = st.head;
     w.tile = st.tile;
@@ -202,7 +200,6 @@ __device__ __forceinline__ bool walk_begin(Walk &w, const AttnParams &p, long lo
 }
 template <int KT>
 __device__ __forceinline__ bool walk_next(Walk &w, const AttnParams &p) {
-    w.unit += w.u1 - w.u0;
     w.left -= w.u1 - w.u0;
     if (w.left <= 0) return false;
     w.u0 = 0;  // units are left, so the item was finished
@@ -220,6 +217,13 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnParams &p) {
     }
     walk_item<KT>(w, p);
     return true;
+}
+
+// The stretches that share the segment's item (only of a segment that is not a whole item).
+__device__ __forceinline__ void walk_parts(const Walk &w, const AttnParams &p, int &b0, int &b1) {
+    const PlanStart *st = p.starts + blockIdx.x;
+    b0 = w.u0 > 0 ? st->first_lo : static_cast<int>(blockIdx.x);
+    b1 = w.u0 > 0 ? st->first_hi : st->last_hi;
 }
 
 // Row j of the sequence is seen by some token of the item; some row of [j, j + n) is.

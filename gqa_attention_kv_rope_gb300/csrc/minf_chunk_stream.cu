@@ -34,7 +34,6 @@ namespace minf {
 namespace {
 
 constexpr int KT = 64;              // keys of a tile
-constexpr int kProducers = 4;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^15
 
 template <int HD, typename T, int NT>
@@ -63,8 +62,10 @@ struct Cfg {
     // a multiple of the groups, so that a stage is always the same group's: its warps then wait on every
     // phase of its barrier
     static constexpr int NS = kRoom / kStage > 8 ? 8 : kRoom / kStage / G * G;
+    // producer warps: a stage is always the same producer's too, for the same reason
+    static constexpr int kProducers = NS % 4 == 0 ? 4 : 2;
     static constexpr int kOffQ = NS * kStage, kOffJoin = kOffQ + kQ, kOffMeta = kOffJoin + kJoin;
-    static_assert(NS >= 2 && kStage % 1024 == 0 && kQ % 16 == 0, "ring");
+    static_assert(NS >= 2 && NS % G == 0 && NS % kProducers == 0 && kStage % 1024 == 0 && kQ % 16 == 0, "ring");
 };
 
 struct Meta {
@@ -153,14 +154,14 @@ struct Maps {
     CUtensorMap k, v;
 };
 
-// Producer warp `pw` of kProducers takes every kProducers-th tile (one warp's instructions for a tile take
-// longer than the tile's bytes).  A lane looks up two of the tile's rows (their block ids one of its
+// Producer warp `pw` takes every kProducers-th tile (one warp's instructions for a tile take longer than
+// the tile's bytes).  A lane looks up two of the tile's rows (their block ids one of its
 // tiles ahead, so that no load is waited for), and issues one of its TMA copies; Q8_0's scales come
 // beside them, a few bytes a row, by cp.async (as TMA boxes they would cost as many requests as the
 // quants).
 template <int HD, typename T, int NT>
 __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Maps &maps, const AttnParams &p, int pw,
-                                        long long total, int ctas) {
+                                        int ctas) {
     using C = Cfg<HD, T, NT>;
     const int lane = threadIdx.x & 31;
     const ChunkKv &c = p.a.c;
@@ -168,7 +169,7 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
     const int is_v = lane / (C::SLABS * pieces), rest = lane % (C::SLABS * pieces), piece = rest / C::SLABS, part = rest % C::SLABS;
     volatile int *abort_flag = &mt.abort_flag;
     Walk w;  // of the tile ahead
-    bool more = walk_begin<KT>(w, p, total, ctas);
+    bool more = walk_begin<KT>(w, p, ctas);
     int u = more ? w.u0 : 0;
     // `by` tiles on in the stretch
     auto step = [&](int by) {
@@ -198,12 +199,12 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
             if (inside || (item_sees_some(w.keys, j & box_mask, p.box_rows) && (j < w.rows.cap || !c.table)))
                 id[i] = c.table ? __ldg(reinterpret_cast<const int32_t *>(w.rows.at) + (j >> c.block_shift)) : static_cast<int>(w.rows.at);
         }
-        step(kProducers);
+        step(C::kProducers);
     };
     step(pw);
     if (!more) return;
     look_up();
-    for (int n = pw, on = 1; on; n += kProducers) {
+    for (int n = pw, on = 1; on; n += C::kProducers) {
         const int st = n % C::NS, hd = head;
         int row[2];
 #pragma unroll
@@ -269,7 +270,7 @@ __device__ __forceinline__ void join_warps(float (&acc)[C::kRegs], float *buf, i
 }
 
 template <int HD, typename T, int NT>
-__device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const AttnParams &p, long long total, int ctas) {
+__device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const AttnParams &p, int ctas) {
     using C = Cfg<HD, T, NT>;
     constexpr int R = C::R, MT = HD / 16, NB = HD / 32, kWarps = C::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n8 = lane >> 2, c4 = lane & 3;
@@ -281,7 +282,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
     constexpr size_t kPart = static_cast<size_t>(R) * (HD + 2);
     int n = 0;
     Walk w;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p)) {
+    for (bool more = walk_begin<KT>(w, p, ctas); more; more = walk_next<KT>(w, p)) {
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
         // Q: a warp a row
         for (int r = warp; r < R; r += kWarps) {
@@ -674,8 +675,8 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                         }
                 __threadfence();
             }
-            const long long item0 = w.unit - w.u0;
-            const int b0 = stretch_of(total, ctas, item0), b1 = stretch_of(total, ctas, item0 + w.keys.units - 1);
+            int b0, b1;
+            walk_parts(w, p, b0, b1);
             __syncwarp();
             if (tid == 0) mt.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
             named_sync(1, C::kComputeThreads);
@@ -783,14 +784,13 @@ __global__ void __launch_bounds__(Cfg<HD, T, NT>::kThreads, 1)
     }
     __syncthreads();
     gdc_wait();  // the plan, and everything before it
-    const long long total = p.head->total;
     const int ctas = p.head->ctas;
     if (warp < C::kWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kComputeRegs));
-        compute<HD, T, NT>(smem, mt, p, total, ctas);
+        compute<HD, T, NT>(smem, mt, p, ctas);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-        produce<HD, T, NT>(smem, mt, maps, p, warp - C::kWarps, total, ctas);
+        if (warp < C::kWarps + C::kProducers) produce<HD, T, NT>(smem, mt, maps, p, warp - C::kWarps, ctas);
     }
     if (*static_cast<volatile int *>(&mt.abort_flag)) {
         // a wait ran out: let copies in flight land before shared memory goes away
@@ -858,8 +858,7 @@ int launch_chunk_stream(const ChunkAttnArgs &a, void *workspace, int rows, int m
     p.most = most;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    // at least two tiles in a stretch: a stretch's own cost (its start, the join) is about one
-    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms, 2), s);
+    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms < kPlanMost ? sms : kPlanMost, 2, 1), s);
     if (st != MINF_OK) return st;
     if (a.hd_kv == 64)
         return n8 == 1 ? launch_kind<64, 1>(p, sms, s) : n8 == 2 ? launch_kind<64, 2>(p, sms, s) : launch_kind<64, 4>(p, sms, s);

@@ -207,8 +207,7 @@ template <int HD, typename T>
 __device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w);
 
 template <int HD, typename T, bool kV>
-__device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &map, const AttnParams &p, long long total,
-                                           int ctas) {
+__device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &map, const AttnParams &p, int ctas) {
     using C = Cfg<HD, T>;
     const int lane = threadIdx.x & 31;
     constexpr uint32_t kTileBytes = KT * HD * 2;
@@ -216,7 +215,7 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     volatile int *abort_flag = &sm.abort_flag;
     Walk w;
     int n = 0, seg = 0;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
+    for (bool more = walk_begin<KT>(w, p, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         if constexpr (kV) {
             // (the last item's rows were taken when it began, tiles ago)
             if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
@@ -262,11 +261,11 @@ __device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p
 }
 // The same for all items, as soon as the row threads have taken the last one's.
 template <int HD, typename T>
-__device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, long long total, int ctas) {
+__device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, int ctas) {
     volatile int *abort_flag = &sm.abort_flag;
     Walk w;
     int seg = 0;
-    for (bool more = walk_begin<KT>(w, p, total, ctas); more; more = walk_next<KT>(w, p), ++seg) {
+    for (bool more = walk_begin<KT>(w, p, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
         copy_q_rows<HD, T>(sm, p, w);
     }
@@ -416,13 +415,13 @@ struct SplitF32 {
 
 // Warp 9: the rows of every tile of the stretch, up to four tiles ahead.
 template <int HD, typename T>
-__device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &p, long long total, int ctas) {
+__device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &p, int ctas) {
     const int lane = threadIdx.x & 31;
     const ChunkKv &c = p.a.c;
     volatile int *abort_flag = &sm.abort_flag;
     int n = 0;
     Walk w;
-    bool more = walk_begin<KT>(w, p, total, ctas);
+    bool more = walk_begin<KT>(w, p, ctas);
     int u = more ? w.u0 : 0;
     for (bool on = more; on; ++n) {
         const int slot = n & 3;
@@ -677,7 +676,7 @@ __device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int
 
 // ----------------------------------------------------------------------------- the rows
 template <int HD, typename T>
-__device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, long long total, int ctas) {
+__device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, int ctas) {
     using C = Cfg<HD, T>;
     constexpr int HALF = HD / 2;  // dims of O a thread owns
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -687,7 +686,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
     volatile int *abort_flag = &sm.abort_flag;
     int32_t *err = p.a.err;
     if (half == 0) sm.token[row] = row / g;
-    if (tid == 0) sm.more[0] = walk_begin<KT>(sm.walk[0], p, total, ctas);
+    if (tid == 0) sm.more[0] = walk_begin<KT>(sm.walk[0], p, ctas);
     named_sync(1, kRowThreads);
     int n = 0;
     for (int seg = 0; sm.more[seg & 1]; ++seg) {
@@ -891,7 +890,6 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         sm.sum[half][row] = l;
         named_sync(1, kRowThreads);
         l = sm.sum[0][row] + sm.sum[1][row];
-        const long long item0 = w.unit - w.u0;  // the item's first unit
         const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
         // 16 dims of each half at a time through shared memory, so that a row's dims go out together
         // (a thread's own 16 bytes a row at a time cost 32 transactions an instruction)
@@ -953,7 +951,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             }
             __threadfence();
             named_sync(1, kRowThreads);
-            const int b0 = stretch_of(total, ctas, item0), b1 = stretch_of(total, ctas, item0 + w.keys.units - 1);
+            int b0, b1;
+            walk_parts(w, p, b0, b1);
             if (tid == 0) sm.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
             named_sync(1, kRowThreads);
             finish = sm.last != 0;
@@ -1074,12 +1073,11 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     tc_after();
     const uint32_t tmem = sm.tmem_base;
     gdc_wait();  // the plan, and everything before it
-    const long long total = p.head->total;
     const int ctas = p.head->ctas;
     const bool idle = static_cast<int>(blockIdx.x) >= ctas;  // no stretch
     if (warp < kRowThreads / 32) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRowRegs));
-        if (!idle) do_rows<HD, T>(sm, p, tmem, total, ctas);
+        if (!idle) do_rows<HD, T>(sm, p, tmem, ctas);
     } else if (!C::HL || warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
         if (warp == kScoreWarp) {
@@ -1090,13 +1088,13 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             __syncwarp();
         } else if constexpr (C::HL) {
             if (warp == kQueryWarp)
-                copy_q<HD, T>(sm, p, total, ctas);
+                copy_q<HD, T>(sm, p, ctas);
             else
-                resolve_rows<HD, T>(sm, p, total, ctas);
+                resolve_rows<HD, T>(sm, p, ctas);
         } else if (warp == kKeyWarp) {
-            copy_tiles<HD, T, false>(sm, tm_k, p, total, ctas);
+            copy_tiles<HD, T, false>(sm, tm_k, p, ctas);
         } else {
-            copy_tiles<HD, T, true>(sm, tm_v, p, total, ctas);
+            copy_tiles<HD, T, true>(sm, tm_v, p, ctas);
         }
     } else if constexpr (C::HL) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSplitRegs));
@@ -1172,7 +1170,7 @@ int launch_chunk_tiles(const ChunkAttnArgs &a, void *workspace, int least, cudaS
     p.most = 0x7fffffff;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms, 1), s);
+    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms < kPlanMost ? sms : kPlanMost, 1, 0), s);
     if (st != MINF_OK) return st;
     if (a.hd_kv == 64)
         return a.c.kv == kKvQ8    ? launch<64, Q8>(p, sms, s)
