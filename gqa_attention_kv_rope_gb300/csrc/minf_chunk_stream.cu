@@ -57,7 +57,7 @@ struct Cfg {
     static constexpr int kQRow = HD * 2 + 16;                        // bytes of a Q row (spread over the banks)
     static constexpr int kQ = TERMS * R * kQRow;
     static constexpr int kRegs = NT * (HD / 16) * 4;                 // fp32 outputs a lane
-    static constexpr int kJoin = kWarps / 2 * kRegs * 32 * 4;        // half of the warps' outputs
+    static constexpr int kJoin = kWarps * (HD / 16) * 4 * 32 * 4;    // every warp's outputs of 8 rows
     static constexpr int kRoom = 227 * 1024 - 1024 - kQ - kJoin - 6 * 1024;
     // a multiple of the groups, so that a stage is always the same group's: its warps then wait on every
     // phase of its barrier
@@ -251,24 +251,6 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
 }
 
 // ----------------------------------------------------------------------------- the computing warps
-// Sums the warps' outputs into warp 0's, always in the same order.
-template <typename C>
-__device__ __forceinline__ void join_warps(float (&acc)[C::kRegs], float *buf, int warp, int lane) {
-#pragma unroll
-    for (int step = C::kWarps / 2; step > 0; step >>= 1) {
-        if (warp >= step && warp < 2 * step) {
-#pragma unroll
-            for (int r = 0; r < C::kRegs; ++r) buf[((warp - step) * C::kRegs + r) * 32 + lane] = acc[r];
-        }
-        named_sync(1, C::kComputeThreads);
-        if (warp < step) {
-#pragma unroll
-            for (int r = 0; r < C::kRegs; ++r) acc[r] += buf[(warp * C::kRegs + r) * 32 + lane];
-        }
-        named_sync(1, C::kComputeThreads);
-    }
-}
-
 template <int HD, typename T, int NT>
 __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const AttnParams &p, int ctas) {
     using C = Cfg<HD, T, NT>;
@@ -620,85 +602,97 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
             if (lane == 0) mbar_arrive(&mt.empty[st]);
         }
         n += tiles;
-        // ---- join the warps
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], o);
-                if (n8 == 0) {
-                    mt.m[warp][t * 8 + 2 * c4 + e] = m[t][e];
-                    mt.l[warp][t * 8 + 2 * c4 + e] = l[t][e];
-                }
-            }
-        named_sync(1, C::kComputeThreads);
-        float M[NT][2], L[NT][2];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = t * 8 + 2 * c4 + e;
-                float mm = -INFINITY, ll = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, mt.m[k][r]);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k)
-                    if (mt.m[k][r] != -INFINITY || mt.l[k][r] != 0.0f) ll = fmaf(mt.l[k][r], ex2_approx(mt.m[k][r] - mm), ll);
-                M[t][e] = mm;
-                L[t][e] = ll;
-                // a warp that saw nothing adds nothing, whatever it holds
-                const float f = m[t][e] == -INFINITY && l[t][e] == 0.0f ? 0.0f : ex2_approx(m[t][e] - mm);
-#pragma unroll
-                for (int k = 0; k < MT; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float &a = acc[(t * MT + k) * 4 + 2 * h + e];
-                        a = f == 0.0f ? 0.0f : a * f;
-                    }
-            }
-        join_warps<C>(acc, join, warp, lane);
-        const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
-        bool finish = whole;
-        if (!whole) {
-            float *part = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
-            if (warp == 0) {
-#pragma unroll
-                for (int r = 0; r < C::kRegs; ++r) part[r * 32 + lane] = acc[r];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (n8 == 0) {
-                            part[R * HD + t * 8 + 2 * c4 + e] = M[t][e];
-                            part[R * HD + R + t * 8 + 2 * c4 + e] = L[t][e];
-                        }
-                __threadfence();
-            }
-            int b0, b1;
-            walk_parts(w, p, b0, b1);
-            __syncwarp();
-            if (tid == 0) mt.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
-            named_sync(1, C::kComputeThreads);
-            finish = mt.last != 0;
-            if (finish) {  // join the stretches' parts, dealt out to the warps, then the warps
-                __threadfence();
-                auto part_of = [&](int b) { return p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart; };
+        // ---- join the warps: row by row their maxima and sums, then, 16 dims a warp, their outputs in order
+        float M[NT][2], L[NT][2], res[NT][4];
+        auto join_all = [&]() {
+            if (n8 == 0) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = t * 8 + 2 * c4 + e;
-                        float mm = -INFINITY, ll = 0.0f;
-#pragma unroll 4
-                        for (int b = b0; b <= b1; ++b) mm = fmaxf(mm, __ldcg(part_of(b) + R * HD + r));
-#pragma unroll 4
-                        for (int b = b0; b <= b1; ++b) {
-                            const float mb = __ldcg(part_of(b) + R * HD + r), lb = __ldcg(part_of(b) + R * HD + R + r);
-                            if (mb != -INFINITY || lb != 0.0f) ll = fmaf(lb, ex2_approx(mb - mm), ll);
-                        }
-                        M[t][e] = mm;
-                        L[t][e] = ll;
+                        mt.m[warp][t * 8 + 2 * c4 + e] = m[t][e];
+                        mt.l[warp][t * 8 + 2 * c4 + e] = l[t][e];
+                    }
+            }
+            named_sync(1, C::kComputeThreads);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = t * 8 + 2 * c4 + e;
+                    float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) mm = fmaxf(mm, mt.m[k][r]);
+#pragma unroll
+                    for (int k = 0; k < kWarps; ++k) {
+                        const float mk = mt.m[k][r], lk = mt.l[k][r];
+                        if (mk != -INFINITY || lk != 0.0f) ll = fmaf(lk, ex2_approx(mk - mm), ll);
+                    }
+                    M[t][e] = mm;
+                    L[t][e] = ll;
+                    // a warp that saw nothing adds nothing, whatever it holds
+                    f[e] = m[t][e] == -INFINITY && l[t][e] == 0.0f ? 0.0f : ex2_approx(m[t][e] - mm);
+                }
+                if (t > 0) named_sync(1, C::kComputeThreads);
+#pragma unroll
+                for (int r = 0; r < MT * 4; ++r)
+                    join[(warp * MT * 4 + r) * 32 + lane] = f[r & 1] == 0.0f ? 0.0f : acc[t * MT * 4 + r] * f[r & 1];
+                named_sync(1, C::kComputeThreads);
+                if (warp < MT) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < kWarps; ++k) y += join[(k * MT * 4 + warp * 4 + e) * 32 + lane];
+                        res[t][e] = y;
+                    }
+                }
+            }
+        };
+        int b0, b1;
+        const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
+        if (!whole) walk_parts(w, p, b0, b1);  // (in flight meanwhile)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], o);
+        join_all();
+        bool finish = whole;
+        if (!whole) {
+            auto part_of = [&](int b) { return p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart; };
+            float *part = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (warp < MT) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[((t * MT + warp) * 4 + e) * 32 + lane] = res[t][e];
+                }
+                if (warp == 0 && n8 == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        part[R * HD + t * 8 + 2 * c4 + e] = M[t][e];
+                        part[R * HD + R + t * 8 + 2 * c4 + e] = L[t][e];
+                    }
+                }
+            }
+            named_sync(1, C::kComputeThreads);
+            if (tid == 0) {
+                __threadfence();  // (the whole CTA's part: the barrier ordered it before this)
+                mt.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
+                __threadfence();
+            }
+            named_sync(1, C::kComputeThreads);
+            finish = mt.last != 0;
+            if (finish) {  // join the stretches' parts, dealt out to the warps in order, then the warps
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        m[t][e] = -INFINITY;
+                        l[t][e] = 0.0f;
                     }
 #pragma unroll
                 for (int r = 0; r < C::kRegs; ++r) acc[r] = 0.0f;
@@ -707,58 +701,63 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     const float *q = part_of(b);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        float f[2];
+                        float y[MT * 4], fo[2], fn[2];
+#pragma unroll
+                        for (int r = 0; r < MT * 4; ++r) y[r] = __ldcg(q + (t * MT * 4 + r) * 32 + lane);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float mb = __ldcg(q + R * HD + t * 8 + 2 * c4 + e), lb = __ldcg(q + R * HD + R + t * 8 + 2 * c4 + e);
-                            f[e] = mb == -INFINITY && lb == 0.0f ? 0.0f : ex2_approx(mb - M[t][e]);
+                            const bool none = mb == -INFINITY && lb == 0.0f, first = m[t][e] == -INFINITY && l[t][e] == 0.0f;
+                            const float mn = fmaxf(m[t][e], mb);
+                            fo[e] = first ? 0.0f : ex2_approx(m[t][e] - mn);
+                            fn[e] = none ? 0.0f : ex2_approx(mb - mn);
+                            l[t][e] = (first ? 0.0f : l[t][e] * fo[e]) + (none ? 0.0f : lb * fn[e]);
+                            m[t][e] = mn;
                         }
 #pragma unroll
                         for (int r = 0; r < MT * 4; ++r) {
-                            const float y = __ldcg(q + (t * MT * 4 + r) * 32 + lane);
-                            if (f[r & 1] != 0.0f) acc[t * MT * 4 + r] = fmaf(y, f[r & 1], acc[t * MT * 4 + r]);
+                            float &a = acc[t * MT * 4 + r];
+                            a = a * fo[r & 1] + (fn[r & 1] == 0.0f ? 0.0f : y[r] * fn[r & 1]);
                         }
                     }
                 }
-                join_warps<C>(acc, join, warp, lane);
+                join_all();
             }
         }
         if (finish) {
-            if (warp == 0) {
+            bool odd = false;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = t * 8 + 2 * c4 + e;
-                        if (r >= rows) continue;
-                        const float inv = L[t][e] == 0.0f ? 0.0f : 1.0f / L[t][e];
-                        float *out = p.a.out + (static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g) * HD;
-                        bool odd = false;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = t * 8 + 2 * c4 + e;
+                    if (warp >= MT || r >= rows) continue;
+                    const float inv = L[t][e] == 0.0f ? 0.0f : 1.0f / L[t][e];
+                    float *out = p.a.out + (static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g) * HD;
+                    bool bad = false;
 #pragma unroll
-                        for (int k = 0; k < MT; ++k)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float y = L[t][e] == 0.0f ? 0.0f : acc[(t * MT + k) * 4 + 2 * h + e] * inv;
-                                const int d = C::Q || C::F32 ? (k >> 1) * 32 + 4 * n8 + 2 * (k & 1) + h : k * 16 + n8 + 8 * h;
-                                out[d] = y;
-                                odd |= !(fabsf(y) < INFINITY);
-                            }
-                        if (odd) mt.odd[r] = 1;
+                    for (int h = 0; h < 2; ++h) {
+                        const float y = L[t][e] == 0.0f ? 0.0f : res[t][2 * h + e] * inv;
+                        const int d = C::Q || C::F32 ? (warp >> 1) * 32 + 4 * n8 + 2 * (warp & 1) + h : warp * 16 + n8 + 8 * h;
+                        out[d] = y;
+                        bad |= !(fabsf(y) < INFINITY);
                     }
-            }
-            named_sync(1, C::kComputeThreads);
+                    if (bad) mt.odd[r] = 1;
+                    odd |= bad;
+                }
             // rows that are not finite: by the definition, a row a warp
-            for (int r = warp; r < rows; r += kWarps) {
-                if (!mt.odd[r]) continue;
-                RowJob job;
-                const long long t = walk_row(w, p) + r / g;
-                job.q = p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd;
-                job.out = p.a.out + (t * p.a.nh + w.head * g + r % g) * HD;
-                job.rows = w.rows;
-                job.p = walk_pos(w, p) + r / g;
-                job.hk = w.head;
-                attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
-            }
+            if (!named_all(1, C::kComputeThreads, !odd))
+                for (int r = warp; r < rows; r += kWarps) {
+                    if (!mt.odd[r]) continue;
+                    RowJob job;
+                    const long long at = static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g;
+                    job.q = p.a.q + at * p.a.hd;
+                    job.out = p.a.out + at * HD;
+                    job.rows = w.rows;
+                    job.p = walk_pos(w, p) + r / g;
+                    job.hk = w.head;
+                    attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
+                }
         }
         named_sync(1, C::kComputeThreads);  // Q, limits and the join buffer are free
     }

@@ -949,45 +949,43 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     part[BM * (HD + 1) + row] = l;
                 }
             }
-            __threadfence();
-            named_sync(1, kRowThreads);
             int b0, b1;
             walk_parts(w, p, b0, b1);
-            if (tid == 0) sm.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
+            named_sync(1, kRowThreads);
+            if (tid == 0) {
+                __threadfence();  // (the whole CTA's part: the barrier ordered it before this)
+                sm.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
+                __threadfence();
+            }
             named_sync(1, kRowThreads);
             finish = sm.last != 0;
             if (finish) {
-                __threadfence();
-                // join the parts in the order of their keys (dead rows read what is there and are not put)
-                float M = -INFINITY;
-#pragma unroll 4
-                for (int b = b0; b <= b1; ++b) {
-                    const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
-                    M = fmaxf(M, __ldcg(q + BM * HD + row));
-                }
-                constexpr int JD = 32;  // dims of a pass
+                // join the parts in the order of their keys (dead rows read what is there and are not put); two
+                // parts' loads are in flight at a time
+                constexpr int JD = C::HL ? 32 : HALF;  // dims of a pass
 #pragma unroll 1
                 for (int d0 = 0; d0 < HALF; d0 += JD) {
-                    float L = 0.0f;
+                    float M = -INFINITY, L = 0.0f;
                     float y[JD];
 #pragma unroll
                     for (int d = 0; d < JD; ++d) y[d] = 0.0f;
-#pragma unroll(C::HL ? 1 : 3)
+#pragma unroll(C::HL ? 1 : 2)
                     for (int b = b0; b <= b1; ++b) {
                         const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
                         const float mb = __ldcg(q + BM * HD + row), lb = __ldcg(q + BM * (HD + 1) + row);
                         float4 x[JD / 4];
 #pragma unroll
                         for (int d = 0; d < JD / 4; ++d) x[d] = __ldcg(reinterpret_cast<const float4 *>(q) + ((half * HALF + d0) / 4 + d) * BM + row);
-                        const bool none = mb == -INFINITY && lb == 0.0f;  // saw nothing, whatever it holds
-                        const float f = none ? 0.0f : ex2_approx(mb - M);
-                        L = fmaf(none ? 0.0f : lb, f, L);
+                        if (mb == -INFINITY && lb == 0.0f) continue;  // saw nothing, whatever it holds
+                        const float mn = fmaxf(M, mb), fo = ex2_approx(M - mn), fn = ex2_approx(mb - mn);
+                        M = mn;
+                        L = L * fo + lb * fn;
 #pragma unroll
                         for (int d = 0; d < JD / 4; ++d) {
-                            y[4 * d] = none ? y[4 * d] : fmaf(x[d].x, f, y[4 * d]);
-                            y[4 * d + 1] = none ? y[4 * d + 1] : fmaf(x[d].y, f, y[4 * d + 1]);
-                            y[4 * d + 2] = none ? y[4 * d + 2] : fmaf(x[d].z, f, y[4 * d + 2]);
-                            y[4 * d + 3] = none ? y[4 * d + 3] : fmaf(x[d].w, f, y[4 * d + 3]);
+                            y[4 * d] = y[4 * d] * fo + x[d].x * fn;
+                            y[4 * d + 1] = y[4 * d + 1] * fo + x[d].y * fn;
+                            y[4 * d + 2] = y[4 * d + 2] * fo + x[d].z * fn;
+                            y[4 * d + 3] = y[4 * d + 3] * fo + x[d].w * fn;
                         }
                     }
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
@@ -996,8 +994,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         y[d] = L == 0.0f ? 0.0f : y[d] * inv;
                         odd |= !(fabsf(y[d]) < INFINITY);
                     }
-                    put(y, d0);
-                    put(y + 16, d0 + 16);
+#pragma unroll
+                    for (int d = 0; d < JD; d += 16) put(y + d, d0 + d);
                 }
             }
         }
