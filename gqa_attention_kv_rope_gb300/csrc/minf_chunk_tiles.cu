@@ -51,9 +51,9 @@ namespace minf {
 namespace {
 
 constexpr int BM = 128, KT = 128;
-constexpr int kRowThreads = 256;  // warps 0-7: two threads a query row
 constexpr int kSplitWarps = 4, kSplitRows = KT / kSplitWarps;  // for K and for V each; rows of a tile a warp takes
-constexpr int kScoreWarp = 8, kKeyWarp = 9, kValueWarp = 10, kQueryWarp = 11;
+// The warps after the row threads': S, K copies (or rows resolved), P V, V copies (or Q rows)
+constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
 constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^(shift + slack) = 2^15
 // TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
 // column)
@@ -65,12 +65,15 @@ struct Cfg {
     static constexpr int SLABS = HD / 64;                        // 128-byte-wide slabs of a tile
     static constexpr int TERMS = HL ? 2 : 1;
     static constexpr int NS = HL ? (HD == 64 ? 2 : 1) : (HD == 64 ? 4 : 2);  // K and V stages
-    // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3, 4).  The rows'
-    // threads hold 64 scores and their halves, so registers move to them; the shares add up to the
-    // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
-    static constexpr int kThreads = HL ? 640 : 384;
-    static constexpr int kRowRegs = HL ? 144 : 208, kIssueRegs = HL ? 48 : 88;
-    static constexpr int kSplitRegs = 72;  // (HL)
+    // Row threads: PARTS threads a row, each with as many of a tile's keys and of the row's dims.  Four (for
+    // binary16) hide one another's waits better than two; the splitting producers leave registers for two.
+    static constexpr int PARTS = HL ? 2 : 4, COLS = KT / PARTS, DIMS = HD / PARTS;
+    static constexpr int kRowThreads = 128 * PARTS, kRowWarps = kRowThreads / 32;
+    // Warp groups: rows, the issuing and copying warps, the splitting producers (two groups).  Registers move
+    // to the rows' threads; the shares add up to no more than the launch's: 512 * 104 + 128 * 64 = 640 * 96
+    // and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
+    static constexpr int kThreads = 640;
+    static constexpr int kRowRegs = HL ? 144 : 104, kIssueRegs = HL ? 48 : 64;
     static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
@@ -84,7 +87,7 @@ struct Smem {
     unsigned long long k_stat[4], v_stat[4];           // hi + lo kinds: factors of a tile written
     unsigned long long row_full[4], row_free[4];       // and its rows resolved, taken
     alignas(16) float out[BM][36];                     // 32 dims of the output rows on their way out
-    float mx[2][2][BM], sum[2][BM];
+    float mx[2][C::PARTS][BM], sum[C::PARTS][BM];
     int odd[BM];                                       // rows whose result is not finite
     int token[BM];                                     // of each row (a division otherwise)
     // the row threads' walk (here, not in every thread's registers): segment n in walk[n % 2]
@@ -166,6 +169,18 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t *u) {
         "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
         "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
         : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t t, const uint32_t *u) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_st(uint32_t t, const uint32_t *u) {
+    if constexpr (N == 8)
+        tm_st8(t, u);
+    else
+        tm_st16(t, u);
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -678,16 +693,17 @@ __device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int
 template <int HD, typename T>
 __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, uint32_t tmem, int ctas) {
     using C = Cfg<HD, T>;
-    constexpr int HALF = HD / 2;  // dims of O a thread owns
+    constexpr int PARTS = C::PARTS, COLS = C::COLS, DIMS = C::DIMS;  // keys and dims of a thread
+    constexpr int OD = 32 / PARTS;                                    // dims of a part in an output pass
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int half = warp >> 2, row = tid & 127;
+    const int part = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
     const int g = p.a.nh / p.a.nk;
     volatile int *abort_flag = &sm.abort_flag;
     int32_t *err = p.a.err;
-    if (half == 0) sm.token[row] = row / g;
+    if (part == 0) sm.token[row] = row / g;
     if (tid == 0) sm.more[0] = walk_begin<KT>(sm.walk[0], p, ctas);
-    named_sync(1, kRowThreads);
+    named_sync(1, C::kRowThreads);
     int n = 0;
     for (int seg = 0; sm.more[seg & 1]; ++seg) {
         const Walk &w = sm.walk[seg & 1];
@@ -696,31 +712,37 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         float c;
         {
             mbar_wait(&sm.q_in, seg & 1, abort_flag, err);
-            float4 x[HALF / 4];
+            float4 x[DIMS / 4];
             float am = 0.0f;
 #pragma unroll
-            for (int d = 0; d < HALF / 4; ++d) {
-                x[d] = row < rows ? *reinterpret_cast<const float4 *>(sm.q + row * C::kQRow + (half * (HALF / 4) + d) * 16)
+            for (int d = 0; d < DIMS / 4; ++d) {
+                x[d] = row < rows ? *reinterpret_cast<const float4 *>(sm.q + row * C::kQRow + (part * (DIMS / 4) + d) * 16)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
                 am = fmaxf(am, fmaxf(fmaxf(fabsf(x[d].x), fabsf(x[d].y)), fmaxf(fabsf(x[d].z), fabsf(x[d].w))));
             }
-            sm.sum[half][row] = am;
-            if (half == 0) sm.odd[row] = 0;
-            named_sync(1, kRowThreads);
+            sm.sum[part][row] = am;
+            if (part == 0) sm.odd[row] = 0;
+            named_sync(1, C::kRowThreads);
             if (tid == 0) mbar_arrive(&sm.q_free);  // (every thread has read its part)
-            const int sh = row_shift(fmaxf(sm.sum[0][row], sm.sum[1][row]), 126);
-            const float f = pow2i(sh);
-            c = p.scale_log2 * pow2i(-sh);
+            am = sm.sum[0][row];
 #pragma unroll
-            for (int d0 = 0; d0 < HALF / 4; d0 += 8) {  // 32 dims: 16 columns
-                uint32_t hi[16], lo[16];
+            for (int k = 1; k < PARTS; ++k) am = fmaxf(am, sm.sum[k][row]);
+            const int sh = row_shift(am, 126);
+            const float f = p.scale_log2 < 0.0f ? -pow2i(sh) : pow2i(sh);
+            // S * c is the score in powers of two, c > 0: a row's largest S is its largest score (the sign of
+            // the caller's scale is Q's; a scale of zero is one too small to matter)
+            c = fmaxf(fabsf(p.scale_log2) * pow2i(-sh), 1e-38f);
+            constexpr int QD = DIMS < 32 ? DIMS : 32;  // dims of a store: half as many columns
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
+            for (int d0 = 0; d0 < DIMS / 4; d0 += QD / 4) {
+                uint32_t hi[QD / 2], lo[QD / 2];
+#pragma unroll
+                for (int d = 0; d < QD / 4; ++d) {
                     split2(x[d0 + d].x * f, x[d0 + d].y * f, hi[2 * d], lo[2 * d]);
                     split2(x[d0 + d].z * f, x[d0 + d].w * f, hi[2 * d + 1], lo[2 * d + 1]);
                 }
-                tm_st16(lanes + kColQ + half * (HALF / 2) + d0 * 2, hi);
-                tm_st16(lanes + kColQ + HD / 2 + half * (HALF / 2) + d0 * 2, lo);
+                tm_st<QD / 2>(lanes + kColQ + part * (DIMS / 2) + d0 * 2, hi);
+                tm_st<QD / 2>(lanes + kColQ + HD / 2 + part * (DIMS / 2) + d0 * 2, lo);
             }
             tm_wait_st();
             tc_before();
@@ -740,18 +762,18 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             sm.more[(seg + 1) & 1] = walk_next<KT>(next, p);
             sm.walk[(seg + 1) & 1] = next;
         }
-        named_sync(1, kRowThreads);
+        named_sync(1, C::kRowThreads);
         float m = -INFINITY, l = 0.0f;
         for (int i = 0; i < tiles; ++i) {
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
             mbar_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
             tc_after();
             if (!warp_live) {
-                named_sync(1, kRowThreads);
+                named_sync(1, C::kRowThreads);
             } else {
-                uint32_t x[64];  // scores, as bits
-                tm_ld32(lanes + kColS + (q & 1) * KT + half * 64, x);
-                tm_ld32(lanes + kColS + (q & 1) * KT + half * 64 + 32, x + 32);
+                uint32_t x[COLS];  // S, then what the exponentials take, as bits
+#pragma unroll
+                for (int e = 0; e < COLS; e += 32) tm_ld32(lanes + kColS + (q & 1) * KT + part * COLS + e, x + e);
                 float cc = c, ve = 0.0f, vi = 1.0f;
                 bool k_rows = false, v_rows = false;
                 if constexpr (C::HL) {
@@ -766,26 +788,23 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 tm_wait_ld();
                 const int2 all = sm.all;
                 const bool mask = j0 + KT > all.y || (j0 < all.x && j0 + KT > p.a.n_sink);
-                if (!C::HL || !(k_rows || v_rows)) {
-                    const float2 c2 = make_float2(cc, cc), e2 = make_float2(ve, ve);
+                // key by key factors (rare): t = S c k + e now, else one multiply-add below takes S to its exponential
+                const bool by_key = C::HL && (k_rows || v_rows);
+                if (by_key) {
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float2 a = C::HL ? fma2(bits2(x[e], x[e + 1]), c2, e2) : mul2(bits2(x[e], x[e + 1]), c2);
-                        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
+                    for (int e = 0; e < COLS; e += 4) {
                         float4 kf = make_float4(cc, cc, cc, cc), vv = make_float4(ve, ve, ve, ve);
                         if (k_rows) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][half * 64 + e]);
+                            const float4 f = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][part * COLS + e]);
                             kf = make_float4(f.x * cc, f.y * cc, f.z * cc, f.w * cc);
                         }
-                        if (v_rows) vv = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][half * 64 + e]);
+                        if (v_rows) vv = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][part * COLS + e]);
                         const float2 a = fma2(bits2(x[e], x[e + 1]), lo2(kf), lo2(vv)), b = fma2(bits2(x[e + 2], x[e + 3]), hi2(kf), hi2(vv));
                         x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
                         x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
                     }
+                    cc = 1.0f;
+                    ve = 0.0f;
                 }
                 if (mask) {
                     // this row's window: keys [r_lo, r_hi) and [0, r_sink)
@@ -799,24 +818,27 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                             r_sink = min(p.a.n_sink, r_hi);
                         }
                     }
-                    const int jb = j0 + half * 64, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
+                    const int jb = j0 + part * COLS, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
+                    for (int e = 0; e < COLS; ++e) {
                         const bool see = (e < e_hi) & ((e >= e_lo) | (e < e_sink));
                         x[e] = see ? x[e] : 0xff800000u;  // -infinity
                     }
                 }
                 float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 64; e += 8)
+                for (int e = 0; e < COLS; e += 8)
 #pragma unroll
                     for (int f = 0; f < 4; ++f)
                         mt[f] = fmaxf(fmaxf(mt[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + 4 + f]));
-                sm.mx[q & 1][half][row] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+                sm.mx[q & 1][part][row] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
                 tc_before();
-                named_sync(1, kRowThreads);  // both threads of a row have read S: P may go over it
+                named_sync(1, C::kRowThreads);  // all threads of a row have read S: P may go over it
                 tc_after();
-                const float mn = fmaxf(sm.mx[q & 1][0][row], sm.mx[q & 1][1][row]);
+                float mn = sm.mx[q & 1][0][row];
+#pragma unroll
+                for (int k = 1; k < PARTS; ++k) mn = fmaxf(mn, sm.mx[q & 1][k][row]);
+                mn = mn * cc + ve;
                 const bool grow = mn > m + kSlack || (m == -INFINITY && mn > m);
                 float corr = 1.0f;
                 if (grow) {
@@ -827,24 +849,24 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     mbar_wait(&sm.o_done[(q - 1) & 1], ((q - 1) >> 1) & 1, abort_flag, err);
                     tc_after();
 #pragma unroll 1
-                    for (int d = 0; d < HALF; d += 16) {
+                    for (int d = 0; d < DIMS; d += 16) {
                         uint32_t o[16];
-                        tm_ld16(lanes + kColO + half * HALF + d, o);
+                        tm_ld16(lanes + kColO + part * DIMS + d, o);
                         tm_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                        tm_st16(lanes + kColO + half * HALF + d, o);
+                        tm_st<16>(lanes + kColO + part * DIMS + d, o);
                     }
                 }
                 const float base = m == -INFINITY ? 0.0f : m - kShift;
-                const float2 nb = make_float2(-base, -base);
+                const float2 c2 = make_float2(cc, cc), nb = make_float2(ve - base, ve - base);
                 float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
-                for (int e0 = 0; e0 < 64; e0 += 32) {
+                for (int e0 = 0; e0 < COLS; e0 += 32) {
                     uint32_t ph[16], pl[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        float2 a = add2(bits2(x[e0 + e], x[e0 + e + 1]), nb), b = add2(bits2(x[e0 + e + 2], x[e0 + e + 3]), nb);
+                        float2 a = fma2(bits2(x[e0 + e], x[e0 + e + 1]), c2, nb), b = fma2(bits2(x[e0 + e + 2], x[e0 + e + 3]), c2, nb);
                         a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         b = make_float2(ex2_approx(b.x), ex2_approx(b.y));
                         s2 = add2(s2, a);
@@ -852,8 +874,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         split2(a.x, a.y, ph[e >> 1], pl[e >> 1]);
                         split2(b.x, b.y, ph[(e >> 1) + 1], pl[(e >> 1) + 1]);
                     }
-                    tm_st16(lanes + kColS + (q & 1) * KT + half * 32 + (e0 >> 1), ph);
-                    tm_st16(lanes + kColS + (q & 1) * KT + 64 + half * 32 + (e0 >> 1), pl);
+                    tm_st<16>(lanes + kColS + (q & 1) * KT + part * (COLS / 2) + (e0 >> 1), ph);
+                    tm_st<16>(lanes + kColS + (q & 1) * KT + 64 + part * (COLS / 2) + (e0 >> 1), pl);
                 }
                 float sum = (s2.x + s2.y) + (s3.x + s3.y);
                 if constexpr (C::HL) {
@@ -861,7 +883,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     if (v_rows) {  // each key's own 2^-e
                         sum = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) sum = fmaf(ex2_approx(__uint_as_float(x[e]) - base), sm.v_inv[q & 3][half * 64 + e], sum);
+                        for (int e = 0; e < COLS; ++e) sum = fmaf(ex2_approx(__uint_as_float(x[e]) * cc + (ve - base)), sm.v_inv[q & 3][part * COLS + e], sum);
                     }
                 }
                 l = l * corr + sum;
@@ -870,7 +892,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
                 // rows of this tile that no token sees: V must hold zeros there
                 mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
-                if (half == 0 && !item_sees(w.keys, j0 + row)) {
+                if (part == 0 && !item_sees(w.keys, j0 + row)) {
 #pragma unroll
                     for (int s = 0; s < C::SLABS; ++s)
 #pragma unroll
@@ -887,84 +909,86 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         n += tiles;
         mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, err);
         tc_after();
-        sm.sum[half][row] = l;
-        named_sync(1, kRowThreads);
-        l = sm.sum[0][row] + sm.sum[1][row];
+        sm.sum[part][row] = l;
+        named_sync(1, C::kRowThreads);
+        l = sm.sum[0][row];
+#pragma unroll
+        for (int k = 1; k < PARTS; ++k) l += sm.sum[k][row];
         const bool whole = w.u0 == 0 && w.u1 == w.keys.units;
-        // 16 dims of each half at a time through shared memory, so that a row's dims go out together
-        // (a thread's own 16 bytes a row at a time cost 32 transactions an instruction)
+        // 32 dims of a row (OD of each part's) at a time through shared memory, so that they go out together (a
+        // thread's own 16 bytes a row at a time cost 32 transactions an instruction)
         float *item_out = p.a.out + (static_cast<long long>(walk_row(w, p)) * p.a.nh + w.head * g) * HD;
         auto put = [&](const float *y, int d) {
-            *reinterpret_cast<float4 *>(&sm.out[row][half * 16]) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
-            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 8]) = make_float4(y[8], y[9], y[10], y[11]);
-            *reinterpret_cast<float4 *>(&sm.out[row][half * 16 + 12]) = make_float4(y[12], y[13], y[14], y[15]);
-            named_sync(1, kRowThreads);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = k * 32 + (tid >> 3);  // eight lanes a row: four of each half
+            for (int e = 0; e < OD; e += 4)
+                *reinterpret_cast<float4 *>(&sm.out[row][part * OD + e]) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+            named_sync(1, C::kRowThreads);
+#pragma unroll
+            for (int k = 0; k < 128 * 8 / C::kRowThreads; ++k) {
+                const int r = k * (C::kRowThreads / 8) + (tid >> 3), q = (tid & 7) * 4;  // eight lanes a row
                 if (r < rows) {
                     const int t = sm.token[r];
-                    *reinterpret_cast<float4 *>(item_out + (t * p.a.nh + r - t * g) * HD + ((tid & 7) >> 2) * HALF + (tid & 3) * 4 + d) =
-                        *reinterpret_cast<const float4 *>(&sm.out[r][(tid & 7) * 4]);
+                    *reinterpret_cast<float4 *>(item_out + (t * p.a.nh + r - t * g) * HD + q / OD * DIMS + q % OD + d) =
+                        *reinterpret_cast<const float4 *>(&sm.out[r][q]);
                 }
             }
-            named_sync(1, kRowThreads);
+            named_sync(1, C::kRowThreads);
         };
         bool finish = whole, odd = false;
         if (whole) {
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll 1
-            for (int d = 0; d < HALF; d += 16) {
+            for (int d = 0; d < DIMS; d += 16) {
                 uint32_t o[16];
                 float y[16];
-                tm_ld16(lanes + kColO + half * HALF + d, o);
+                tm_ld16(lanes + kColO + part * DIMS + d, o);
                 tm_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     y[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
                     odd |= !(fabsf(y[e]) < INFINITY);
                 }
-                put(y, d);
+#pragma unroll
+                for (int e = 0; e < 16; e += OD) put(y + e, d + e);
             }
         } else {
             // this stretch's part: O as [dims / 4][rows] float4, then the rows' maxima and sums
             constexpr size_t kPart = static_cast<size_t>(BM) * (HD + 2);
-            float *part = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
+            float *mine = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
             if (warp_live) {
 #pragma unroll
-                for (int d = 0; d < HALF; d += 32) {
-                    uint32_t o[32];
-                    tm_ld32(lanes + kColO + half * HALF + d, o);
+                for (int d = 0; d < DIMS; d += 16) {
+                    uint32_t o[16];
+                    tm_ld16(lanes + kColO + part * DIMS + d, o);
                     tm_wait_ld();
                     if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            reinterpret_cast<float4 *>(part)[((half * HALF + d + e) >> 2) * BM + row] =
+                        for (int e = 0; e < 16; e += 4)
+                            reinterpret_cast<float4 *>(mine)[((part * DIMS + d + e) >> 2) * BM + row] =
                                 make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
                     }
                 }
-                if (live && half == 0) {
-                    part[BM * HD + row] = m;
-                    part[BM * (HD + 1) + row] = l;
+                if (live && part == 0) {
+                    mine[BM * HD + row] = m;
+                    mine[BM * (HD + 1) + row] = l;
                 }
             }
             int b0, b1;
             walk_parts(w, p, b0, b1);
-            named_sync(1, kRowThreads);
+            named_sync(1, C::kRowThreads);
             if (tid == 0) {
                 __threadfence();  // (the whole CTA's part: the barrier ordered it before this)
                 sm.last = atomicAdd(p.tickets + b0, 1) == b1 - b0;
                 __threadfence();
             }
-            named_sync(1, kRowThreads);
+            named_sync(1, C::kRowThreads);
             finish = sm.last != 0;
             if (finish) {
                 // join the parts in the order of their keys (dead rows read what is there and are not put); two
                 // parts' loads are in flight at a time
-                constexpr int JD = C::HL ? 32 : HALF;  // dims of a pass
+                constexpr int JD = C::HL ? 32 : DIMS;  // dims of a pass
 #pragma unroll 1
-                for (int d0 = 0; d0 < HALF; d0 += JD) {
+                for (int d0 = 0; d0 < DIMS; d0 += JD) {
                     float M = -INFINITY, L = 0.0f;
                     float y[JD];
 #pragma unroll
@@ -975,7 +999,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         const float mb = __ldcg(q + BM * HD + row), lb = __ldcg(q + BM * (HD + 1) + row);
                         float4 x[JD / 4];
 #pragma unroll
-                        for (int d = 0; d < JD / 4; ++d) x[d] = __ldcg(reinterpret_cast<const float4 *>(q) + ((half * HALF + d0) / 4 + d) * BM + row);
+                        for (int d = 0; d < JD / 4; ++d) x[d] = __ldcg(reinterpret_cast<const float4 *>(q) + ((part * DIMS + d0) / 4 + d) * BM + row);
                         if (mb == -INFINITY && lb == 0.0f) continue;  // saw nothing, whatever it holds
                         const float mn = fmaxf(M, mb), fo = ex2_approx(M - mn), fn = ex2_approx(mb - mn);
                         M = mn;
@@ -995,7 +1019,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         odd |= !(fabsf(y[d]) < INFINITY);
                     }
 #pragma unroll
-                    for (int d = 0; d < JD; d += 16) put(y + d, d0 + d);
+                    for (int d = 0; d < JD; d += OD) put(y + d, d0 + d);
                 }
             }
         }
@@ -1003,8 +1027,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             odd = odd && live;
             if (odd) sm.odd[row] = 1;
             // rows that are not finite: by the definition, a row a warp
-            if (!named_all(1, kRowThreads, !odd))
-                for (int r = warp; r < rows; r += kRowThreads / 32) {
+            if (!named_all(1, C::kRowThreads, !odd))
+                for (int r = warp; r < rows; r += C::kRowWarps) {
                     if (!sm.odd[r]) continue;
                     RowJob job;
                     const long long at = static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g;
@@ -1017,7 +1041,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 }
         }
         tc_before();
-        named_sync(1, kRowThreads);  // sm.odd and sm.sum are free for the next segment
+        named_sync(1, C::kRowThreads);  // sm.odd and sm.sum are free for the next segment
     }
     if (tid == 0) sm.seg_tiles = 0;
     __syncwarp();
@@ -1035,9 +1059,9 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     if (tid == 0) {
         mbar_init(&sm.q_in, 1);
         mbar_init(&sm.q_free, 1);
-        mbar_init(&sm.q_full, kRowThreads / 32);
+        mbar_init(&sm.q_full, C::kRowWarps);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.p_ready[i], kRowThreads / 32);
+            mbar_init(&sm.p_ready[i], C::kRowWarps);
             mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.s_full[i], 1);
         }
@@ -1060,7 +1084,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             prefetch_tensormap(&tm_v);
         }
     }
-    if (warp == kScoreWarp) {
+    if (warp == C::kRowWarps + kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sm.tmem_base)),
                      "r"(kTmemCols)
                      : "memory");
@@ -1072,41 +1096,42 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     const uint32_t tmem = sm.tmem_base;
     gdc_wait();  // the plan, and everything before it
     const int ctas = p.head->ctas;
+    const int role = warp - C::kRowWarps;
     const bool idle = static_cast<int>(blockIdx.x) >= ctas;  // no stretch
-    if (warp < kRowThreads / 32) {
+    if (warp < C::kRowWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRowRegs));
         if (!idle) do_rows<HD, T>(sm, p, tmem, ctas);
-    } else if (!C::HL || warp < 12) {
+    } else if (!C::HL || warp < C::kRowWarps + 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
-        if (warp == kScoreWarp) {
+        if (warp == C::kRowWarps + kScoreWarp) {
             if (lane == 0 && !idle) issue_scores<HD, T>(sm, tmem, p.a.err);
             __syncwarp();
-        } else if (warp == kValueWarp) {
+        } else if (role == kValueWarp) {
             if (lane == 0 && !idle) issue_values<HD, T>(sm, tmem, p.a.err);
             __syncwarp();
         } else if constexpr (C::HL) {
-            if (warp == kQueryWarp)
+            if (role == kQueryWarp)
                 copy_q<HD, T>(sm, p, ctas);
             else
                 resolve_rows<HD, T>(sm, p, ctas);
-        } else if (warp == kKeyWarp) {
+        } else if (role == kKeyWarp) {
             copy_tiles<HD, T, false>(sm, tm_k, p, ctas);
         } else {
             copy_tiles<HD, T, true>(sm, tm_v, p, ctas);
         }
     } else if constexpr (C::HL) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSplitRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
         if (idle) {
-        } else if (warp < 16) {
-            split_tiles<HD, T, false>(sm, p, warp - 12);
+        } else if (role < 8) {
+            split_tiles<HD, T, false>(sm, p, role - 4);
         } else {
-            split_tiles<HD, T, true>(sm, p, warp - 16);
+            split_tiles<HD, T, true>(sm, p, role - 8);
         }
     }
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == kScoreWarp) {
+    if (warp == C::kRowWarps + kScoreWarp) {
         if (*static_cast<volatile int *>(&sm.abort_flag)) {
             // a wait ran out: let copies and MMAs in flight finish before TMEM and shared memory go away
             const unsigned long long t0 = gtimer();
