@@ -65,15 +65,16 @@ struct Cfg {
     static constexpr int SLABS = HD / 64;                        // 128-byte-wide slabs of a tile
     static constexpr int TERMS = HL ? 2 : 1;
     static constexpr int NS = HL ? (HD == 64 ? 2 : 1) : (HD == 64 ? 4 : 2);  // K and V stages
-    // Row threads: PARTS threads a row, each with as many of a tile's keys and of the row's dims.  Four (for
-    // binary16) hide one another's waits better than two; the splitting producers leave registers for two.
-    static constexpr int PARTS = HL ? 2 : 4, COLS = KT / PARTS, DIMS = HD / PARTS;
+    // Row threads: two threads a row, each with half of a tile's keys and of the row's dims.  (Four, which
+    // hide one another's waits better but meet at a wider barrier, measured the same over binary16: 1155 us
+    // against 1102 on the ragged batch below.)
+    static constexpr int PARTS = 2, COLS = KT / PARTS, DIMS = HD / PARTS;
     static constexpr int kRowThreads = 128 * PARTS, kRowWarps = kRowThreads / 32;
-    // Warp groups: rows, the issuing and copying warps, the splitting producers (two groups).  Registers move
-    // to the rows' threads; the shares add up to no more than the launch's: 512 * 104 + 128 * 64 = 640 * 96
-    // and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
-    static constexpr int kThreads = 640;
-    static constexpr int kRowRegs = HL ? 144 : 104, kIssueRegs = HL ? 48 : 64;
+    // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3, 4).  The rows'
+    // threads hold 64 scores and their halves, so registers move to them; the shares add up to the
+    // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
+    static constexpr int kThreads = HL ? 640 : 384;
+    static constexpr int kRowRegs = HL ? 144 : 208, kIssueRegs = HL ? 48 : 88;
     static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
