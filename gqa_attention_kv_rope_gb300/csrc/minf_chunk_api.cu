@@ -54,6 +54,12 @@ int set_paged(ChunkKv *c, const void *k, const void *v, int kv, int64_t pool_row
     return MINF_OK;
 }
 
+// Two stretches of floats share some.  (A query row is read again after parts of out are written.)
+bool overlap(const float *a, size_t na, const float *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb * sizeof(float) && y < x + na * sizeof(float);
+}
+
 bool ok_seqs(const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq) {
     return n_past && nt >= 0 && n_seq >= 0 && (chunk_off || nt == n_seq);
 }
@@ -117,6 +123,7 @@ int attention(ChunkAttnArgs &a, float *out, const float *q, const int32_t *chunk
     if (nt == 0 || n_seq == 0) return MINF_OK;
     const size_t need = chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk);
     if (!ws || !aligned16(ws) || ws_bytes < need) return MINF_ERR_WORKSPACE;
+    if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd)) return MINF_ERR_ARG;
     a.out = out;
     a.q = q;
     a.sq = {chunk_off, n_past, nt, n_seq};
@@ -191,6 +198,7 @@ int layer_step(float *xn, const float *h, const float *gain, float eps, int n_em
     if (nt == 0 || n_seq == 0) return MINF_OK;
     if (!ws || !aligned16(ws) || ws_bytes < chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk))
         return MINF_ERR_WORKSPACE;
+    if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd)) return MINF_ERR_ARG;
     st = launch_rms_norm(xn, h, gain, nt, n_embd, eps, cs(stream));
     if (st != MINF_OK) return st;
     st = rope_store(q, k, q, k, v, rope_pos, n_axis, pair_axis, chunk_off, n_past, nt, n_seq, nh, nk, hd, hd_kv, theta,

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     }
     // a thread a stretch: its start, moved to an item's border that is near
     __shared__ long long start[kPlanMost + 1];
-    __shared__ int first_lo[kPlanMost + 1], first_hi[kPlanMost + 1];
+    __shared__ int first_hi[kPlanMost + 1];
     __shared__ int kept_warp[kPlanThreads / 32];
     long long x = tid < ctas ? tid * total / ctas : total;
     int l = 0, tile = 0, head = 0, tiles = 0;
@@ -185,10 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         while (start[lo] > item0) --lo;
         while (hi + 1 < n && start[hi + 1] < item1) ++hi;
     }
-    if (keep) {
-        first_lo[at] = lo;
-        first_hi[at] = hi;
-    }
+    if (keep) first_hi[at] = hi;
     __syncthreads();
     if (keep) {
         PlanStart st;

@@ -4,10 +4,10 @@
 // kv head's query heads, and its units are the key tiles of `kt` rows that any of its tokens sees
 // (the sinks' tiles, then the window's).  All units in order (sequence, kv head, token tile, key
 // tile) are cut into equal stretches, one a CTA, so every CTA streams the same amount whatever the
-// lengths are.  (A part of an item costs as much as several tiles to write and to join: a cut that would
-// fall within `snap` units of an item's border falls on it, and no stretch is shorter than min_units.)  An item that lies in one stretch is finished by its CTA; one that crosses
-// stretches is joined, in order, by the last of its CTAs to finish: two calls with the same
-// inputs add in the same order.
+// lengths are.  (A cut that would fall within `snap` units of an item's border falls on it, and no
+// stretch is shorter than min_units: a part of an item costs about a tile to write and to join.)  An
+// item that lies in one stretch is finished by its CTA; one that crosses stretches is joined, in order,
+// by the last of its CTAs to finish: two calls with the same inputs add in the same order.
 //
 // The lengths are device data, so the cut is made on the device by a one-block kernel ahead of
 // the attention kernel (which is launched at once and waits for it).  That kernel also checks
@@ -16,6 +16,7 @@
 #pragma once
 
 #include "minf_chunk.cuh"
+#include "minf_sm103.cuh"
 
 namespace minf {
 
@@ -217,6 +218,36 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnParams &p) {
     }
     walk_item<KT>(w, p);
     return true;
+}
+
+// mbar_wait of the attention kernels.  Rows that are computed again by their definition (attn_row) may take
+// far longer than the wait's budget; while they are (abort_flag is kRowsAgain) the clock of everyone who
+// waits for that CTA's next step starts anew.  abort_flag is 1 once a wait has run out.
+constexpr int kRowsAgain = 2;
+__device__ __forceinline__ uint32_t gtimer_lo() {  // nanoseconds, modulo 2^32: one register
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool chunk_wait(unsigned long long *b, uint32_t parity, volatile int *abort_flag, int32_t *err) {
+    if (mbar_try(b, parity)) return true;
+    if (*abort_flag == 1) return false;
+    uint32_t t0 = gtimer_lo();
+    while (true) {
+        if (mbar_try(b, parity)) return true;
+        const int f = *abort_flag;
+        if (f == 1) return false;
+        if (f == kRowsAgain) t0 = gtimer_lo();
+        if (gtimer_lo() - t0 > static_cast<uint32_t>(kWaitBudgetNs)) {
+            *abort_flag = 1;
+            flag_error(err, MINF_ERRBIT_TIMEOUT);
+            return false;
+        }
+    }
+}
+// One thread says so around the rows (it leaves the flag of a wait that has run out as it is).
+__device__ __forceinline__ void rows_again(int *abort_flag, bool on) {
+    atomicCAS(abort_flag, on ? 0 : kRowsAgain, on ? kRowsAgain : 0);
 }
 
 // The stretches that share the segment's item (only of a segment that is not a whole item).

@@ -69,23 +69,28 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
         l = l * corr + sum;
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] *= corr;
-        for (unsigned left = __ballot_sync(0xffffffffu, row >= 0); left; left &= left - 1) {
-            const int b = __ffs(left) - 1;
-            const float pb = __shfl_sync(0xffffffffu, pr, b);
-            const long long rb = __shfl_sync(0xffffffffu, row, b);
-            if (lane < D4) {
-                if constexpr (PER == 4) {
-                    const float4 v = row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + lane);
-                    acc[0] = fmaf(pb, v.x, acc[0]);
-                    acc[1] = fmaf(pb, v.y, acc[1]);
-                    acc[2] = fmaf(pb, v.z, acc[2]);
-                    acc[3] = fmaf(pb, v.w, acc[3]);
-                }
+        if (!__any_sync(0xffffffffu, row >= 0)) continue;
+        for (int b0 = 0; b0 < 32; b0 += 4) {  // four rows' loads in flight
+            float4 v[4];
+            float pb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long rb = __shfl_sync(0xffffffffu, row, b0 + i);
+                pb[i] = __shfl_sync(0xffffffffu, pr, b0 + i);
+                if (rb < 0) pb[i] = 0.0f;  // (a missing block's row counts in l)
+                v[i] = rb >= 0 ? row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + lane * PER / 4) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if constexpr (PER == 2) {
-                const float4 v = row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + (lane >> 1));
-                acc[0] = fmaf(pb, lane & 1 ? v.z : v.x, acc[0]);
-                acc[1] = fmaf(pb, lane & 1 ? v.w : v.y, acc[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (PER == 4) {
+                    acc[0] = fmaf(pb[i], v[i].x, acc[0]);
+                    acc[1] = fmaf(pb[i], v[i].y, acc[1]);
+                    acc[2] = fmaf(pb[i], v[i].z, acc[2]);
+                    acc[3] = fmaf(pb[i], v[i].w, acc[3]);
+                } else {
+                    acc[0] = fmaf(pb[i], lane & 1 ? v[i].z : v[i].x, acc[0]);
+                    acc[1] = fmaf(pb[i], lane & 1 ? v[i].w : v[i].y, acc[1]);
+                }
             }
         }
     }

@@ -34,7 +34,7 @@ namespace minf {
 namespace {
 
 constexpr int KT = 64;              // keys of a tile
-constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^15
+constexpr float kShift = 12.0f, kSlack = 3.0f;  // P is at most 2^15 (as in minf_chunk_tiles.cu)
 
 template <int HD, typename T, int NT>
 struct Cfg {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void produce(unsigned char *ring, Meta &mt, const Map
         if (more) look_up();
         const int key = piece * p.box_rows;
         const int r0 = __shfl_sync(0xffffffffu, row[0], key & 31), r1 = __shfl_sync(0xffffffffu, row[1], key & 31);
-        if (n >= C::NS && !__all_sync(0xffffffffu, mbar_wait(&mt.empty[st], ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
+        if (n >= C::NS && !__all_sync(0xffffffffu, chunk_wait(&mt.empty[st], ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
         if (lane == 0) mbar_expect_tx(&mt.full[st], 2 * C::kTile);
         __syncwarp();
         unsigned char *stage = ring + st * C::kStage;
@@ -348,7 +348,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
             if (q % C::G != grp) continue;
             const int st = q % C::NS, j0 = unit_tile(w.keys, w.u0 + i) * KT + key0;
             unsigned char *kst = smem + st * C::kStage, *vst = kst + C::kTile;
-            mbar_wait(&mt.full[st], (q / C::NS) & 1, abort_flag, p.a.err);
+            chunk_wait(&mt.full[st], (q / C::NS) & 1, abort_flag, p.a.err);
             if (item_sees_some(w.keys, j0, 16)) {
                 const bool edge = j0 < w.keys.lo || j0 + 16 > w.keys.hi;
                 if (!C::Q && edge) {
@@ -724,6 +724,7 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                 join_all();
             }
         }
+        bool again = false;
         if (finish) {
             bool odd = false;
 #pragma unroll
@@ -746,7 +747,9 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     odd |= bad;
                 }
             // rows that are not finite: by the definition, a row a warp
-            if (!named_all(1, C::kComputeThreads, !odd))
+            again = !named_all(1, C::kComputeThreads, !odd);
+            if (again) {
+                if (tid == 0) rows_again(&mt.abort_flag, true);
                 for (int r = warp; r < rows; r += kWarps) {
                     if (!mt.odd[r]) continue;
                     RowJob job;
@@ -758,8 +761,10 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                     job.hk = w.head;
                     attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
                 }
+            }
         }
         named_sync(1, C::kComputeThreads);  // Q, limits and the join buffer are free
+        if (again && tid == 0) rows_again(&mt.abort_flag, false);
     }
 }
 
@@ -791,7 +796,7 @@ __global__ void __launch_bounds__(Cfg<HD, T, NT>::kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
         if (warp < C::kWarps + C::kProducers) produce<HD, T, NT>(smem, mt, maps, p, warp - C::kWarps, ctas);
     }
-    if (*static_cast<volatile int *>(&mt.abort_flag)) {
+    if (*static_cast<volatile int *>(&mt.abort_flag) == 1) {
         // a wait ran out: let copies in flight land before shared memory goes away
         const unsigned long long t0 = gtimer();
         while (gtimer() - t0 < kWaitBudgetNs / 4) {

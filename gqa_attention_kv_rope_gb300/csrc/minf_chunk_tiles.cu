@@ -13,7 +13,7 @@
 // 97 clocks of its bandwidth, against 64 of tensor work with one of them in TMEM.
 // S of the next tile runs while the row threads work on this one; the tile after next goes into the
 // buffer that P V has just finished with.  O is rescaled only when a row's maximum has grown by
-// more than 2^8 since the last time (P is then at most 2^15, still a binary16 value, and the rescale
+// more than 2^3 since the last time (P is then at most 2^15, still a binary16 value, and the rescale
 // is a rare pass over O instead of one a tile).
 //
 // Precision: fp32 results from binary16 products.  Every operand that is not exactly binary16 is
@@ -54,7 +54,10 @@ constexpr int BM = 128, KT = 128;
 constexpr int kSplitWarps = 4, kSplitRows = KT / kSplitWarps;  // for K and for V each; rows of a tile a warp takes
 // The warps after the row threads': S, K copies (or rows resolved), P V, V copies (or Q rows)
 constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
-constexpr float kShift = 7.0f, kSlack = 8.0f;  // P is at most 2^(shift + slack) = 2^15
+// P is at most 2^(shift + slack) = 2^15, and lo keeps it to 2^-25: n keys that all lose as much are off by
+// n 2^-25 of a sum of at least 2^shift (2^-20 for 2^17 of them).  A rescale comes when a row's scores grow by
+// a factor of 2^slack.
+constexpr float kShift = 12.0f, kSlack = 3.0f;
 // TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
 // column)
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kTmemCols = 512;
@@ -234,7 +237,7 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     for (bool more = walk_begin<KT>(w, p, ctas); more; more = walk_next<KT>(w, p), ++seg) {
         if constexpr (kV) {
             // (the last item's rows were taken when it began, tiles ago)
-            if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
+            if (seg > 0 && !__all_sync(0xffffffffu, chunk_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
             copy_q_rows<HD, T>(sm, p, w);
         }
         for (int u = w.u0; u < w.u1; ++u, ++n) {
@@ -251,7 +254,7 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
                     row = p.a.c.rows;
                 }
             }
-            if (n >= C::NS && !__all_sync(0xffffffffu, mbar_wait(empty, ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
+            if (n >= C::NS && !__all_sync(0xffffffffu, chunk_wait(empty, ((n / C::NS) - 1) & 1, abort_flag, p.a.err))) return;
             if (lane == 0) mbar_expect_tx(full, kTileBytes);
             __syncwarp();
             if (lane < copies)
@@ -282,7 +285,7 @@ __device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, int
     Walk w;
     int seg = 0;
     for (bool more = walk_begin<KT>(w, p, ctas); more; more = walk_next<KT>(w, p), ++seg) {
-        if (seg > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
+        if (seg > 0 && !__all_sync(0xffffffffu, chunk_wait(&sm.q_free, (seg - 1) & 1, abort_flag, p.a.err))) return;
         copy_q_rows<HD, T>(sm, p, w);
     }
 }
@@ -441,7 +444,7 @@ __device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &
     int u = more ? w.u0 : 0;
     for (bool on = more; on; ++n) {
         const int slot = n & 3;
-        if (n >= 4 && !__all_sync(0xffffffffu, mbar_wait(&sm.row_free[slot], ((n >> 2) - 1) & 1, abort_flag, p.a.err))) return;
+        if (n >= 4 && !__all_sync(0xffffffffu, chunk_wait(&sm.row_free[slot], ((n >> 2) - 1) & 1, abort_flag, p.a.err))) return;
         on = more;
         if (on) {
             const int j0 = unit_tile(w.keys, u) * KT + lane;
@@ -482,7 +485,7 @@ __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p
     // The rows of tile n; false once a wait has run out.
     auto take_rows = [&](int n) -> bool {
         const int slot = n & 3;
-        const bool ok = mbar_wait(&sm.row_full[slot], (n >> 2) & 1, abort_flag, p.a.err);
+        const bool ok = chunk_wait(&sm.row_full[slot], (n >> 2) & 1, abort_flag, p.a.err);
         head = ok ? sm.row_head[slot] : -1;
         row = head < 0 ? -1 : sm.rows[slot][my_row];
         __syncwarp();
@@ -571,7 +574,7 @@ __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p
             }
         }
         auto wait_empty = [&]() {  // (one that runs out shows in the next take_rows)
-            if (n >= C::NS) mbar_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], phase, abort_flag, p.a.err);
+            if (n >= C::NS) chunk_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], phase, abort_flag, p.a.err);
             __syncwarp();
         };
         if constexpr (Q) {
@@ -634,14 +637,14 @@ __device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, uint32_t tmem, int
     const uint64_t dk = desc128(su32(sm.k), 16);
     const uint32_t qh = tmem + kColQ, ql = qh + HD / 2;
     for (int n = 0, seg = 0;; ++seg) {
-        if (!mbar_wait(&sm.q_full, seg & 1, abort_flag, err)) return;
+        if (!chunk_wait(&sm.q_full, seg & 1, abort_flag, err)) return;
         const int tiles = *static_cast<volatile int *>(&sm.seg_tiles);
         if (tiles == 0) return;
         for (int i = 0; i < tiles; ++i, ++n) {
             const int st = n % C::NS;
-            if (!mbar_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, err)) return;
+            if (!chunk_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, err)) return;
             // this buffer's last P: its product must be done (the item's first two tiles: with the last item)
-            if (i >= 2 && !mbar_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, err)) return;
+            if (i >= 2 && !chunk_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, err)) return;
             tc_after();
             const uint32_t d = tmem + kColS + static_cast<uint32_t>(n & 1) * KT;
             const uint64_t k0 = dk + st * D::kStage;
@@ -671,9 +674,9 @@ __device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int
     const uint64_t dv = desc128(su32(sm.v), D::kSlab);
     for (int n = 0;; ++n) {
         const int st = n % C::NS;
-        if (!mbar_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
+        if (!chunk_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
         const int flag = *static_cast<volatile int *>(&sm.p_flag[n & 1]);
-        if (!mbar_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
+        if (!chunk_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
         tc_after();
         const uint64_t v0 = dv + st * D::kStage;
         const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
@@ -712,7 +715,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         // this half row of Q, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
         float c;
         {
-            mbar_wait(&sm.q_in, seg & 1, abort_flag, err);
+            chunk_wait(&sm.q_in, seg & 1, abort_flag, err);
             float4 x[DIMS / 4];
             float am = 0.0f;
 #pragma unroll
@@ -731,8 +734,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             const int sh = row_shift(am, 126);
             const float f = p.scale_log2 < 0.0f ? -pow2i(sh) : pow2i(sh);
             // S * c is the score in powers of two, c > 0: a row's largest S is its largest score (the sign of
-            // the caller's scale is Q's; a scale of zero is one too small to matter)
-            c = fmaxf(fabsf(p.scale_log2) * pow2i(-sh), 1e-38f);
+            // the caller's scale is Q's; a scale of zero is the smallest one, so that hidden keys' -infinity stays)
+            c = fabsf(p.scale_log2) * pow2i(-sh);
+            if (c == 0.0f) c = __uint_as_float(1u);
             constexpr int QD = DIMS < 32 ? DIMS : 32;  // dims of a store: half as many columns
 #pragma unroll
             for (int d0 = 0; d0 < DIMS / 4; d0 += QD / 4) {
@@ -767,7 +771,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         float m = -INFINITY, l = 0.0f;
         for (int i = 0; i < tiles; ++i) {
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
-            mbar_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
+            chunk_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
             tc_after();
             if (!warp_live) {
                 named_sync(1, C::kRowThreads);
@@ -778,8 +782,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 float cc = c, ve = 0.0f, vi = 1.0f;
                 bool k_rows = false, v_rows = false;
                 if constexpr (C::HL) {
-                    mbar_wait(&sm.k_stat[q & 3], (q >> 2) & 1, abort_flag, err);
-                    mbar_wait(&sm.v_stat[q & 3], (q >> 2) & 1, abort_flag, err);
+                    chunk_wait(&sm.k_stat[q & 3], (q >> 2) & 1, abort_flag, err);
+                    chunk_wait(&sm.v_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     const auto fk = sm.k_tile[q & 3], fv = sm.v_tile[q & 3];
                     k_rows = fk.by_row, v_rows = fv.by_row;
                     cc = c * fk.fac;  // (1, 0 and 1 where they are row by row)
@@ -847,7 +851,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     m = mn;
                 }
                 if (i > 0 && __any_sync(0xffffffffu, grow)) {
-                    mbar_wait(&sm.o_done[(q - 1) & 1], ((q - 1) >> 1) & 1, abort_flag, err);
+                    chunk_wait(&sm.o_done[(q - 1) & 1], ((q - 1) >> 1) & 1, abort_flag, err);
                     tc_after();
 #pragma unroll 1
                     for (int d = 0; d < DIMS; d += 16) {
@@ -892,7 +896,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             }
             if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
                 // rows of this tile that no token sees: V must hold zeros there
-                mbar_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
+                chunk_wait(&sm.v_full[q % C::NS], (q / C::NS) & 1, abort_flag, err);
                 if (part == 0 && !item_sees(w.keys, j0 + row)) {
 #pragma unroll
                     for (int s = 0; s < C::SLABS; ++s)
@@ -908,7 +912,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
         }
         n += tiles;
-        mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, err);
+        chunk_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, err);
         tc_after();
         sm.sum[part][row] = l;
         named_sync(1, C::kRowThreads);
@@ -935,7 +939,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             }
             named_sync(1, C::kRowThreads);
         };
-        bool finish = whole, odd = false;
+        bool finish = whole, odd = false, again = false;
         if (whole) {
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll 1
@@ -1028,7 +1032,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             odd = odd && live;
             if (odd) sm.odd[row] = 1;
             // rows that are not finite: by the definition, a row a warp
-            if (!named_all(1, C::kRowThreads, !odd))
+            again = !named_all(1, C::kRowThreads, !odd);
+            if (again) {
+                if (tid == 0) rows_again(&sm.abort_flag, true);
                 for (int r = warp; r < rows; r += C::kRowWarps) {
                     if (!sm.odd[r]) continue;
                     RowJob job;
@@ -1040,9 +1046,11 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     job.hk = w.head;
                     attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
                 }
+            }
         }
         tc_before();
         named_sync(1, C::kRowThreads);  // sm.odd and sm.sum are free for the next segment
+        if (again && tid == 0) rows_again(&sm.abort_flag, false);
     }
     if (tid == 0) sm.seg_tiles = 0;
     __syncwarp();
@@ -1133,7 +1141,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     __syncthreads();
     tc_after();
     if (warp == C::kRowWarps + kScoreWarp) {
-        if (*static_cast<volatile int *>(&sm.abort_flag)) {
+        if (*static_cast<volatile int *>(&sm.abort_flag) == 1) {
             // a wait ran out: let copies and MMAs in flight finish before TMEM and shared memory go away
             const unsigned long long t0 = gtimer();
             while (gtimer() - t0 < kWaitBudgetNs / 4) {

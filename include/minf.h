@@ -604,7 +604,7 @@ MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f1
  * the sequence that stay visible beside the window (n_sink 0: none; without a window it changes
  * nothing).  A token that sees nothing (p < 0) gets zeros.  Values in rows that a token does not
  * see, infinities and NaN among them, do not reach its result.  The new tokens' own rows must
- * have been stored.  q [nt, n_head, hd] is rotated; out [nt, n_head*hd_kv].
+ * have been stored.  q [nt, n_head, hd] is rotated; out [nt, n_head*hd_kv], which must not overlap q.
  * minf_gqa_attn_chunk_paged reads paged pools; minf_gqa_attn_window reads contiguous regions:
  * sequence s has rows seq_row_off[s] .. + seq_cap[s] of the arena [arena_rows, W], as for
  * minf_gqa_attn_decode (seq_row_off NULL: one sequence, the regions' max_cap rows; seq_cap NULL:
@@ -615,12 +615,13 @@ MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f1
  * 16-byte aligned.  Its contents need no preparation and no call leaves anything in it for the
  * next, so calls of any shape may share it one after the other; two calls that run concurrently
  * must not.
- * Sums and softmax statistics are fp32; products run on the tensor cores with operands split
- * into halves whose sum carries 22 bits or more.
+ * Sums and softmax statistics are fp32; products run on the tensor cores with operands split into
+ * halves whose sum carries 22 bits or more (softmax weights below 2^-15 of a row's largest: 2^-37 of it).
+ * A row that sees an infinity or a NaN is computed again key by key: right, but slow.
  * Device errors: MINF_ERRBIT_ATTN_POS (p < 0, or p >= cap: the window is clamped to cap), _BLOCK
  * (a visible row's block is missing: read as zeros), _CHUNK (nothing written), _TIMEOUT.
  * Errors: as minf_gqa_attn_decode; MINF_ERR_ARG for window < 0, n_sink < 0, max_chunk <= 0,
- * chunk_off NULL with nt != n_seq, seq_row_off NULL with n_seq > 1; MINF_ERR_WORKSPACE.
+ * chunk_off NULL with nt != n_seq, seq_row_off NULL with n_seq > 1, out overlapping q; MINF_ERR_WORKSPACE.
  */
 MINF_API size_t minf_attn_chunk_workspace_bytes(int nt, int n_seq, int n_head, int n_kv_head, int hd_kv, int max_chunk);
 MINF_API int minf_gqa_attn_chunk_paged(float *out, const float *q, const float *k_pool, const float *v_pool, int64_t pool_rows,

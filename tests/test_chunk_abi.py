@@ -120,3 +120,11 @@ def test_workspace_sizes(lib):
     f = lib.minf_attn_chunk_workspace_bytes
     assert f(0, 1, 14, 2, 64, 1) == 0 and f(4, 1, 15, 2, 64, 1) == 0 and f(4, 1, 14, 2, 96, 1) == 0
     assert f(1, 1, 14, 2, 64, 1) >= 256 and f(5000, 64, 16, 8, 128, 4096) >= 256
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("at", [0, 16, 8 * 14 * 64 * 4 - 16, -8 * 14 * 64 * 4 + 16])
+def test_out_may_not_overlap_q(lib, end, at):
+    q = 1 << 20
+    for f, args in (("minf_gqa_attn_chunk_paged", attn_args), ("minf_gqa_attn_window", window_args)):
+        assert getattr(lib, f + end)(*args(q=P(q), out=P(q + at))) == 1

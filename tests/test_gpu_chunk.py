@@ -467,6 +467,82 @@ def test_regions_of_one_sequence(m):
     assert err.item() == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("long", [0, 25])
+def test_many_sequences(m, kind, long):
+    # more sequences than the plan has threads, and than it holds in shared memory; some without tokens
+    r = rng(30, long)
+    new = r.integers(0, 3, 1300)
+    new[[3, 600, 1299]] = max(2, long)
+    check(m, Batch((8, 1, 64, 64), kind, new.tolist(), r.integers(0, 150, 1300).tolist(), paged=True, block=16, seed=30))
+
+
+def test_many_token_tiles(m):
+    # more token tiles than the plan holds in shared memory
+    check(m, Batch((8, 1, 64, 64), "f16", [18000], [5], paged=False, seed=31, window=24, sinks=2))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new", [[20, 1], [3]])
+def test_rows_of_one_tile_far_apart(m, kind, new):
+    # rows whose magnitudes differ by up to 2^24 in one tile of keys, and blocks that differ in one row;
+    # an output is off by no more than 1e-5 of the largest value that it could have been
+    b = Batch((16, 8, 128, 128), kind, new, [300, 77][:len(new)], paged=True, block=16, seed=32)
+    mag_k, mag_v = (np.exp2(rng(32, k).integers(-12, 13, (b.pool_rows, 1))).astype(np.float32) for k in (1, 2))
+    x, y = (rng(32, k).standard_normal((b.pool_rows, b.w)).astype(np.float32) for k in (3, 4))
+    y[:, ::64] *= np.float32(2.0 ** -8)
+    b.k, b.v = hold(x * mag_k, kind), hold(y * mag_v, kind)
+    b.q = b.q * np.float32(2.0 ** -12)
+    got, err = b.run(m)
+    assert np.abs(got - b.ref()).max() <= 1e-5 * 5 * 2.0 ** 12 and err == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new", [[1], [32]])
+@pytest.mark.parametrize("gap", [13, 17, 20])
+def test_many_small_weights_beside_a_large_one(m, kind, new, gap):
+    # row 0 weighs 2^gap times any other row.  60032 weights that are each off by 2^-37 of the largest, in the
+    # numerator and (not rounded) the sum: 4.4e-7; a stretch of at most 4 tiles adds 4 * 16 products' sums
+    # a row, each off by 2^-23 of it: 7.6e-6.  Together below 1e-5.
+    nk, hd, past = 1, 64, 60000
+    b = Batch((4, nk, hd, hd), kind, new, [past], paged=False, seed=33)
+    k, v = np.zeros((b.pool_rows, b.w), np.float32), np.ones((b.pool_rows, b.w), np.float32)
+    row = b.row(0, 0)
+    k[row, 0], v[row] = gap * np.log(2.0), -1.0
+    b.k, b.v = hold(k, kind), hold(v, kind)
+    b.q[:] = 0.0
+    b.q[:, :, 0] = 1.0
+    got, err = b.run(m, scale=1.0)
+    assert np.abs(got - b.ref()).max() <= 1e-5 and err == 0
+
+
+def test_scale_that_is_not_a_number(m):
+    for new in ([20], [1]):
+        b = Batch((14, 2, 64, 64), "f16", new, [70], paged=True, seed=34)
+        got, err = b.run(m, scale=float("nan"))
+        assert np.isnan(got).all() and err == 0
+
+
+def test_rows_that_take_long_do_not_run_out_of_time(m):
+    # an infinity that every token sees: all rows are computed again key by key, far beyond a wait's limit
+    nh, hd, new, past = 8, 64, 4864, 80000
+    cap = new + past
+    k, v = (torch.randn(cap, hd, device="cuda", generator=torch.Generator("cuda").manual_seed(s)).half() for s in (1, 2))
+    v[0, 0] = float("inf")
+    q = torch.randn(new, nh, hd, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    out, err = torch.empty(new, nh * hd, device="cuda"), i32([0])
+    ws = m.kv.chunk_workspace(new, 1, nh, 1, hd, new)
+    m.minf_gqa_attn_window_f16(out, q, k, v, None, None, cap, i32([0, new]), i32([past]), new, nh, 1, hd, hd, hd ** -0.5, 0,
+                               0, ws, err)
+    assert err.item() == 0
+    out = out.view(new, nh, hd)
+    assert torch.isinf(out[:, :, 0]).all() and torch.isfinite(out[:, :, 1:]).all()
+    for t in (0, 777, new - 1):
+        s = (q[t].double() @ k[:past + t + 1].double().T) * hd ** -0.5
+        ref = torch.softmax(s, -1) @ v[:past + t + 1, 1:].double()
+        close(out[t, :, 1:].cpu().numpy(), ref.cpu().numpy())
+
+
 # ----------------------------------------------------------------------------- rotation
 def ref_rope(x, pos, axis, hd, style):
     """x [nt, heads, hd], pos [n_axis, nt]: (rotated, |a| + |b| of each value's pair), in 64 bits."""
