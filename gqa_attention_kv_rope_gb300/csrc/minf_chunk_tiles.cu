@@ -135,13 +135,17 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+// The whole warp comes here with the same operands and its leader issues: operands that the compiler knows
+// to be the warp's own stay in uniform registers (from one lane's registers each one is moved there first).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p, l;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 l, %5, 0;\n @l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(leader)
                  : "memory");
 }
-__device__ __forceinline__ void commit(unsigned long long *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t leader, unsigned long long *bar) {
+    asm volatile("{\n .reg .pred l;\n setp.ne.b32 l, %1, 0;\n @l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(su32(bar)),
+                 "r"(leader)
+                 : "memory");
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -628,6 +632,11 @@ struct Desc {
     static constexpr uint64_t kStage = C::TERMS * kTerm;
 };
 
+// chunk_wait by a warp, whose lanes go on or leave together.
+__device__ __forceinline__ bool all_wait(unsigned long long *b, uint32_t parity, volatile int *abort_flag, int32_t *err) {
+    return __all_sync(0xffffffffu, chunk_wait(b, parity, abort_flag, err));
+}
+
 template <int HD, typename T>
 __device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, uint32_t tmem, int32_t *err) {
     using C = Cfg<HD, T>;
@@ -636,15 +645,16 @@ __device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, uint32_t tmem, int
     constexpr uint32_t kId = idesc_f16(BM, KT, false);
     const uint64_t dk = desc128(su32(sm.k), 16);
     const uint32_t qh = tmem + kColQ, ql = qh + HD / 2;
+    const uint32_t leader = (threadIdx.x & 31) == 0;
     for (int n = 0, seg = 0;; ++seg) {
-        if (!chunk_wait(&sm.q_full, seg & 1, abort_flag, err)) return;
-        const int tiles = *static_cast<volatile int *>(&sm.seg_tiles);
+        if (!all_wait(&sm.q_full, seg & 1, abort_flag, err)) return;
+        const int tiles = __shfl_sync(0xffffffffu, *static_cast<volatile int *>(&sm.seg_tiles), 0);
         if (tiles == 0) return;
         for (int i = 0; i < tiles; ++i, ++n) {
             const int st = n % C::NS;
-            if (!chunk_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, err)) return;
+            if (!all_wait(&sm.k_full[st], (n / C::NS) & 1, abort_flag, err)) return;
             // this buffer's last P: its product must be done (the item's first two tiles: with the last item)
-            if (i >= 2 && !chunk_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, err)) return;
+            if (i >= 2 && !all_wait(&sm.o_done[n & 1], ((n - 2) >> 1) & 1, abort_flag, err)) return;
             tc_after();
             const uint32_t d = tmem + kColS + static_cast<uint32_t>(n & 1) * KT;
             const uint64_t k0 = dk + st * D::kStage;
@@ -654,13 +664,13 @@ __device__ __forceinline__ void issue_scores(Smem<HD, T> &sm, uint32_t tmem, int
                 const uint64_t ks = k0 + s * (D::kSlab >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    mma_ts(d, qh + s * 32 + kk * 8, ks + 2 * kk, kId, s > 0 || kk > 0);
-                    mma_ts(d, ql + s * 32 + kk * 8, ks + 2 * kk, kId, true);
-                    if constexpr (C::HL) mma_ts(d, qh + s * 32 + kk * 8, ks + D::kTerm + 2 * kk, kId, true);
+                    mma_ts(leader, d, qh + s * 32 + kk * 8, ks + 2 * kk, kId, s > 0 || kk > 0);
+                    mma_ts(leader, d, ql + s * 32 + kk * 8, ks + 2 * kk, kId, true);
+                    if constexpr (C::HL) mma_ts(leader, d, qh + s * 32 + kk * 8, ks + D::kTerm + 2 * kk, kId, true);
                 }
             }
-            commit(&sm.s_full[n & 1]);
-            commit(&sm.k_empty[st]);
+            commit(leader, &sm.s_full[n & 1]);
+            commit(leader, &sm.k_empty[st]);
         }
     }
 }
@@ -672,23 +682,24 @@ __device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int
     volatile int *abort_flag = &sm.abort_flag;
     constexpr uint32_t kId = idesc_f16(BM, HD, true);
     const uint64_t dv = desc128(su32(sm.v), D::kSlab);
+    const uint32_t leader = (threadIdx.x & 31) == 0;
     for (int n = 0;; ++n) {
         const int st = n % C::NS;
-        if (!chunk_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
-        const int flag = *static_cast<volatile int *>(&sm.p_flag[n & 1]);
-        if (!chunk_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
+        if (!all_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
+        const int flag = __shfl_sync(0xffffffffu, *static_cast<volatile int *>(&sm.p_flag[n & 1]), 0);
+        if (!all_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
         tc_after();
         const uint64_t v0 = dv + st * D::kStage;
         const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
 #pragma unroll 4
         for (int kk = 0; kk < KT / 16; ++kk) {
             const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
-            mma_ts(tmem + kColO, ph + kk * 8, v0 + o, kId, !(flag & 1) || kk > 0);
-            mma_ts(tmem + kColO, pl + kk * 8, v0 + o, kId, true);
-            if constexpr (C::HL) mma_ts(tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
+            mma_ts(leader, tmem + kColO, ph + kk * 8, v0 + o, kId, !(flag & 1) || kk > 0);
+            mma_ts(leader, tmem + kColO, pl + kk * 8, v0 + o, kId, true);
+            if constexpr (C::HL) mma_ts(leader, tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
         }
-        commit(&sm.o_done[n & 1]);
-        commit(&sm.v_empty[st]);
+        commit(leader, &sm.o_done[n & 1]);
+        commit(leader, &sm.v_empty[st]);
         if (flag & 2) return;
     }
 }
@@ -1113,11 +1124,9 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
     } else if (!C::HL || warp < C::kRowWarps + 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
         if (warp == C::kRowWarps + kScoreWarp) {
-            if (lane == 0 && !idle) issue_scores<HD, T>(sm, tmem, p.a.err);
-            __syncwarp();
+            if (!idle) issue_scores<HD, T>(sm, __shfl_sync(0xffffffffu, tmem, 0), p.a.err);
         } else if (role == kValueWarp) {
-            if (lane == 0 && !idle) issue_values<HD, T>(sm, tmem, p.a.err);
-            __syncwarp();
+            if (!idle) issue_values<HD, T>(sm, __shfl_sync(0xffffffffu, tmem, 0), p.a.err);
         } else if constexpr (C::HL) {
             if (role == kQueryWarp)
                 copy_q<HD, T>(sm, p, ctas);
