@@ -51,7 +51,7 @@ namespace minf {
 namespace {
 
 constexpr int BM = 128, KT = 128;
-constexpr int kSplitWarps = 4, kSplitRows = KT / kSplitWarps;  // for K and for V each; rows of a tile a warp takes
+constexpr int kSplitWarps = 8, kSplitRows = KT / kSplitWarps;  // rows of K and of V of a tile a warp takes
 // The warps after the row threads': S, K copies (or rows resolved), P V, V copies (or Q rows)
 constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
 // P is at most 2^(shift + slack) = 2^15, and lo keeps it to 2^-25: n keys that all lose as much are off by
@@ -346,8 +346,8 @@ struct SplitQ8 {
     }
     // hi is the rounded product of a scaled scale and a quant, two binary16 values; the rest, at most 7 bits,
     // comes exactly out of a fused multiply-add.
-    // d: this lane's row's scales, scaled.
-    __device__ __forceinline__ void put(uint32_t hi0, uint32_t lo0, uint2 d, int warp, int sub, int l8) {
+    // d: the scaled scales, of row r in lane lane0 + r.
+    __device__ __forceinline__ void put(uint32_t hi0, uint32_t lo0, uint2 d, int lane0, int warp, int sub, int l8) {
         // where the lane's chunks go in even and odd steps (four rows on, the swizzle differs in one bit)
         uint32_t at[2][CH];
 #pragma unroll
@@ -358,10 +358,10 @@ struct SplitQ8 {
         }
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-            uint32_t dd = __shfl_sync(0xffffffffu, d.x, 4 * i + sub);
+            uint32_t dd = __shfl_sync(0xffffffffu, d.x, lane0 + 4 * i + sub);
             int b = l8 * VPL / 32;  // the lane's block of the row
             if constexpr (HD == 128) {
-                const uint32_t dy = __shfl_sync(0xffffffffu, d.y, 4 * i + sub);
+                const uint32_t dy = __shfl_sync(0xffffffffu, d.y, lane0 + 4 * i + sub);
                 dd = b & 2 ? dy : dd;
             }
             dd = __byte_perm(dd, dd, b & 1 ? 0x3232 : 0x1010);
@@ -473,17 +473,19 @@ __device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &
     }
 }
 
-template <int HD, typename T, bool kV>
+// The splitting warps take K and V of a tile in turn, 16 rows each: K of the next tile while P V runs, V while
+// S does.  (Four warps for K and four for V took twice as long over a product's operand, with the tensor cores
+// waiting for it.)  Lanes 0-15 hold what belongs to the warp's K rows, lanes 16-31 to its V rows.
+template <int HD, typename T>
 __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p, int warp) {
     using C = Cfg<HD, T>;
     constexpr bool Q = std::is_same<T, Q8>::value;
-    constexpr int kMostShift = kV ? 60 : 126;
-    const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
-    const int my_row = warp * kSplitRows + lane;
+    const int lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3, kv = lane >> 4;
+    const int my_row = warp * kSplitRows + (lane & 15);
     const ChunkKv &c = p.a.c;
-    const void *pool = kV ? c.v : c.k;
+    const void *pool = kv ? c.v : c.k;
     volatile int *abort_flag = &sm.abort_flag;
-    std::conditional_t<Q, SplitQ8<HD>, SplitF32<HD>> sp;
+    std::conditional_t<Q, SplitQ8<HD>, SplitF32<HD>> sk, sv;
     uint2 scales = make_uint2(0, 0);
     int row = -1, head = -1;  // the rows taken last
     // The rows of tile n; false once a wait has run out.
@@ -495,7 +497,7 @@ __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.row_free[slot]);
         if constexpr (Q) {
-            scales = sp.load_scales(pool, c, row, max(head, 0));
+            scales = sk.load_scales(pool, c, row, max(head, 0));
         } else if (row >= 0) {
             const unsigned char *q = static_cast<const unsigned char *>(pool) + row * c.row_bytes + head * (HD * 4);
 #pragma unroll
@@ -503,122 +505,124 @@ __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p
         }
         return ok;
     };
-    // This lane's row's shift in the tile whose rows were taken last, agreed on by the four warps: the tile's
-    // where its rows are within 2^16 of its largest, else the row's own.  False, in all four, once a wait
-    // has run out in one of them: they leave together.
-    auto agree = [&](int slot, bool ok, int &sh, int &by_row) -> bool {
+    // This lane's row's shift in tile n, whose rows were taken last, agreed on by the warps: the tile's where
+    // its rows are within 2^16 of its largest, else the row's own (fp32 K rows: always their own, elsewhere).
+    // False, in all of the warps, once a wait has run out in one of them: they leave together.
+    int sh = 0, by_row = 0;
+    auto agree = [&](int n, bool ok) -> bool {
+        const int slot = n & 3;
         float am = 0.0f;
         if constexpr (Q) {
-            am = sp.most(scales);
+            am = sk.most(scales);
         } else {
 #pragma unroll 1
             for (int r0 = 0; r0 < kSplitRows; r0 += 8) {
-                sp.load(pool, c, row, max(head, 0), r0, sub, l8);
+                sv.load(c.v, c, row, max(head, 0), r0, sub, l8);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float y = __shfl_sync(0xffffffffu, sp.amax(i), (lane & 3) * 8);  // to the row's lane
-                    if ((lane >> 2) == (r0 >> 2) + i) am = y;
+                    const float y = __shfl_sync(0xffffffffu, sv.amax(i), (lane & 3) * 8);  // to the row's lanes
+                    if (((lane & 15) >> 2) == (r0 >> 2) + i) am = y;
                 }
             }
         }
-        sh = row_shift(am, kMostShift);
+        sh = row_shift(am, kv ? 60 : 126);
         const int none = 1 << 20;  // rows of zeros go by whatever the others do
-        const int2 mine = make_int2(__reduce_min_sync(0xffffffffu, am > 0.0f ? sh : none), __reduce_max_sync(0xffffffffu, am > 0.0f ? sh : -none));
-        if (lane == 0) sm.shifts[kV][slot][warp] = mine;
-        if (!named_all(kV ? 3 : 2, kSplitWarps * 32, ok)) return false;
-        int2 all = sm.shifts[kV][slot][0];
+        int least = am > 0.0f ? sh : none, most = am > 0.0f ? sh : -none;
 #pragma unroll
-        for (int k = 1; k < kSplitWarps; ++k) {
-            const int2 o = sm.shifts[kV][slot][k];
-            all = make_int2(min(all.x, o.x), max(all.y, o.y));
+        for (int o = 1; o < 16; o <<= 1) {
+            least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         }
-        by_row = all.y - all.x > 16;  // (no row at all: not row by row)
-        if (!by_row) sh = all.x == none ? 0 : all.x;
-        return true;
-    };
-    auto scaled = [&](int sh) {
-        return make_uint2(SplitQ8<HD>::times(scales.x, pow2i(sh)), SplitQ8<HD>::times(scales.y, pow2i(sh)));
-    };
-    bool ok = take_rows(0);
-    if constexpr (Q) sp.load(pool, c, row, max(head, 0), sub, l8);
-    uint2 d = make_uint2(0, 0), d_next = d;  // Q8_0: the scaled scales
-    int sh = 0, by_row = 0;
-    // V: exponents of tile n out.
-    auto publish = [&](int n) {
-        const int slot = n & 3;
-        if (by_row) sm.v_exp[slot][my_row] = static_cast<float>(-sh);
-        if (by_row || !Q) sm.v_inv[slot][my_row] = pow2i(sh);
-        if (warp == 0 && lane == 0) sm.v_tile[slot] = {by_row ? 0.0f : static_cast<float>(-sh), by_row ? 1.0f : pow2i(sh), by_row};
+        if ((lane & 15) == 0) sm.shifts[kv][slot][warp] = make_int2(least, most);
+        if (!named_all(2, kSplitWarps * 32, ok)) return false;
+#pragma unroll
+        for (int k = 0; k < kSplitWarps; ++k) {
+            const int2 o = sm.shifts[kv][slot][k];
+            least = min(least, o.x);
+            most = max(most, o.y);
+        }
+        by_row = most - least > 16;  // (no row at all: not row by row)
+        if (!by_row) sh = least == none ? 0 : least;
+        if (head < 0) return true;
+        // V's exponents out
+        if (kv) {
+            if (by_row) sm.v_exp[slot][my_row] = static_cast<float>(-sh);
+            if (by_row || !Q) sm.v_inv[slot][my_row] = pow2i(sh);
+            if (warp == 0 && lane == 16) sm.v_tile[slot] = {by_row ? 0.0f : static_cast<float>(-sh), by_row ? 1.0f : pow2i(sh), by_row};
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_stat[slot]);
+        return true;
     };
-    if constexpr (kV) {
-        if (!agree(0, ok, sh, by_row)) return;
-        publish(0);
-        if constexpr (Q) d = scaled(sh);
+    bool ok = take_rows(0);
+    if constexpr (Q) {
+        sk.load(c.k, c, row, max(head, 0), sub, l8);
+        sv.load(c.v, c, row, max(head, 0), sub, l8);
     }
-    for (int n = 0;; ++n) {
-        if constexpr (!kV && Q) {
-            if (!agree(n & 3, ok, sh, by_row)) return;
-            d = scaled(sh);
-        } else if constexpr (!kV) {
-            if (!named_all(2, kSplitWarps * 32, ok)) return;
-        }
-        if (head < 0) return;
-        const int st = n % C::NS, cur = row, cur_head = head, phase = ((n / C::NS) - 1) & 1;
-        const uint32_t hi = su32(kV ? sm.v[st][0][0] : sm.k[st][0][0]), lo = hi + C::SLABS * KT * 128;
-        ok = take_rows(n + 1);
-        if constexpr (kV) {
-            int sh1 = 0, by1 = 0;
-            if (!agree((n + 1) & 3, ok, sh1, by1)) return;
-            if (head >= 0) {
-                sh = sh1, by_row = by1;
-                publish(n + 1);
-                if constexpr (Q) d_next = scaled(sh);
-            }
-        }
-        auto wait_empty = [&]() {  // (one that runs out shows in the next take_rows)
-            if (n >= C::NS) chunk_wait(kV ? &sm.v_empty[st] : &sm.k_empty[st], phase, abort_flag, p.a.err);
-            __syncwarp();
-        };
+    if (!agree(0, ok)) return;
+    for (int n = 0; head >= 0; ++n) {
+        const int st = n % C::NS, slot = n & 3, cur = row, cur_head = head, phase = ((n / C::NS) - 1) & 1;
+        const uint32_t k_hi = su32(sm.k[st][0][0]), v_hi = su32(sm.v[st][0][0]), to_lo = C::SLABS * KT * 128;
+        uint2 d = make_uint2(0, 0);  // Q8_0: the scaled scales
+        if constexpr (Q) d = make_uint2(sk.times(scales.x, pow2i(sh)), sk.times(scales.y, pow2i(sh)));
+        // K
+        ok = true;
         if constexpr (Q) {
-            wait_empty();
-            if constexpr (!kV) {
-                if (by_row) sm.k_fac[n & 3][my_row] = pow2i(-sh);
-                if (warp == 0 && lane == 0) sm.k_tile[n & 3] = {0.0f, by_row ? 1.0f : pow2i(-sh), by_row};
-            }
-            sp.put(hi, lo, d, warp, sub, l8);
+            if (n >= C::NS) ok = chunk_wait(&sm.k_empty[st], phase, abort_flag, p.a.err);
+            __syncwarp();
+            if (!kv && by_row) sm.k_fac[slot][my_row] = pow2i(-sh);
+            if (warp == 0 && lane == 0) sm.k_tile[slot] = {0.0f, by_row ? 1.0f : pow2i(-sh), by_row};
+            sk.put(k_hi, k_hi + to_lo, d, 0, warp, sub, l8);
         } else {
 #pragma unroll 1
             for (int r0 = 0; r0 < kSplitRows; r0 += 8) {
-                sp.load(pool, c, cur, cur_head, r0, sub, l8);
+                sk.load(c.k, c, cur, cur_head, r0, sub, l8);
                 if (r0 == 0) {
-                    wait_empty();
-                    if (!kV && warp == 0 && lane == 0) sm.k_tile[n & 3] = {0.0f, 1.0f, 1};
+                    if (n >= C::NS) ok = chunk_wait(&sm.k_empty[st], phase, abort_flag, p.a.err);
+                    __syncwarp();
+                    if (warp == 0 && lane == 0) sm.k_tile[slot] = {0.0f, 1.0f, 1};
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int r = warp * kSplitRows + r0 + 4 * i + sub;
-                    float f;
-                    if constexpr (kV) {
-                        f = sm.v_inv[n & 3][r];
-                    } else {
-                        const int s = row_shift(sp.amax(i), kMostShift);
-                        if (l8 == 0) sm.k_fac[n & 3][r] = pow2i(-s);
-                        f = pow2i(s);
-                    }
-                    sp.put(hi, lo, i, r, l8, f);
+                    const int r = warp * kSplitRows + r0 + 4 * i + sub, s = row_shift(sk.amax(i), 126);
+                    if (l8 == 0) sm.k_fac[slot][r] = pow2i(-s);
+                    sk.put(k_hi, k_hi + to_lo, i, r, l8, pow2i(s));
                 }
             }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (!kV) mbar_arrive(&sm.k_stat[n & 3]);
-            mbar_arrive(kV ? &sm.v_full[st] : &sm.k_full[st]);
+            mbar_arrive(&sm.k_stat[slot]);
+            mbar_arrive(&sm.k_full[st]);
         }
-        if constexpr (Q) sp.load(pool, c, row, max(head, 0), sub, l8);
-        d = d_next;
+        ok = take_rows(n + 1) && ok;
+        if constexpr (Q) sk.load(c.k, c, row, max(head, 0), sub, l8);
+        // V
+        if constexpr (Q) {
+            if (n >= C::NS) ok = chunk_wait(&sm.v_empty[st], phase, abort_flag, p.a.err) && ok;
+            __syncwarp();
+            sv.put(v_hi, v_hi + to_lo, d, 16, warp, sub, l8);
+        } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < kSplitRows; r0 += 8) {
+                sv.load(c.v, c, cur, cur_head, r0, sub, l8);
+                if (r0 == 0) {
+                    if (n >= C::NS) ok = chunk_wait(&sm.v_empty[st], phase, abort_flag, p.a.err) && ok;
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = warp * kSplitRows + r0 + 4 * i + sub;
+                    sv.put(v_hi, v_hi + to_lo, i, r, l8, sm.v_inv[slot][r]);
+                }
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_full[st]);
+        if constexpr (Q) sv.load(c.v, c, row, max(head, 0), sub, l8);
+        if (!agree(n + 1, ok)) return;
     }
 }
 
@@ -1095,7 +1099,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             mbar_init(&sm.k_stat[i], kSplitWarps);
             mbar_init(&sm.v_stat[i], kSplitWarps);
             mbar_init(&sm.row_full[i], 1);
-            mbar_init(&sm.row_free[i], 2 * kSplitWarps);
+            mbar_init(&sm.row_free[i], kSplitWarps);
         }
         sm.abort_flag = 0;
         mbar_init_fence();
@@ -1139,12 +1143,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
         }
     } else if constexpr (C::HL) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
-        if (idle) {
-        } else if (role < 8) {
-            split_tiles<HD, T, false>(sm, p, role - 4);
-        } else {
-            split_tiles<HD, T, true>(sm, p, role - 8);
-        }
+        if (!idle) split_tiles<HD, T>(sm, p, role - 4);
     }
     tc_before();
     __syncthreads();
