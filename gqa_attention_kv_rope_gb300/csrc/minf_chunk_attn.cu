@@ -36,12 +36,18 @@ int launch_chunk_attn(const ChunkAttnArgs &a, cudaStream_t s) {
     if (a.sq.nt == 0 || a.sq.n_seq == 0) return MINF_OK;
     const Choice c = choose(a.sq.n_seq, a.nh / a.nk, a.max_chunk);
     char *ws = static_cast<char *>(a.ws);
+    Plans plans = {};
+    AttnParams tiles, stream;
+    int n = 0;
     if (c.tiles) {
-        const int st = launch_chunk_tiles(a, ws, c.stream ? c.most + 1 : 1, s);
-        if (st != MINF_OK) return st;
+        plan_chunk_tiles(plans.a[n++], tiles, a, ws, c.stream ? c.most + 1 : 1);
         ws += up256(chunk_tiles_workspace(a.sq.nt, a.sq.n_seq, a.nh, a.nk, a.hd_kv));
     }
-    return c.stream ? launch_chunk_stream(a, ws, c.rows, c.most, s) : MINF_OK;
+    if (c.stream) plan_chunk_stream(plans.a[n++], stream, a, ws, c.rows, c.most);
+    int st = launch_chunk_plan(plans, n, s);
+    if (st == MINF_OK && c.tiles) st = launch_chunk_tiles(tiles, s);
+    if (st == MINF_OK && c.stream) st = launch_chunk_stream(stream, c.rows, s);
+    return st;
 }
 
 }  // namespace minf

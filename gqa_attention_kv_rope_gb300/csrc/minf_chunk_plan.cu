@@ -1,4 +1,4 @@
-// minf_chunk_plan.cu -- the one-block kernel that cuts a chunk attention into stretches.
+// minf_chunk_plan.cu -- the kernel that cuts a chunk attention into stretches, a block a plan.
 #include "minf_chunk_plan.cuh"
 #include "minf_sm103.cuh"
 
@@ -12,7 +12,8 @@ constexpr int kFewTiles = 4;    // token tiles that a sequence's own thread adds
 
 // A thread a sequence (its loads are the only ones that wait on memory), a warp for a sequence of many
 // token tiles; then a thread a stretch looks its start up in the sums.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ Plans plans) {
+    const PlanArgs &a = plans.a[blockIdx.x];
     gdc_launch_dependents();  // the attention kernel sets itself up meanwhile
     __shared__ long long warp_sum[kPlanThreads / 32];
     __shared__ long long held_seq[kHeld + 1], held_tile[kHeld];
@@ -205,8 +206,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 
 }  // namespace
 
-int launch_chunk_plan(const PlanArgs &a, cudaStream_t s) {
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+int launch_chunk_plan(const Plans &p, int n, cudaStream_t s) {
+    plan_kernel<<<n, kPlanThreads, 0, s>>>(p);
     return cudaPeekAtLastError() == cudaSuccess ? MINF_OK : MINF_ERR_CUDA;
 }
 

@@ -9,7 +9,7 @@
 // item that lies in one stretch is finished by its CTA; one that crosses stretches is joined, in order,
 // by the last of its CTAs to finish: two calls with the same inputs add in the same order.
 //
-// The lengths are device data, so the cut is made on the device by a one-block kernel ahead of
+// The lengths are device data, so the cut is made on the device, by a kernel of one block a plan ahead of
 // the attention kernel (which is launched at once and waits for it).  That kernel also checks
 // chunk_off and zeroes the join tickets, so a workspace needs no preparation and carries nothing
 // from one call to the next.
@@ -108,7 +108,11 @@ inline PlanLayout plan_layout(int nt, int n_seq, int tt, int max_ctas, size_t pa
     return l;
 }
 
-int launch_chunk_plan(const PlanArgs &a, cudaStream_t s);
+// The plans of one call: that of the kernel for long chunks and that of the one for few rows, where it runs both.
+struct Plans {
+    PlanArgs a[2];
+};
+int launch_chunk_plan(const Plans &p, int n, cudaStream_t s);
 
 // What both attention kernels are launched with.
 struct AttnParams {
@@ -124,8 +128,9 @@ struct AttnParams {
 };
 
 // Fills the plan's arguments and the kernel's pointers for a workspace laid out as `lay`.
-inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int max_ctas, int min_units, int snap) {
-    PlanArgs pl = {};
+inline void plan_args(PlanArgs &pl, AttnParams &p, const PlanLayout &lay, void *workspace, int max_ctas, int min_units, int snap) {
+    char *ws = static_cast<char *>(workspace);
+    pl = {};
     pl.c = p.a.c;
     pl.sq = p.a.sq;
     pl.nk = p.a.nk;
@@ -148,7 +153,6 @@ inline PlanArgs plan_args(AttnParams &p, const PlanLayout &lay, char *ws, int ma
     p.starts = pl.starts;
     p.tickets = pl.tickets;
     p.parts = reinterpret_cast<float *>(ws + lay.parts);
-    return pl;
 }
 
 // A CTA's way through its stretch, segment by segment: a segment is the stretch's part of one item.

@@ -851,10 +851,9 @@ size_t chunk_stream_workspace(int nt, int n_seq, int nh, int nk, int hd_kv, int 
     return stream_layout(nt, n_seq, nh / nk, hd_kv, row_tiles(rows)).total;
 }
 
-int launch_chunk_stream(const ChunkAttnArgs &a, void *workspace, int rows, int most, cudaStream_t s) {
+void plan_chunk_stream(PlanArgs &plan, AttnParams &p, const ChunkAttnArgs &a, void *workspace, int rows, int most) {
     const int sms = sm_count(), g = a.nh / a.nk, n8 = row_tiles(rows);
-    const PlanLayout lay = stream_layout(a.sq.nt, a.sq.n_seq, g, a.hd_kv, n8);
-    AttnParams p = {};
+    p = {};
     p.a = a;
     p.tt = 8 * n8 / g;
     p.kt = KT;
@@ -862,9 +861,12 @@ int launch_chunk_stream(const ChunkAttnArgs &a, void *workspace, int rows, int m
     p.most = most;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms < kPlanMost ? sms : kPlanMost, 2, 1), s);
-    if (st != MINF_OK) return st;
-    if (a.hd_kv == 64)
+    plan_args(plan, p, stream_layout(a.sq.nt, a.sq.n_seq, g, a.hd_kv, n8), workspace, sms < kPlanMost ? sms : kPlanMost, 2, 1);
+}
+
+int launch_chunk_stream(const AttnParams &p, int rows, cudaStream_t s) {
+    const int sms = sm_count(), n8 = row_tiles(rows);
+    if (p.a.hd_kv == 64)
         return n8 == 1 ? launch_kind<64, 1>(p, sms, s) : n8 == 2 ? launch_kind<64, 2>(p, sms, s) : launch_kind<64, 4>(p, sms, s);
     return n8 == 1 ? launch_kind<128, 1>(p, sms, s) : n8 == 2 ? launch_kind<128, 2>(p, sms, s) : launch_kind<128, 4>(p, sms, s);
 }

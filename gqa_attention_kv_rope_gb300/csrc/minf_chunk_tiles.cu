@@ -1199,10 +1199,9 @@ size_t chunk_tiles_workspace(int nt, int n_seq, int nh, int nk, int hd_kv) {
     return tiles_layout(nt, n_seq, nh, nk, hd_kv).total;
 }
 
-int launch_chunk_tiles(const ChunkAttnArgs &a, void *workspace, int least, cudaStream_t s) {
+void plan_chunk_tiles(PlanArgs &plan, AttnParams &p, const ChunkAttnArgs &a, void *workspace, int least) {
     const int sms = sm_count();
-    const PlanLayout lay = tiles_layout(a.sq.nt, a.sq.n_seq, a.nh, a.nk, a.hd_kv);
-    AttnParams p = {};
+    p = {};
     p.a = a;
     p.tt = BM / (a.nh / a.nk);
     p.kt = KT;
@@ -1210,15 +1209,14 @@ int launch_chunk_tiles(const ChunkAttnArgs &a, void *workspace, int least, cudaS
     p.most = 0x7fffffff;
     p.scale_log2 = a.scale * kLog2e;
     p.box_rows = a.c.table && (1 << a.c.block_shift) < KT ? 1 << a.c.block_shift : KT;
-    const int st = launch_chunk_plan(plan_args(p, lay, static_cast<char *>(workspace), sms < kPlanMost ? sms : kPlanMost, 1, 0), s);
-    if (st != MINF_OK) return st;
-    if (a.hd_kv == 64)
-        return a.c.kv == kKvQ8    ? launch<64, Q8>(p, sms, s)
-               : a.c.kv == kKvF16 ? launch<64, __half>(p, sms, s)
-                                  : launch<64, float>(p, sms, s);
-    return a.c.kv == kKvQ8    ? launch<128, Q8>(p, sms, s)
-           : a.c.kv == kKvF16 ? launch<128, __half>(p, sms, s)
-                              : launch<128, float>(p, sms, s);
+    plan_args(plan, p, tiles_layout(a.sq.nt, a.sq.n_seq, a.nh, a.nk, a.hd_kv), workspace, sms < kPlanMost ? sms : kPlanMost, 1, 0);
+}
+
+int launch_chunk_tiles(const AttnParams &p, cudaStream_t s) {
+    const int sms = sm_count(), kv = p.a.c.kv;
+    if (p.a.hd_kv == 64)
+        return kv == kKvQ8 ? launch<64, Q8>(p, sms, s) : kv == kKvF16 ? launch<64, __half>(p, sms, s) : launch<64, float>(p, sms, s);
+    return kv == kKvQ8 ? launch<128, Q8>(p, sms, s) : kv == kKvF16 ? launch<128, __half>(p, sms, s) : launch<128, float>(p, sms, s);
 }
 
 }  // namespace minf
