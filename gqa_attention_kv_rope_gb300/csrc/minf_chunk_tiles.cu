@@ -28,12 +28,21 @@
 // whole tile (its small rows still have all their 22 bits) and the row threads need no factor a key:
 // those would take half of the shared-memory bandwidth.
 //
-// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues S, warp 10 issues P V (two threads, so
-// that neither's waits hold up the other's products), warp 11 copies the next item's Q rows in; then
-// the producers: for binary16 warps 9 (K) and 11 (V) issue TMA copies straight into the swizzled
-// layout that the tensor cores read, a block or a stretch of rows a copy; otherwise warp 9
-// resolves the tiles' rows ahead, warps 12-15 load, split and write K and warps 16-19 V (K of the next
-// tile while P V runs, V while S does).
+// Roles of a CTA (one an SM): warps 0-7 rows, warp 8 issues S, warp 10 issues P V (two warps, so that
+// neither's waits hold up the other's products: one warp for both measured 1180 us against 1142 on the
+// batch below); then the producers: for binary16 warps 9 (K) and 11 (V and the next item's Q rows) issue TMA
+// copies straight into the swizzled layout that the tensor cores read, a block or a stretch of rows a
+// copy; otherwise warp 9 resolves the tiles' rows ahead, warp 11 copies Q rows, and warps 12-19 load,
+// split and write K and V in turn.
+//
+// What bounds it, on the batch of six ragged prompts of 500 to 2048 tokens over 12000 cached binary16 rows
+// (16 query heads on 8 of 128 dims; 684 GFLOP): 1.10 ms, 622 TFLOP/s, twice that on the tensor cores, whose
+// rate of 1.88 PFLOP/s allows 0.73 ms.  A tile takes 3100 clocks, of which S and P V take 2600 (a
+// 128x128x16 step some 81, as in the library's own products); the rest is the way from P V's end
+// over S of the next tile but one to the row threads, which a third S buffer would hide if TMEM had room
+// for it.  S cut into two halves of 64 keys, so that the first could start earlier, measured 1260 us.
+// Q8_0 and fp32 tiles take 6000 to 8000 clocks, against 3900 of tensor work in three products: the splitting
+// warps write 128 KB of halves a tile, and there is no room for a second stage of them at 128 dims.
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
 // not); rows that only some tokens see can still carry infinities or NaN into the sums of those that
@@ -54,10 +63,9 @@ constexpr int BM = 128, KT = 128;
 constexpr int kSplitWarps = 8, kSplitRows = KT / kSplitWarps;  // rows of K and of V of a tile a warp takes
 // The warps after the row threads': S, K copies (or rows resolved), P V, V copies (or Q rows)
 constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
-// P is at most 2^(shift + slack) = 2^15, and lo keeps it to 2^-25: n keys that all lose as much are off by
-// n 2^-25 of a sum of at least 2^shift (2^-20 for 2^17 of them).  A rescale comes when a row's scores grow by
-// a factor of 2^slack.
-constexpr float kShift = 12.0f, kSlack = 3.0f;
+// P is at most 2^kShift, and lo keeps it to 2^-25: n keys that all lose as much are off by n 2^-25 of a sum of
+// at least 2^kShift (2^-23 for 2^17 of them).
+constexpr float kShift = 15.0f;
 // TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
 // column)
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kTmemCols = 512;
@@ -111,10 +119,9 @@ struct Smem {
     } k_tile[C::HL ? 4 : 1], v_tile[C::HL ? 4 : 1];
     uint32_t tmem_base;
     int abort_flag, last;
-    // the row threads lead the two issuing threads (which would need registers to walk on their own):
-    // tiles of the segment whose Q is ready (0: no more), and of a tile whose P is: 1 the segment's
-    // first, 2 the last of all
-    int seg_tiles, p_flag[2];
+    // the row threads lead the two issuing warps (which would need registers to walk on their own): tiles of
+    // the segment whose Q is ready (0: no more), and whether the tile whose P is ready is the last of all
+    int seg_tiles, p_last[2];
 };
 
 // ----------------------------------------------------------------------------- tensor-core wrappers
@@ -160,14 +167,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t t, uint32_t *u) {
           "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
           "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
           "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-        : "r"(t)
-        : "memory");
-}
-__device__ __forceinline__ void tm_ld16(uint32_t t, uint32_t *u) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(t)
         : "memory");
 }
@@ -690,21 +689,22 @@ __device__ __forceinline__ void issue_values(Smem<HD, T> &sm, uint32_t tmem, int
     for (int n = 0;; ++n) {
         const int st = n % C::NS;
         if (!all_wait(&sm.p_ready[n & 1], (n >> 1) & 1, abort_flag, err)) return;
-        const int flag = __shfl_sync(0xffffffffu, *static_cast<volatile int *>(&sm.p_flag[n & 1]), 0);
+        const int last = __shfl_sync(0xffffffffu, *static_cast<volatile int *>(&sm.p_last[n & 1]), 0);
         if (!all_wait(&sm.v_full[st], (n / C::NS) & 1, abort_flag, err)) return;
         tc_after();
         const uint64_t v0 = dv + st * D::kStage;
-        const uint32_t ph = tmem + kColS + static_cast<uint32_t>(n & 1) * KT, pl = ph + 64;
+        const uint32_t p0 = tmem + kColS + static_cast<uint32_t>(n & 1) * KT;
 #pragma unroll 4
         for (int kk = 0; kk < KT / 16; ++kk) {
             const uint64_t o = static_cast<uint64_t>(kk) * (16 * 128 >> 4);
-            mma_ts(leader, tmem + kColO, ph + kk * 8, v0 + o, kId, !(flag & 1) || kk > 0);
-            mma_ts(leader, tmem + kColO, pl + kk * 8, v0 + o, kId, true);
-            if constexpr (C::HL) mma_ts(leader, tmem + kColO, ph + kk * 8, v0 + D::kTerm + o, kId, true);
+            const uint32_t ph = p0 + (kk >> 1) * 32 + (kk & 1) * 8;  // 32 keys' hi halves, then their lo halves
+            mma_ts(leader, tmem + kColO, ph, v0 + o, kId, kk > 0);
+            mma_ts(leader, tmem + kColO, ph + 16, v0 + o, kId, true);
+            if constexpr (C::HL) mma_ts(leader, tmem + kColO, ph, v0 + D::kTerm + o, kId, true);
         }
         commit(leader, &sm.o_done[n & 1]);
         commit(leader, &sm.v_empty[st]);
-        if (flag & 2) return;
+        if (last) return;
     }
 }
 
@@ -727,7 +727,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
     for (int seg = 0; sm.more[seg & 1]; ++seg) {
         const Walk &w = sm.walk[seg & 1];
         const int rows = w.cnt * g, tiles = w.u1 - w.u0;
-        // this half row of Q, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
+        // this part of the Q row, scaled, as hi + lo halves into TMEM (all MMAs that read the last ones are done)
         float c;
         {
             chunk_wait(&sm.q_in, seg & 1, abort_flag, err);
@@ -783,7 +783,24 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             sm.walk[(seg + 1) & 1] = next;
         }
         named_sync(1, C::kRowThreads);
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, last_corr = 1.0f;
+        float2 acc[DIMS / 2];
+#pragma unroll
+        for (int d = 0; d < DIMS / 2; ++d) acc[d] = make_float2(0.0f, 0.0f);
+        // O of tile q, which stands at that tile's maximum, into the sums, which stand at the one before
+        auto fold = [&](int q) {
+            chunk_wait(&sm.o_done[q & 1], (q >> 1) & 1, abort_flag, err);
+            tc_after();
+            const float2 f = make_float2(last_corr, last_corr);
+#pragma unroll
+            for (int d = 0; d < DIMS; d += 32) {
+                uint32_t o[32];
+                tm_ld32(lanes + kColO + part * DIMS + d, o);
+                tm_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) acc[(d + e) >> 1] = fma2(acc[(d + e) >> 1], f, bits2(o[e], o[e + 1]));
+            }
+        };
         for (int i = 0; i < tiles; ++i) {
             const int j0 = unit_tile(w.keys, w.u0 + i) * KT, q = n + i;
             chunk_wait(&sm.s_full[q & 1], (q >> 1) & 1, abort_flag, err);
@@ -791,9 +808,6 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             if (!warp_live) {
                 named_sync(1, C::kRowThreads);
             } else {
-                uint32_t x[COLS];  // S, then what the exponentials take, as bits
-#pragma unroll
-                for (int e = 0; e < COLS; e += 32) tm_ld32(lanes + kColS + (q & 1) * KT + part * COLS + e, x + e);
                 float cc = c, ve = 0.0f, vi = 1.0f;
                 bool k_rows = false, v_rows = false;
                 if constexpr (C::HL) {
@@ -805,108 +819,102 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     ve = fv.exp;
                     vi = fv.fac;
                 }
-                tm_wait_ld();
+                const float tile_c = cc;
+                // key by key factors (rare): t = S c k + e as the scores are read, else one multiply-add below takes
+                // S to its exponential
+                const bool by_key = C::HL && (k_rows || v_rows);
+                if (by_key) cc = 1.0f;
                 const int2 all = sm.all;
                 const bool mask = j0 + KT > all.y || (j0 < all.x && j0 + KT > p.a.n_sink);
-                // key by key factors (rare): t = S c k + e now, else one multiply-add below takes S to its exponential
-                const bool by_key = C::HL && (k_rows || v_rows);
-                if (by_key) {
-#pragma unroll
-                    for (int e = 0; e < COLS; e += 4) {
-                        float4 kf = make_float4(cc, cc, cc, cc), vv = make_float4(ve, ve, ve, ve);
-                        if (k_rows) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][part * COLS + e]);
-                            kf = make_float4(f.x * cc, f.y * cc, f.z * cc, f.w * cc);
-                        }
-                        if (v_rows) vv = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][part * COLS + e]);
-                        const float2 a = fma2(bits2(x[e], x[e + 1]), lo2(kf), lo2(vv)), b = fma2(bits2(x[e + 2], x[e + 3]), hi2(kf), hi2(vv));
-                        x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
-                        x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
-                    }
-                    cc = 1.0f;
-                    ve = 0.0f;
-                }
-                if (mask) {
-                    // this row's window: keys [r_lo, r_hi) and [0, r_sink)
+                int r_hi = 0, r_lo = 0, r_sink = 0;  // this row's window: keys [r_lo, r_hi) and [0, r_sink)
+                if (mask && live) {
                     const long long pos = walk_pos(w, p) + sm.token[row];
-                    int r_hi = 0, r_lo = 0, r_sink = 0;
-                    if (pos >= 0) {
-                        r_hi = pos + 1 < w.rows.cap ? static_cast<int>(pos + 1) : w.rows.cap;
-                        if (p.a.window) {
-                            const long long lo = pos - p.a.window + 1;
-                            r_lo = lo <= 0 ? 0 : (lo < r_hi ? static_cast<int>(lo) : r_hi);
-                            r_sink = min(p.a.n_sink, r_hi);
-                        }
-                    }
-                    const int jb = j0 + part * COLS, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
-#pragma unroll
-                    for (int e = 0; e < COLS; ++e) {
-                        const bool see = (e < e_hi) & ((e >= e_lo) | (e < e_sink));
-                        x[e] = see ? x[e] : 0xff800000u;  // -infinity
+                    r_hi = static_cast<int>(pos + 1 < w.rows.cap ? (pos + 1 > 0 ? pos + 1 : 0) : w.rows.cap);
+                    if (p.a.window) {
+                        const long long lo = pos - p.a.window + 1;
+                        r_lo = lo > 0 ? static_cast<int>(lo < 0x7fffffff ? lo : 0x7fffffff) : 0;
+                        r_sink = min(p.a.n_sink, r_hi);
                     }
                 }
+                const uint32_t s_col = lanes + kColS + (q & 1) * KT + part * COLS;
+                // 32 of the thread's scores, hidden ones as -infinity
+                auto scores = [&](int h, uint32_t *x) {
+                    tm_ld32(s_col + h, x);
+                    tm_wait_ld();
+                    if (by_key) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            float4 kf = make_float4(tile_c, tile_c, tile_c, tile_c), vv = make_float4(ve, ve, ve, ve);
+                            if (k_rows) {
+                                const float4 f = *reinterpret_cast<const float4 *>(&sm.k_fac[q & 3][part * COLS + h + e]);
+                                kf = make_float4(f.x * tile_c, f.y * tile_c, f.z * tile_c, f.w * tile_c);
+                            }
+                            if (v_rows) vv = *reinterpret_cast<const float4 *>(&sm.v_exp[q & 3][part * COLS + h + e]);
+                            const float2 a = fma2(bits2(x[e], x[e + 1]), lo2(kf), lo2(vv)), b = fma2(bits2(x[e + 2], x[e + 3]), hi2(kf), hi2(vv));
+                            x[e] = __float_as_uint(a.x), x[e + 1] = __float_as_uint(a.y);
+                            x[e + 2] = __float_as_uint(b.x), x[e + 3] = __float_as_uint(b.y);
+                        }
+                    }
+                    if (mask) {
+                        const int jb = j0 + part * COLS + h, e_hi = r_hi - jb, e_lo = r_lo - jb, e_sink = r_sink - jb;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const bool see = (e < e_hi) & ((e >= e_lo) | (e < e_sink));
+                            x[e] = see ? x[e] : 0xff800000u;  // -infinity
+                        }
+                    }
+                };
                 float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < COLS; e += 8)
+                for (int h = 0; h < COLS; h += 32) {
+                    uint32_t x[32];
+                    scores(h, x);
 #pragma unroll
-                    for (int f = 0; f < 4; ++f)
-                        mt[f] = fmaxf(fmaxf(mt[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + 4 + f]));
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            mt[f] = fmaxf(fmaxf(mt[f], __uint_as_float(x[e + f])), __uint_as_float(x[e + 4 + f]));
+                }
                 sm.mx[q & 1][part][row] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
-                tc_before();
-                named_sync(1, C::kRowThreads);  // all threads of a row have read S: P may go over it
-                tc_after();
+                named_sync(1, C::kRowThreads);
                 float mn = sm.mx[q & 1][0][row];
 #pragma unroll
                 for (int k = 1; k < PARTS; ++k) mn = fmaxf(mn, sm.mx[q & 1][k][row]);
-                mn = mn * cc + ve;
-                const bool grow = mn > m + kSlack || (m == -INFINITY && mn > m);
-                float corr = 1.0f;
-                if (grow) {
-                    corr = ex2_approx(m - mn);
-                    m = mn;
-                }
-                if (i > 0 && __any_sync(0xffffffffu, grow)) {
-                    chunk_wait(&sm.o_done[(q - 1) & 1], ((q - 1) >> 1) & 1, abort_flag, err);
-                    tc_after();
-#pragma unroll 1
-                    for (int d = 0; d < DIMS; d += 16) {
-                        uint32_t o[16];
-                        tm_ld16(lanes + kColO + part * DIMS + d, o);
-                        tm_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                        tm_st<16>(lanes + kColO + part * DIMS + d, o);
-                    }
-                }
+                const float te = by_key ? 0.0f : ve;
+                mn = fmaxf(m, mn * cc + te);
+                const float corr = mn == -INFINITY ? 1.0f : ex2_approx(m - mn);
+                m = mn;
                 const float base = m == -INFINITY ? 0.0f : m - kShift;
-                const float2 c2 = make_float2(cc, cc), nb = make_float2(ve - base, ve - base);
+                const float2 c2 = make_float2(cc, cc), nb = make_float2(te - base, te - base);
                 float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
-                for (int e0 = 0; e0 < COLS; e0 += 32) {
-                    uint32_t ph[16], pl[16];
+                for (int h = 0; h < COLS; h += 32) {
+                    uint32_t x[32], ph[16], pl[16];
+                    scores(h, x);
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        float2 a = fma2(bits2(x[e0 + e], x[e0 + e + 1]), c2, nb), b = fma2(bits2(x[e0 + e + 2], x[e0 + e + 3]), c2, nb);
+                        float2 a = fma2(bits2(x[e], x[e + 1]), c2, nb), b = fma2(bits2(x[e + 2], x[e + 3]), c2, nb);
                         a = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                         b = make_float2(ex2_approx(b.x), ex2_approx(b.y));
-                        s2 = add2(s2, a);
-                        s3 = add2(s3, b);
+                        if (C::HL && v_rows) {  // each key's own 2^-e
+                            const float4 f = *reinterpret_cast<const float4 *>(&sm.v_inv[q & 3][part * COLS + h + e]);
+                            s2 = fma2(a, lo2(f), s2);
+                            s3 = fma2(b, hi2(f), s3);
+                        } else {
+                            s2 = add2(s2, a);
+                            s3 = add2(s3, b);
+                        }
                         split2(a.x, a.y, ph[e >> 1], pl[e >> 1]);
                         split2(b.x, b.y, ph[(e >> 1) + 1], pl[(e >> 1) + 1]);
                     }
-                    tm_st<16>(lanes + kColS + (q & 1) * KT + part * (COLS / 2) + (e0 >> 1), ph);
-                    tm_st<16>(lanes + kColS + (q & 1) * KT + 64 + part * (COLS / 2) + (e0 >> 1), pl);
+                    // over the scores they came from: 32 keys' hi halves, then their lo halves
+                    tm_st16(s_col + h, ph);
+                    tm_st16(s_col + h + 16, pl);
                 }
-                float sum = (s2.x + s2.y) + (s3.x + s3.y);
-                if constexpr (C::HL) {
-                    sum *= vi;
-                    if (v_rows) {  // each key's own 2^-e
-                        sum = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < COLS; ++e) sum = fmaf(ex2_approx(__uint_as_float(x[e]) * cc + (ve - base)), sm.v_inv[q & 3][part * COLS + e], sum);
-                    }
-                }
-                l = l * corr + sum;
+                const float sum = (s2.x + s2.y) + (s3.x + s3.y);
+                l = l * corr + (C::HL ? sum * vi : sum);
+                if (i > 0) fold(q - 1);  // (P V of this tile goes over it)
+                last_corr = corr;
                 tm_wait_st();
             }
             if (!C::HL && (j0 < w.keys.lo || j0 + KT > w.keys.hi)) {
@@ -922,13 +930,12 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 fence_async_smem();
             }
             tc_before();
-            if (tid == 0) sm.p_flag[q & 1] = (i == 0 ? 1 : 0) | (i + 1 == tiles && tiles == w.left ? 2 : 0);
+            if (tid == 0) sm.p_last[q & 1] = i + 1 == tiles && tiles == w.left;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
         }
         n += tiles;
-        chunk_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, err);
-        tc_after();
+        if (warp_live) fold(n - 1);
         sm.sum[part][row] = l;
         named_sync(1, C::kRowThreads);
         l = sm.sum[0][row];
@@ -957,15 +964,13 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         bool finish = whole, odd = false, again = false;
         if (whole) {
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-#pragma unroll 1
+#pragma unroll
             for (int d = 0; d < DIMS; d += 16) {
-                uint32_t o[16];
                 float y[16];
-                tm_ld16(lanes + kColO + part * DIMS + d, o);
-                tm_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    y[e] = l == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                    const float2 o = acc[(d + e) >> 1];
+                    y[e] = l == 0.0f ? 0.0f : (e & 1 ? o.y : o.x) * inv;
                     odd |= !(fabsf(y[e]) < INFINITY);
                 }
 #pragma unroll
@@ -975,20 +980,12 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             // this stretch's part: O as [dims / 4][rows] float4, then the rows' maxima and sums
             constexpr size_t kPart = static_cast<size_t>(BM) * (HD + 2);
             float *mine = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
-            if (warp_live) {
+            if (live) {
 #pragma unroll
-                for (int d = 0; d < DIMS; d += 16) {
-                    uint32_t o[16];
-                    tm_ld16(lanes + kColO + part * DIMS + d, o);
-                    tm_wait_ld();
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            reinterpret_cast<float4 *>(mine)[((part * DIMS + d + e) >> 2) * BM + row] =
-                                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-                    }
-                }
-                if (live && part == 0) {
+                for (int d = 0; d < DIMS; d += 4)
+                    reinterpret_cast<float4 *>(mine)[((part * DIMS + d) >> 2) * BM + row] =
+                        make_float4(acc[d >> 1].x, acc[d >> 1].y, acc[(d >> 1) + 1].x, acc[(d >> 1) + 1].y);
+                if (part == 0) {
                     mine[BM * HD + row] = m;
                     mine[BM * (HD + 1) + row] = l;
                 }
