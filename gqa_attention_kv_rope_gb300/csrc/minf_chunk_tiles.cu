@@ -83,9 +83,9 @@ struct Cfg {
     static constexpr int kRowThreads = 128 * PARTS, kRowWarps = kRowThreads / 32;
     // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3, 4).  The rows'
     // threads hold 64 scores and their halves, so registers move to them; the shares add up to the
-    // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 144 + 128 * 48 + 256 * 72 = 640 * 96.
+    // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 152 + 128 * 48 + 256 * 64 = 640 * 96.
     static constexpr int kThreads = HL ? 640 : 384;
-    static constexpr int kRowRegs = HL ? 144 : 208, kIssueRegs = HL ? 48 : 88;
+    static constexpr int kRowRegs = HL ? 152 : 208, kIssueRegs = HL ? 48 : 88;
     static constexpr int kQRow = HD * 4 + 16;  // bytes of a staged Q row (spread over the banks)
 };
 
@@ -864,10 +864,12 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         }
                     }
                 };
+                constexpr bool kHold = !C::HL;  // (registers for all of the scores; else they are read again)
+                uint32_t xs[kHold ? COLS : 32];
                 float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int h = 0; h < COLS; h += 32) {
-                    uint32_t x[32];
+                    uint32_t *x = xs + (kHold ? h : 0);
                     scores(h, x);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -889,8 +891,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 float2 s2 = make_float2(0.0f, 0.0f), s3 = s2;
 #pragma unroll
                 for (int h = 0; h < COLS; h += 32) {
-                    uint32_t x[32], ph[16], pl[16];
-                    scores(h, x);
+                    uint32_t *x = xs + (kHold ? h : 0), ph[16], pl[16];
+                    if (!kHold) scores(h, x);
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         float2 a = fma2(bits2(x[e], x[e + 1]), c2, nb), b = fma2(bits2(x[e + 2], x[e + 3]), c2, nb);
@@ -1139,7 +1141,7 @@ __global__ void __launch_bounds__(Cfg<HD, T>::kThreads, 1)
             copy_tiles<HD, T, true>(sm, tm_v, p, ctas);
         }
     } else if constexpr (C::HL) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(72));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(64));
         if (!idle) split_tiles<HD, T>(sm, p, role - 4);
     }
     tc_before();
