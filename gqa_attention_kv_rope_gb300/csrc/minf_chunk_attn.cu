@@ -6,8 +6,15 @@ namespace minf {
 
 namespace {
 
-constexpr int kStreamRows = 32;  // query rows (tokens x heads of a kv head) the streaming kernel takes at once
-constexpr int kFewRows = 8;      // and in a call that also has long chunks
+// Query rows (tokens x heads of a kv head) up to which the streaming kernel runs alone.  Measured on 16 query
+// heads over 8 kv heads of 128 dims, 64 sequences of 4096 rows, streaming kernel and tiles: binary16 16 rows
+// 195 and 210 us, 32 rows 363 and 212; Q8_0 32 rows 627 and 725; fp32 (16 sequences) 238 and 267.  One sequence
+// of 8192 rows, binary16: 8 rows 25 and 56, 32 rows 49 and 54.
+constexpr int kStreamRows = 32, kStreamRowsF16 = 16;
+// And in a call that also has long chunks: there the streaming kernel takes the few tokens of the others.  31
+// single tokens beside 3 chunks of 391, Q8_0: 267 us, all in tiles 575; with the streaming kernel laid out
+// for 32 rows 533 (it computes as many for every token).
+constexpr int kFewRows = 8;
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -17,9 +24,9 @@ struct Choice {
     bool stream, tiles;
     int rows, most;  // of the streaming kernel
 };
-Choice choose(int n_seq, int g, int max_chunk) {
+Choice choose(int kv, int n_seq, int g, int max_chunk) {
     const long long rows = static_cast<long long>(g) * max_chunk;
-    if (rows <= kStreamRows) return {true, false, static_cast<int>(rows), 0x7fffffff};
+    if (rows <= (kv == kKvF16 ? kStreamRowsF16 : kStreamRows)) return {true, false, static_cast<int>(rows), 0x7fffffff};
     return {n_seq > 1, true, kFewRows, kFewRows / g};
 }
 
@@ -27,14 +34,19 @@ Choice choose(int n_seq, int g, int max_chunk) {
 
 size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk) {
     if (nt <= 0 || n_seq <= 0 || nh <= 0 || nk <= 0 || nh % nk || (hd_kv != 64 && hd_kv != 128) || max_chunk <= 0) return 0;
-    const Choice c = choose(n_seq, nh / nk, max_chunk);
-    return (c.tiles ? up256(chunk_tiles_workspace(nt, n_seq, nh, nk, hd_kv)) : 0) +
-           (c.stream ? chunk_stream_workspace(nt, n_seq, nh, nk, hd_kv, c.rows) : 0);
+    size_t most = 0;  // of the types
+    for (const int kv : {kKvF32, kKvF16, kKvQ8}) {
+        const Choice c = choose(kv, n_seq, nh / nk, max_chunk);
+        const size_t need = (c.tiles ? up256(chunk_tiles_workspace(nt, n_seq, nh, nk, hd_kv)) : 0) +
+                            (c.stream ? chunk_stream_workspace(nt, n_seq, nh, nk, hd_kv, c.rows) : 0);
+        if (need > most) most = need;
+    }
+    return most;
 }
 
 int launch_chunk_attn(const ChunkAttnArgs &a, cudaStream_t s) {
     if (a.sq.nt == 0 || a.sq.n_seq == 0) return MINF_OK;
-    const Choice c = choose(a.sq.n_seq, a.nh / a.nk, a.max_chunk);
+    const Choice c = choose(a.c.kv, a.sq.n_seq, a.nh / a.nk, a.max_chunk);
     char *ws = static_cast<char *>(a.ws);
     Plans plans = {};
     AttnParams tiles, stream;

@@ -34,7 +34,16 @@ namespace minf {
 namespace {
 
 constexpr int KT = 64;              // keys of a tile
-constexpr float kShift = 12.0f, kSlack = 3.0f;  // P is at most 2^15 (as in minf_chunk_tiles.cu)
+// P is at most 2^(shift + slack) = 2^15; outputs are rescaled when a row's scores have grown by 2^slack.  The
+// halves keep P to 2^-25: n keys that all lose as much are off by n 2^-25 of a sum of at least 2^shift.
+constexpr float kShift = 12.0f, kSlack = 3.0f;
+
+// A tile's products into the sums, in rounded fp32: the tensor cores' own accumulation cuts the low bits off,
+// always towards zero (2e-5 after the 65536 keys of one stretch, now below 2e-6).
+__device__ __forceinline__ void sum4(float *acc, const float *d) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += d[e];
+}
 
 template <int HD, typename T, int NT>
 struct Cfg {
@@ -548,12 +557,13 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                         const uint32_t a1[4] = {q_pair(t1, 0x4140), q_pair(t1, 0x4342), q_pair(t3, 0x4140), q_pair(t3, 0x4342)};
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            float(&d0)[4] = *reinterpret_cast<float(*)[4]>(&acc[(t * MT + 2 * b) * 4]);
-                            float(&d1)[4] = *reinterpret_cast<float(*)[4]>(&acc[(t * MT + 2 * b + 1) * 4]);
-                            mma_f16(d0, a0, b_hi[t][b][0], b_hi[t][b][1]);
-                            mma_f16(d1, a1, b_hi[t][b][0], b_hi[t][b][1]);
+                            float d0[4] = {}, d1[4] = {};
                             mma_f16(d0, a0, b_lo[t][b][0], b_lo[t][b][1]);
                             mma_f16(d1, a1, b_lo[t][b][0], b_lo[t][b][1]);
+                            mma_f16(d0, a0, b_hi[t][b][0], b_hi[t][b][1]);
+                            mma_f16(d1, a1, b_hi[t][b][0], b_hi[t][b][1]);
+                            sum4(&acc[(t * MT + 2 * b) * 4], d0);
+                            sum4(&acc[(t * MT + 2 * b + 1) * 4], d1);
                         }
                     }
                 } else if constexpr (C::F32) {
@@ -574,13 +584,14 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                             }
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                float(&d)[4] = *reinterpret_cast<float(*)[4]>(&acc[(t * MT + 2 * b + i2) * 4]);
-                                mma_bf16(d, a1, b_hi[t][0][0], b_hi[t][0][1]);
-                                mma_bf16(d, a1, b_lo[t][0][0], b_lo[t][0][1]);
-                                mma_bf16(d, a2, b_hi[t][0][0], b_hi[t][0][1]);
-                                mma_bf16(d, a1, b_3[t][0], b_3[t][1]);
-                                mma_bf16(d, a2, b_lo[t][0][0], b_lo[t][0][1]);
+                                float d[4] = {};
                                 mma_bf16(d, a3, b_hi[t][0][0], b_hi[t][0][1]);
+                                mma_bf16(d, a2, b_lo[t][0][0], b_lo[t][0][1]);
+                                mma_bf16(d, a1, b_3[t][0], b_3[t][1]);
+                                mma_bf16(d, a2, b_hi[t][0][0], b_hi[t][0][1]);
+                                mma_bf16(d, a1, b_lo[t][0][0], b_lo[t][0][1]);
+                                mma_bf16(d, a1, b_hi[t][0][0], b_hi[t][0][1]);
+                                sum4(&acc[(t * MT + 2 * b + i2) * 4], d);
                             }
                         }
                     }
@@ -591,9 +602,10 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                         ldsm4t(su32(vst + (k >> 2) * (KT * 128) + at16<C>(key0 + (lane >> 4) * 8 + (lane & 7), (k & 3) * 2 + ((lane >> 3) & 1))), a);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            float(&d)[4] = *reinterpret_cast<float(*)[4]>(&acc[(t * MT + k) * 4]);
-                            mma_f16(d, a, b_hi[t][0][0], b_hi[t][0][1]);
+                            float d[4] = {};
                             mma_f16(d, a, b_lo[t][0][0], b_lo[t][0][1]);
+                            mma_f16(d, a, b_hi[t][0][0], b_hi[t][0][1]);
+                            sum4(&acc[(t * MT + k) * 4], d);
                         }
                     }
                 }
@@ -834,9 +846,9 @@ int launch(const AttnParams &p, int grid, cudaStream_t s) {
 
 template <int HD, int NT>
 int launch_kind(const AttnParams &p, int grid, cudaStream_t s) {
-    return p.a.c.kv == kKvQ8    ? launch<HD, Q8, NT>(p, grid, s)
-           : p.a.c.kv == kKvF16 ? launch<HD, __half, NT>(p, grid, s)
-                                : launch<HD, float, NT>(p, grid, s);
+    if constexpr (NT < 4)  // (more than 16 rows of binary16 go to the tiles)
+        if (p.a.c.kv == kKvF16) return launch<HD, __half, NT>(p, grid, s);
+    return p.a.c.kv == kKvQ8 ? launch<HD, Q8, NT>(p, grid, s) : launch<HD, float, NT>(p, grid, s);
 }
 
 int row_tiles(int rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }

@@ -6,15 +6,17 @@
 // group.  A CTA walks its stretch of units (minf_chunk_plan.cuh); per tile of 128 keys:
 //   S = Q K^T   tcgen05.mma kind::f16, M = N = 128, Q from TMEM, into one of two TMEM buffers
 //   P = 2^(s - m)   two threads a row (64 keys each): read S, mask, share the row's maximum,
-//                   and write P as binary16 halves hi + lo over the S they came from
-//   O += P V    tcgen05.mma kind::f16 with P from TMEM, V as it lies in memory (keys x dims, the
-//               transposed operand), into TMEM
+//                   and write P as binary16 halves hi + lo over the scores they came from
+//   O = P V     tcgen05.mma kind::f16 with P from TMEM, V as it lies in memory (keys x dims, the
+//               transposed operand), into TMEM; the row threads add the tile's O to their sums in
+//               registers (sum = sum 2^(m_old - m) + O) while S and P of the next tile are under way
 // Q and P come from TMEM because an operand pair from shared memory (8 KB a 128x128x16 step) takes
 // 97 clocks of its bandwidth, against 64 of tensor work with one of them in TMEM.
 // S of the next tile runs while the row threads work on this one; the tile after next goes into the
-// buffer that P V has just finished with.  O is rescaled only when a row's maximum has grown by
-// more than 2^3 since the last time (P is then at most 2^15, still a binary16 value, and the rescale
-// is a rare pass over O instead of one a tile).
+// buffer that P V has just finished with.
+// The sums over the tiles are not left to the tensor cores: their accumulation cuts the low bits off, always
+// towards zero, so that an output over 12000 keys was 2e-5 off 64 bits.  Added tile by tile in rounded fp32
+// it is 8e-7 off (a plain fp32 evaluation: 1.7e-6), for 2% of the time.
 //
 // Precision: fp32 results from binary16 products.  Every operand that is not exactly binary16 is
 // split into hi + lo halves (22 bits), scaled by a power of two that keeps both normal; a product
@@ -35,14 +37,15 @@
 // copy; otherwise warp 9 resolves the tiles' rows ahead, warp 11 copies Q rows, and warps 12-19 load,
 // split and write K and V in turn.
 //
-// What bounds it, on the batch of six ragged prompts of 500 to 2048 tokens over 12000 cached binary16 rows
-// (16 query heads on 8 of 128 dims; 684 GFLOP): 1.10 ms, 622 TFLOP/s, twice that on the tensor cores, whose
-// rate of 1.88 PFLOP/s allows 0.73 ms.  A tile takes 3100 clocks, of which S and P V take 2600 (a
-// 128x128x16 step some 81, as in the library's own products); the rest is the way from P V's end
-// over S of the next tile but one to the row threads, which a third S buffer would hide if TMEM had room
-// for it.  S cut into two halves of 64 keys, so that the first could start earlier, measured 1260 us.
-// Q8_0 and fp32 tiles take 6000 to 8000 clocks, against 3900 of tensor work in three products: the splitting
-// warps write 128 KB of halves a tile, and there is no room for a second stage of them at 128 dims.
+// What bounds it, on a batch of six ragged prompts of up to 2048 tokens over up to 12000 cached binary16 rows
+// (16 query heads on 8 of 128 dims; 684 GFLOP): 1.13 ms, 607 TFLOP/s, twice that on the tensor cores, whose
+// measured rate of 1.88 PFLOP/s allows 0.73 ms.  A tile takes 2800 to 3100 clocks, of which S and P V take
+// 2600 (81 to 88 a 128x128x16 step) and the row threads 2500: both are nearly full.  S cut into two halves
+// of 64 keys, so that the first could start earlier, measured 1260 us.  Q8_0 and fp32 tiles take about
+// 10000 clocks, against 3900 of tensor work in three products: the splitting warps write 128 KB of halves
+// a tile, there is no room for a second stage of them at 128 dims, and the warps of a CTA wait on one another.
+// Tried there and not kept: K split a tile ahead of V (265 us against 264 on 34 sequences, 31 of them single
+// tokens), the tiles' factors found by the warp that resolves the rows (277 us).
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
 // not); rows that only some tokens see can still carry infinities or NaN into the sums of those that
@@ -66,8 +69,8 @@ constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
 // P is at most 2^kShift, and lo keeps it to 2^-25: n keys that all lose as much are off by n 2^-25 of a sum of
 // at least 2^kShift (2^-23 for 2^17 of them).
 constexpr float kShift = 15.0f;
-// TMEM columns: the S buffers (P over them: hi, then lo, two keys a column), O, Q (hi, then lo, two dims a
-// column)
+// TMEM columns: the S buffers (P over them: of each 32 keys hi, then lo, two keys a column), O of a tile, Q (hi,
+// then lo, two dims a column)
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kTmemCols = 512;
 
 template <int HD, typename T>
@@ -76,13 +79,12 @@ struct Cfg {
     static constexpr int SLABS = HD / 64;                        // 128-byte-wide slabs of a tile
     static constexpr int TERMS = HL ? 2 : 1;
     static constexpr int NS = HL ? (HD == 64 ? 2 : 1) : (HD == 64 ? 4 : 2);  // K and V stages
-    // Row threads: two threads a row, each with half of a tile's keys and of the row's dims.  (Four, which
-    // hide one another's waits better but meet at a wider barrier, measured the same over binary16: 1155 us
-    // against 1102 on the ragged batch below.)
+    // Row threads: two threads a row, each with half of a tile's keys and of the row's dims.  (Four,
+    // which hide one another's waits better but meet at a wider barrier: 1155 us against 1102 over binary16.)
     static constexpr int PARTS = 2, COLS = KT / PARTS, DIMS = HD / PARTS;
     static constexpr int kRowThreads = 128 * PARTS, kRowWarps = kRowThreads / 32;
     // Warp groups: rows (0, 1), the issuing and copying warps (2), the splitting producers (3, 4).  The rows'
-    // threads hold 64 scores and their halves, so registers move to them; the shares add up to the
+    // threads hold scores and 64 output sums, so registers move to them; the shares add up to the
     // launch's: 256 * 208 + 128 * 88 = 384 * 168, and 256 * 152 + 128 * 48 + 256 * 64 = 640 * 96.
     static constexpr int kThreads = HL ? 640 : 384;
     static constexpr int kRowRegs = HL ? 152 : 208, kIssueRegs = HL ? 48 : 88;

@@ -543,6 +543,32 @@ def test_rows_that_take_long_do_not_run_out_of_time(m):
         close(out[t, :, 1:].cpu().numpy(), ref.cpu().numpy())
 
 
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+@pytest.mark.parametrize("n_seq,new,past", [(152, 1, 65536), (152, 3, 50000), (40, 64, 30000)])
+def test_sums_over_many_keys(m, kind, n_seq, new, past):
+    # one CTA goes over all of a sequence's keys.  Sums of 16 or 128 keys are cut off below 2^-23, once; adding
+    # up to 512 of them rounds by 2^-25 each, independently: 7e-7; a weight is off by its score's rounding and
+    # the exponential's, below 2e-6 together: 4e-6 of the result in the 2-norm.
+    # (The sequences share their rows.)
+    nh, hd, cap = 8, 64, past + new
+    gen = torch.Generator("cuda").manual_seed(past)
+    k, v = (torch.randn(cap, hd, device="cuda", generator=gen).to(torch.float16 if kind == "f16" else torch.float32)
+            for _ in range(2))
+    v = v + 1
+    nt = n_seq * new
+    q = torch.randn(nt, nh, hd, device="cuda", generator=gen)
+    out, err = torch.empty(nt, nh * hd, device="cuda"), i32([0])
+    ws = m.kv.chunk_workspace(nt, n_seq, nh, 1, hd, new)
+    getattr(m, "minf_gqa_attn_window" + END[kind])(
+        out, q, k, v, torch.zeros(n_seq, dtype=torch.int64, device="cuda"), None, cap, i32(np.arange(n_seq + 1) * new),
+        i32([past] * n_seq), new, nh, 1, hd, hd, hd ** -0.5, 0, 0, ws, err)
+    assert err.item() == 0
+    for t in (0, nt // 2, nt - 1):
+        p = past + t % new
+        ref = torch.softmax(q[t].double() @ k[:p + 1].double().T * hd ** -0.5, -1) @ v[:p + 1].double()
+        assert (out[t].view(nh, hd) - ref).norm() <= 4e-6 * ref.norm()
+
+
 # ----------------------------------------------------------------------------- rotation
 def ref_rope(x, pos, axis, hd, style):
     """x [nt, heads, hd], pos [n_axis, nt]: (rotated, |a| + |b| of each value's pair), in 64 bits."""
