@@ -127,7 +127,7 @@ void row_grid(int nt, long long units_tok, int &tok, dim3 &grid) {
         if (split > room) split = room;
         if (split > 64) split = 64;
     }
-    grid = dim3((nt + tok - 1) / tok, static_cast<unsigned>(split));
+    grid = dim3(static_cast<unsigned>((static_cast<long long>(nt) + tok - 1) / tok), static_cast<unsigned>(split));
 }
 
 }  // namespace

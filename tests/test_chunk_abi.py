@@ -128,3 +128,10 @@ def test_out_may_not_overlap_q(lib, end, at):
     q = 1 << 20
     for f, args in (("minf_gqa_attn_chunk_paged", attn_args), ("minf_gqa_attn_window", window_args)):
         assert getattr(lib, f + end)(*args(q=P(q), out=P(q + at))) == 1
+
+
+@pytest.mark.parametrize("nh,nk", [(9, 1), (16, 1), (32, 1), (129, 1), (1 << 20, 1), (64, 4)])
+def test_workspace_of_geometries_that_no_call_takes(lib, nh, nk):
+    for max_chunk in (1, 4, 1000):
+        assert lib.minf_attn_chunk_workspace_bytes(4, 2, nh, nk, 64, max_chunk) == 0
+    assert lib.minf_gqa_attn_chunk_paged(*attn_args(nh=nh, nk=nk)) == 3
