@@ -650,8 +650,8 @@ def minf_rope_axes(y, x, pos, pair_axis, n_head, hd, theta, freq_scale, style, e
     here = torch.cuda.current_device()
     _size("x", x, nt * n_head * hd)
     _size("y", y, nt * n_head * hd)
-    _check(lib().minf_rope_axes(_ptr(y, _F32, "y", here), _ptr(x, _F32, "x", here), _ptr(pos, _I32, "pos", here), nt, n_axis,
-                                _axis_bytes(pair_axis, hd), n_head, hd, theta, freq_scale, style,
+    _check(lib().minf_rope_axes(_ptr(y, _F32, "y", here), _ptr(x, _F32, "x", here), _ptr(pos, _I32, "pos", here), nt,
+                                n_axis, _axis_bytes(pair_axis, hd), n_head, hd, theta, freq_scale, style,
                                 _ptr(err, _I32, "err", here), _stream(stream)), "minf_rope_axes")
 
 
@@ -673,7 +673,8 @@ def _rope_kv_append_chunk_paged(end, q_out, k_out, q, k, v, rope_pos, pair_axis,
         axes = None
     name = "minf_rope_kv_append_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _ptr(q_out, _F32, "q_out", here), _ptr(k_out, _F32, "k_out", here), _ptr(q, _F32, "q", here), _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here),
+        _ptr(q_out, _F32, "q_out", here), _ptr(k_out, _F32, "k_out", here), _ptr(q, _F32, "q", here),
+        _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here),
         _ptr(rope_pos, _I32, "rope_pos", here), n_axis, axes, _ptr(chunk_off, _I32, "chunk_off", here),
         _ptr(n_past, _I32, "n_past", here), nt, n_seq, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style,
         _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0],
@@ -715,7 +716,8 @@ def _kv_read_chunk_paged(end, k_rows, v_rows, k_pool, v_pool, block_table, block
     rows = torch.float16 if k_rows.dtype == torch.float16 else torch.float32
     name = "minf_kv_read_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _ptr(k_rows, rows, "k_rows", here), _ptr(v_rows, rows, "v_rows", here), rows == torch.float16, _ptr(k_pool, dt, "k_pool", here),
+        _ptr(k_rows, rows, "k_rows", here), _ptr(v_rows, rows, "v_rows", here), rows == torch.float16,
+        _ptr(k_pool, dt, "k_pool", here),
         _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0], w, _ptr(block_table, _I32, "block_table", here),
         block_table.shape[1], block_rows, _ptr(chunk_off, _I32, "chunk_off", here),
         _ptr(n_past, _I32, "n_past", here), nt, n_seq, _ptr(err, _I32, "err", here), _stream(stream)), name)
@@ -759,8 +761,8 @@ def _gqa_attn_chunk_paged(end, out, q, k_pool, v_pool, block_table, block_rows, 
     _chunk_pool(end, k_pool, v_pool, block_table, n_seq, n_kv_head * hd_kv)
     name = "minf_gqa_attn_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here),
-        k_pool.shape[0], _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows,
+        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_pool, dt, "k_pool", here),
+        _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0], _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows,
         _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk, n_head,
         n_kv_head, hd, hd_kv, scale, window, n_sink, _ptr(ws, _U8, "ws", here), _nbytes(ws),
         _ptr(err, _I32, "err", here), _stream(stream)), name)
@@ -798,8 +800,9 @@ def _gqa_attn_window(end, out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, c
         raise ValueError(f"the regions have {k_reg.shape[0]} rows, max_cap is {max_cap}")
     name = "minf_gqa_attn_window" + end
     _check(getattr(lib(), name)(
-        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_reg, dt, "k_reg", here), _ptr(v_reg, dt, "v_reg", here),
-        _ptr(seq_row_off, torch.int64, "seq_row_off", here), _ptr(seq_cap, _I32, "seq_cap", here), max_cap, k_reg.shape[0],
+        _ptr(out, _F32, "out", here), _ptr(q, _F32, "q", here), _ptr(k_reg, dt, "k_reg", here),
+        _ptr(v_reg, dt, "v_reg", here), _ptr(seq_row_off, torch.int64, "seq_row_off", here),
+        _ptr(seq_cap, _I32, "seq_cap", here), max_cap, k_reg.shape[0],
         _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk, n_head,
         n_kv_head, hd, hd_kv, scale, window, n_sink, _ptr(ws, _U8, "ws", here), _nbytes(ws),
         _ptr(err, _I32, "err", here), _stream(stream)), name)
@@ -842,8 +845,9 @@ def _layer_step_chunk_paged(end, xn, h, gain, eps, q, k, v, rope_pos, pair_axis,
         axes = None
     name = "minf_layer_attn_step_chunk_paged" + end
     _check(getattr(lib(), name)(
-        _ptr(xn, _F32, "xn", here), _ptr(h, _F32, "h", here), _ptr(gain, _F32, "gain", here), eps, n_embd, _ptr(q, _F32, "q", here),
-        _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here), _ptr(rope_pos, _I32, "rope_pos", here), n_axis, axes,
+        _ptr(xn, _F32, "xn", here), _ptr(h, _F32, "h", here), _ptr(gain, _F32, "gain", here), eps, n_embd,
+        _ptr(q, _F32, "q", here), _ptr(k, _F32, "k", here), _ptr(v, _F32, "v", here),
+        _ptr(rope_pos, _I32, "rope_pos", here), n_axis, axes,
         _ptr(chunk_off, _I32, "chunk_off", here), _ptr(n_past, _I32, "n_past", here), nt, n_seq, max_chunk,
         _ptr(k_pool, dt, "k_pool", here), _ptr(v_pool, dt, "v_pool", here), k_pool.shape[0],
         _ptr(block_table, _I32, "block_table", here), block_table.shape[1], block_rows, n_head, n_kv_head, hd, hd_kv,
