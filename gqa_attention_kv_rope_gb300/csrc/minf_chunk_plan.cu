@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     long long *seq_units = a.sq.n_seq <= kHeld ? held_seq : a.seq_units;
     long long *tile_units = tiles_most <= kHeld ? held_tile : a.tile_units;
     for (int b = tid; b < a.max_ctas; b += kPlanThreads) a.tickets[b] = 0;
-    long long before = 0;  // units of the sequences of earlier rounds
+    long long before = 0;  // units of the sequences of earlier passes
     int bad = 0, reported = 0;
     for (int s0 = 0; s0 < a.sq.n_seq; s0 += kPlanThreads) {
         const int s = s0 + tid;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             before += y;
         }
         if (s < a.sq.n_seq) seq_units[s] = here;
-        __syncthreads();  // warp_sum is free for the next round
+        __syncthreads();  // warp_sum is free for the next pass
     }
     if (reported) flag_error(a.err, MINF_ERRBIT_ATTN_POS);
     if (__syncthreads_or(bad)) {
