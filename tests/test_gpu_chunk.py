@@ -380,6 +380,30 @@ def test_repeatable_and_on_another_stream(m):
             assert np.array_equal(first, again)
 
 
+def test_two_calls_at_once(m):
+    # on two streams, each with a workspace of its own: the bits of the calls made alone
+    calls = []
+    for kind, new in (("f16", [200, 3, 90]), ("q8", [60, 1, 1]), ("f32", [1, 1, 1])):
+        b = Batch((16, 8, 128, 128), kind, new, [900, 1500, 40], paged=True, block=64, seed=35)
+        alone, err = b.run(m)
+        assert err == 0
+        nh, nk, hd, hd_kv = b.geom
+        args = (dev(b.q), dev(b.k), dev(b.v), i32(b.table), b.block, i32(b.starts), i32(b.past), max(new), nh, nk, hd, hd_kv,
+                b.scale, 0, 0)
+        calls.append((getattr(m, "minf_gqa_attn_chunk_paged" + END[kind]), args, alone,
+                      m.kv.chunk_workspace(b.nt, 3, nh, nk, hd_kv, max(new)), torch.cuda.Stream(),
+                      [torch.full((b.nt, nh * hd_kv), 7.0, device="cuda") for _ in range(6)], i32([0])))
+    torch.cuda.synchronize()
+    for k in range(6):
+        for f, args, _, ws, stream, outs, err in calls:
+            f(outs[k], *args, ws, err, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, alone, _, _, outs, err in calls:
+        assert err.item() == 0
+        for out in outs:
+            assert np.array_equal(out.cpu().numpy(), alone)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("max_chunk", [1, 64])
 def test_graph_replays_with_other_lengths(m, kind, max_chunk):
