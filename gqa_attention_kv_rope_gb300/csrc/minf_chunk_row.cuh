@@ -3,7 +3,9 @@
 // The definition, as directly as a warp can compute it: the visible keys in groups of 32, a key a
 // lane, with the running maximum and sum of an online softmax in fp32; then every lane adds the
 // group's weighted V rows for its own dimensions, leaving out the hidden ones, so that nothing a
-// hidden row holds (infinities, NaN, whatever an unwritten row has) reaches the result.
+// hidden row holds (infinities, NaN, whatever an unwritten row has) reaches the result.  Weights are
+// at most 1 and a row has fewer than 2^31 keys, so with the weights of V taken 2^-32 times no sum of
+// finite values passes the range of fp32 (a term below 2^-117 of an output is lost).
 #pragma once
 
 #include "minf_chunk.cuh"
@@ -17,6 +19,8 @@ struct RowJob {
     long long p;     // the query's position
     int hk;          // kv head
 };
+
+constexpr float kValueScale = 2.3283064365386963e-10f;  // 2^-32
 
 // Returns (in every lane) whether a block the row sees is missing; its rows count as zeros.
 template <typename T, int HD>
@@ -77,7 +81,7 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
             for (int i = 0; i < 4; ++i) {
                 const long long rb = __shfl_sync(0xffffffffu, row, b0 + i);
                 pb[i] = __shfl_sync(0xffffffffu, pr, b0 + i);
-                if (rb < 0) pb[i] = 0.0f;  // (a missing block's row counts in l)
+                pb[i] = rb < 0 ? 0.0f : pb[i] * kValueScale;  // (a missing block's row counts in l)
                 v[i] = rb >= 0 ? row_ld4<T>(c.v, rb, c.W, c.row_bytes, job.hk * D4 + lane * PER / 4) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
@@ -94,7 +98,7 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // nothing visible: zeros
+    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * kValueScale);  // nothing visible: zeros
 #pragma unroll
     for (int i = 0; i < PER; ++i) job.out[lane * PER + i] = l == 0.0f ? 0.0f : acc[i] * inv;
     return __any_sync(0xffffffffu, missing);

@@ -1,0 +1,37 @@
+"""The chunk operators at their edges, against the definition in 64 bits.
+
+Tolerances are those of test_gpu_chunk.py.  Where values of very different magnitude are summed, an output is held
+to 1e-5 of sum_j p_j |V_j|, the weighted sum of magnitudes: a score is off by less than 2e-6 (a few
+2^-24 sum|q k| scale, below 10 here) and so a weight by 4e-6 of itself in numerator and sum together, the exponential
+and the 22 bits of a value add less than 1e-6."""
+import numpy as np
+import pytest
+
+from test_gpu_chunk import Batch, m, rng  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------- values of far apart magnitudes
+def magnitude_sums(b):
+    """sum_j p_j |V_j| of every output."""
+    v, b.v = b.v, np.abs(b.v)
+    sums = b.ref()
+    b.v = v
+    return sums
+
+
+@pytest.mark.parametrize("new", [[40, 2], [3]])
+@pytest.mark.parametrize("past", [10, 400, 3000])
+def test_values_near_the_largest(m, new, past):
+    # fp32 rows up to 1.5e38 beside rows of zeros: the weighted sum is finite, the sum of many such values is not
+    for by_tile in (False, True):
+        b = Batch((14, 2, 64, 64), "f32", new, [past, 5][:len(new)], paged=False, seed=100)
+        zero = rng(100, past).random(b.pool_rows) < 0.5
+        if by_tile:
+            zero = (np.arange(b.pool_rows) // 128) % 2 == 0
+        b.v[zero] = 0
+        b.v *= np.float32(3e37)
+        got, err = b.run(m)
+        d = np.abs(got - b.ref())
+        assert np.isfinite(got).all() and (d <= 1e-5 * magnitude_sums(b)).all() and err == 0
