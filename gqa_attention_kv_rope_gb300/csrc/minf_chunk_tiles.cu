@@ -26,6 +26,9 @@
 // V_j = V'_j 2^e_j, and the softmax runs on t_j = s_j + e_j, so P'_j = 2^(t_j - M) weighs V'_j and
 // P'_j 2^-e_j is the term of the sum: a large row cannot push the others out of binary16's range for
 // the rows that do not see it.  (Rows below 2^-46 keep the scale 2^60: what they lose is below 2^-70.)
+// A term of the sum goes through P'_j, which is lost below 2^-126: where the exponents of the tiles that a row goes
+// over are more than kSpan apart (fp32 rows alone can be) the row is computed again by its definition.  Within
+// kSpan what is lost scores at least 126 - kSpan below the row's best key: a weight below 2^-46.
 // Where a tile's rows are within 2^16 of its largest, as they nearly always are, one factor serves the
 // whole tile (its small rows still have all their 22 bits) and the row threads need no factor a key:
 // those would take half of the shared-memory bandwidth.
@@ -69,6 +72,7 @@ constexpr int kScoreWarp = 0, kKeyWarp = 1, kValueWarp = 2, kQueryWarp = 3;
 // P is at most 2^kShift, and lo keeps it to 2^-25: n keys that all lose as much are off by n 2^-25 of a sum of
 // at least 2^kShift (2^-23 for 2^17 of them).
 constexpr float kShift = 15.0f;
+constexpr int kSpan = 80;
 // TMEM columns: the S buffers (P over them: of each 32 keys hi, then lo, two keys a column), O of a tile, Q (hi,
 // then lo, two dims a column)
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kTmemCols = 512;
@@ -119,6 +123,7 @@ struct Smem {
         float exp, fac;  // the tile's: V's e and 2^-e; K's factor in fac
         int by_row;      // its rows have their own
     } k_tile[C::HL ? 4 : 1], v_tile[C::HL ? 4 : 1];
+    int2 v_span[C::HL ? 4 : 1], span;  // V's smallest and largest exponents: of a tile, of the segment
     uint32_t tmem_base;
     int abort_flag, last;
     // the row threads lead the two issuing warps (which would need registers to walk on their own): tiles of
@@ -197,6 +202,9 @@ __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ void st_shared(uint32_t addr, const uint32_t (&u)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
 }
+
+// Floats of a part: O, the rows' maxima and sums, V's exponents.
+__host__ __device__ constexpr size_t part_floats(int hd) { return static_cast<size_t>(BM) * (hd + 2) + 4; }
 
 // Byte offset of the 16-byte chunk c of a row in a 128-byte-swizzled slab.
 __device__ __forceinline__ uint32_t sw16(int row, int c) {
@@ -543,13 +551,17 @@ __device__ __forceinline__ void split_tiles(Smem<HD, T> &sm, const AttnParams &p
             most = max(most, o.y);
         }
         by_row = most - least > 16;  // (no row at all: not row by row)
-        if (!by_row) sh = least == none ? 0 : least;
+        // (a row of zeros goes by the largest row's: any will do for its values, and its weight stays)
+        if (!by_row || !(am > 0.0f)) sh = least == none ? 0 : least;
         if (head < 0) return true;
         // V's exponents out
         if (kv) {
             if (by_row) sm.v_exp[slot][my_row] = static_cast<float>(-sh);
             if (by_row || !Q) sm.v_inv[slot][my_row] = pow2i(sh);
-            if (warp == 0 && lane == 16) sm.v_tile[slot] = {by_row ? 0.0f : static_cast<float>(-sh), by_row ? 1.0f : pow2i(sh), by_row};
+            if (warp == 0 && lane == 16) {
+                sm.v_tile[slot] = {by_row ? 0.0f : static_cast<float>(-sh), by_row ? 1.0f : pow2i(sh), by_row};
+                sm.v_span[slot] = by_row ? make_int2(-most, -least) : make_int2(-sh, -sh);
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.v_stat[slot]);
@@ -716,6 +728,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
     using C = Cfg<HD, T>;
     constexpr int PARTS = C::PARTS, COLS = C::COLS, DIMS = C::DIMS;  // keys and dims of a thread
     constexpr int OD = 32 / PARTS;                                    // dims of a part in an output pass
+    constexpr bool F32 = std::is_same<T, float>::value;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int part = warp >> 2, row = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -778,6 +791,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             const long long first = walk_pos(w, p), last = first + w.cnt - 1;
             const long long lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
             const long long hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
+            sm.span = make_int2(0x7fff, -0x7fff);
             sm.all = make_int2(lo < 0x7fffffff ? static_cast<int>(lo) : 0x7fffffff, hi > 0 ? static_cast<int>(hi) : 0);
             // the next segment
             Walk next = w;
@@ -816,6 +830,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     chunk_wait(&sm.k_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     chunk_wait(&sm.v_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     const auto fk = sm.k_tile[q & 3], fv = sm.v_tile[q & 3];
+                    if (F32 && tid == 0) sm.span = make_int2(min(sm.span.x, sm.v_span[q & 3].x), max(sm.span.y, sm.v_span[q & 3].y));
                     k_rows = fk.by_row, v_rows = fv.by_row;
                     cc = c * fk.fac;  // (1, 0 and 1 where they are row by row)
                     ve = fv.exp;
@@ -967,6 +982,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         };
         bool finish = whole, odd = false, again = false;
         if (whole) {
+            if (F32) odd = sm.span.y - sm.span.x > kSpan;
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
             for (int d = 0; d < DIMS; d += 16) {
@@ -981,8 +997,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 for (int e = 0; e < 16; e += OD) put(y + e, d + e);
             }
         } else {
-            // this stretch's part: O as [dims / 4][rows] float4, then the rows' maxima and sums
-            constexpr size_t kPart = static_cast<size_t>(BM) * (HD + 2);
+            // this stretch's part: O as [dims / 4][rows] float4, then the rows' maxima and sums and V's exponents
+            constexpr size_t kPart = part_floats(HD);
             float *mine = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (w.u0 == 0 ? 1 : 0)) * kPart;
             if (live) {
 #pragma unroll
@@ -994,6 +1010,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     mine[BM * (HD + 1) + row] = l;
                 }
             }
+            if (F32 && tid == 0) *reinterpret_cast<int2 *>(mine + BM * (HD + 2)) = sm.span;
             int b0, b1;
             walk_parts(w, p, b0, b1);
             named_sync(1, C::kRowThreads);
@@ -1008,6 +1025,15 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 // join the parts in the order of their keys (dead rows read what is there and are not put); two
                 // parts' loads are in flight at a time
                 constexpr int JD = C::HL ? 32 : DIMS;  // dims of a pass
+                if (F32) {
+                    int2 span = sm.span;
+                    for (int b = b0; b <= b1; ++b) {
+                        const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
+                        const int2 o = __ldcg(reinterpret_cast<const int2 *>(q + BM * (HD + 2)));
+                        span = make_int2(min(span.x, o.x), max(span.y, o.y));
+                    }
+                    odd = span.y - span.x > kSpan;
+                }
 #pragma unroll 1
                 for (int d0 = 0; d0 < DIMS; d0 += JD) {
                     float M = -INFINITY, L = 0.0f;
@@ -1191,7 +1217,7 @@ int launch(const AttnParams &p, int grid, cudaStream_t s) {
 }
 
 PlanLayout tiles_layout(int nt, int n_seq, int nh, int nk, int hd_kv) {
-    return plan_layout(nt, n_seq, BM / (nh / nk), sm_count(), static_cast<size_t>(BM) * (hd_kv + 2) * sizeof(float));
+    return plan_layout(nt, n_seq, BM / (nh / nk), sm_count(), part_floats(hd_kv) * sizeof(float));
 }
 
 }  // namespace

@@ -35,3 +35,30 @@ def test_values_near_the_largest(m, new, past):
         got, err = b.run(m)
         d = np.abs(got - b.ref())
         assert np.isfinite(got).all() and (d <= 1e-5 * magnitude_sums(b)).all() and err == 0
+
+
+@pytest.mark.parametrize("new", [[40, 2], [3]])
+@pytest.mark.parametrize("past", [10, 60, 400, 3000])
+@pytest.mark.parametrize("sizes", [(0.0, 1.0, 1e30), (0.0, 1e-20, 1.0, 1e30), (1e-20, 1e20)])
+def test_values_of_all_magnitudes_keep_their_weights(m, new, past, sizes):
+    # fp32 rows, side by side in one tile and tile by tile
+    for by_tile in (False, True):
+        b = Batch((14, 2, 64, 64), "f32", new, [past, 5][:len(new)], paged=False, seed=101)
+        pick = rng(101, past).integers(0, len(sizes), b.pool_rows)
+        if by_tile:
+            pick = (np.arange(b.pool_rows) // 128) % len(sizes)
+        b.v = (b.v * np.array(sizes)[pick][:, None]).astype(np.float32)
+        got, err = b.run(m)
+        d = np.abs(got - b.ref())
+        assert np.isfinite(got).all() and (d <= 1e-5 * magnitude_sums(b) + 1e-25).all() and err == 0
+
+
+def test_a_row_of_zeros_beside_a_large_one_is_a_third(m):
+    # equal scores, V rows 0, 1 and 1e30: a third of 1e30, for tokens that see the three
+    b = Batch((14, 2, 64, 64), "f32", [40], [0], paged=False, seed=102)
+    b.q[:] = 0
+    b.v[:] = 0
+    b.v[b.row(0, 1)], b.v[b.row(0, 2)] = 1.0, 1e30
+    got, err = b.run(m)
+    want = np.array([0.0, 0.5] + [1e30 / (i + 1) for i in range(2, 40)])[:, None]
+    assert (np.abs(got - want) <= 1e-6 * want).all() and err == 0
