@@ -104,5 +104,10 @@ __device__ __forceinline__ float4 row_ld4(const void *base, long long row, int W
 __device__ __forceinline__ bool chunk_sees(long long p, int j, int window, int n_sink) {
     return j <= p && (window == 0 || j > p - window || j < n_sink);
 }
+// Whether it sees any of the sequence's rows 0 .. cap-1.
+__device__ __forceinline__ bool chunk_sees_any(long long p, int cap, int window, int n_sink) {
+    const long long last = p < cap - 1 ? p : cap - 1;
+    return last >= 0 && (window == 0 || last > p - window || n_sink > 0);
+}
 
 }  // namespace minf

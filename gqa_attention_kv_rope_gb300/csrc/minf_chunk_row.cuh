@@ -98,9 +98,11 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
             }
         }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * kValueScale);  // nothing visible: zeros
+    // nothing visible: zeros.  Nothing but scores of minus infinity: 0 / 0, as the softmax of such rows is.
+    const bool none = !chunk_sees_any(job.p, job.rows.cap, window, n_sink);
+    const float inv = 1.0f / (l * kValueScale);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) job.out[lane * PER + i] = l == 0.0f ? 0.0f : acc[i] * inv;
+    for (int i = 0; i < PER; ++i) job.out[lane * PER + i] = none ? 0.0f : acc[i] * inv;
     return __any_sync(0xffffffffu, missing);
 }
 

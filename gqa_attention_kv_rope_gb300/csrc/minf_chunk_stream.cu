@@ -745,12 +745,13 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                 for (int e = 0; e < 2; ++e) {
                     const int r = t * 8 + 2 * c4 + e;
                     if (warp >= MT || r >= rows) continue;
-                    const float inv = L[t][e] == 0.0f ? 0.0f : 1.0f / L[t][e];
+                    const bool empty = L[t][e] == 0.0f;  // it sees nothing, or nothing but scores of minus infinity
+                    const float inv = empty ? 0.0f : 1.0f / L[t][e];
                     float *out = p.a.out + (static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g) * HD;
-                    bool bad = false;
+                    bool bad = empty && (mt.lim[r].y < mt.lim[r].x || mt.lim[r].z > 0);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float y = L[t][e] == 0.0f ? 0.0f : res[t][2 * h + e] * inv;
+                        const float y = empty ? 0.0f : res[t][2 * h + e] * inv;
                         const int d = C::Q || C::F32 ? (warp >> 1) * 32 + 4 * n8 + 2 * (warp & 1) + h : warp * 16 + n8 + 8 * h;
                         out[d] = y;
                         bad |= !(fabsf(y) < INFINITY);

@@ -981,8 +981,11 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             named_sync(1, C::kRowThreads);
         };
         bool finish = whole, odd = false, again = false;
+        // a row whose sum is zero sees nothing, or nothing but scores of minus infinity
+        auto sees = [&]() { return live && chunk_sees_any(walk_pos(w, p) + sm.token[row], w.rows.cap, p.a.window, p.a.n_sink); };
         if (whole) {
             if (F32) odd = sm.span.y - sm.span.x > kSpan;
+            if (l == 0.0f) odd |= sees();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll
             for (int d = 0; d < DIMS; d += 16) {
@@ -1059,6 +1062,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                             y[4 * d + 3] = y[4 * d + 3] * fo + x[d].w * fn;
                         }
                     }
+                    if (L == 0.0f) odd |= sees();
                     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
                     for (int d = 0; d < JD; ++d) {

@@ -602,7 +602,8 @@ MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f1
  *   j visible: 0 <= j <= min(p, cap - 1), and window == 0 or j > p - window or j < n_sink.
  * window: positions each token sees back, itself included (0: no limit); n_sink: first rows of
  * the sequence that stay visible beside the window (n_sink 0: none; without a window it changes
- * nothing).  A token that sees nothing (p < 0) gets zeros.  Values in rows that a token does not
+ * nothing).  A token that sees nothing (p < 0) gets zeros; one that sees nothing but scores of minus
+ * infinity gets NaN, the softmax of such a row.  Values in rows that a token does not
  * see, infinities and NaN among them, do not reach its result.  The new tokens' own rows must
  * have been stored.  q [nt, n_head, hd] is rotated; out [nt, n_head*hd_kv], which must not overlap q.
  * minf_gqa_attn_chunk_paged reads paged pools; minf_gqa_attn_window reads contiguous regions:

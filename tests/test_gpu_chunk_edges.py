@@ -7,7 +7,7 @@ and the 22 bits of a value add less than 1e-6."""
 import numpy as np
 import pytest
 
-from test_gpu_chunk import Batch, m, rng  # noqa: F401
+from test_gpu_chunk import KINDS, Batch, check, m, rng  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,45 @@ def test_a_row_of_zeros_beside_a_large_one_is_a_third(m):
     got, err = b.run(m)
     want = np.array([0.0, 0.5] + [1e30 / (i + 1) for i in range(2, 40)])[:, None]
     assert (np.abs(got - want) <= 1e-6 * want).all() and err == 0
+
+
+# ----------------------------------------------------------------------------- scores that are minus infinity
+def minus_infinity(b, rows):
+    """Keys of score minus infinity (b.q's first values are positive)."""
+    b.q[:, :, :32] = np.abs(b.q[:, :, :32]) + np.float32(0.1)
+    for r in rows:
+        if b.kind == "q8":  # a block's scale: its quants are ones
+            for h in range(b.geom[1]):
+                b.k[r, h * b.geom[3]:h * b.geom[3] + 32] = 1
+                at = b.w + h * (b.geom[3] // 32) * 2
+                b.k[r, at:at + 2] = np.array([-np.inf], np.float16).view(np.uint8)
+        else:
+            b.k[r, ::b.geom[3]] = -np.inf
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new", [[1, 1], [3, 1], [40, 2]])
+@pytest.mark.parametrize("geom", [(14, 2, 64, 64), (16, 8, 128, 128)], ids=str)
+def test_rows_whose_every_visible_score_is_minus_infinity(m, kind, new, geom):
+    # without a past: the first token sees one key.  The softmax of nothing but minus infinities is not a number.
+    b = Batch(geom, kind, new, [0, 30], paged=True, block=16, seed=103)
+    minus_infinity(b, [b.row(0, 0)])
+    got = check(m, b)
+    assert np.isnan(got[0]).all() and np.isfinite(got[1:]).all()
+    # a window that holds such keys alone, and sinks that are such keys
+    for window, sinks in ((6, 0), (6, 2)):
+        b = Batch(geom, kind, new, [150, 30], paged=False, seed=104, window=window, sinks=sinks)
+        minus_infinity(b, [b.row(0, j) for j in list(range(sinks)) + list(range(140, 155))])
+        got = check(m, b)
+        assert np.isnan(got[0]).all() and np.isfinite(got[new[0]:]).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_of_minus_infinity_over_many_parts(m, kind):
+    # all of a long row's keys: the parts that are joined are all empty
+    b = Batch((14, 2, 64, 64), kind, [1], [3000], paged=True, block=64, seed=105)
+    minus_infinity(b, range(b.pool_rows))
+    assert np.isnan(check(m, b)).all()
+    b = Batch((14, 2, 64, 64), kind, [20], [3000], paged=False, seed=106)
+    minus_infinity(b, range(b.pool_rows))
+    assert np.isnan(check(m, b)).all()
