@@ -5,7 +5,9 @@
 // group's weighted V rows for its own dimensions, leaving out the hidden ones, so that nothing a
 // hidden row holds (infinities, NaN, whatever an unwritten row has) reaches the result.  Weights are
 // at most 1 and a row has fewer than 2^31 keys, so with the weights of V taken 2^-32 times no sum of
-// finite values passes the range of fp32 (a term below 2^-117 of an output is lost).
+// finite values passes the range of fp32 (a term below 2^-117 of an output is lost).  Nor does a
+// score of finite rows: one that does is summed again from operands 2^-66 times, and maxima and
+// differences of scores are taken in 64 bits.
 #pragma once
 
 #include "minf_chunk.cuh"
@@ -22,13 +24,31 @@ struct RowJob {
 
 constexpr float kValueScale = 2.3283064365386963e-10f;  // 2^-32
 
+// q . K[row] of one kv head, both times `f`.
+template <typename T, int HD>
+__device__ __forceinline__ float attn_dot(const ChunkKv &c, const float *q, long long row, int hk, float f) {
+    constexpr int D4 = HD / 4;
+    const float4 *q4 = reinterpret_cast<const float4 *>(q);
+    float s = 0.0f;
+#pragma unroll 4
+    for (int d = 0; d < D4; ++d) {
+        const float4 k = row_ld4<T>(c.k, row, c.W, c.row_bytes, hk * D4 + d), x = __ldg(q4 + d);
+        s = fmaf(x.x * f, k.x * f, s);
+        s = fmaf(x.y * f, k.y * f, s);
+        s = fmaf(x.z * f, k.z * f, s);
+        s = fmaf(x.w * f, k.w * f, s);
+    }
+    return s;
+}
+
 // Returns (in every lane) whether a block the row sees is missing; its rows count as zeros.
 template <typename T, int HD>
 __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float scale_log2, int window, int n_sink) {
     constexpr int D4 = HD / 4, PER = HD / 32;  // values a lane owns
     const int lane = threadIdx.x & 31;
     const long long last = job.p < job.rows.cap - 1 ? job.p : job.rows.cap - 1;  // last visible key
-    float m = -INFINITY, l = 0.0f, acc[PER];
+    double m = -INFINITY;
+    float l = 0.0f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
     bool missing = false;
@@ -44,28 +64,21 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
             row = seq_row(c, job.rows, j);
             if (row < 0) missing = true;
         }
-        float s = 0.0f;
+        double s = 0.0;
         if (row >= 0) {
-            const float4 *q4 = reinterpret_cast<const float4 *>(job.q);
-#pragma unroll 4
-            for (int d = 0; d < D4; ++d) {
-                const float4 k = row_ld4<T>(c.k, row, c.W, c.row_bytes, job.hk * D4 + d), q = __ldg(q4 + d);
-                s = fmaf(q.x, k.x, s);
-                s = fmaf(q.y, k.y, s);
-                s = fmaf(q.z, k.z, s);
-                s = fmaf(q.w, k.w, s);
-            }
+            const float x = attn_dot<T, HD>(c, job.q, row, job.hk, 1.0f);
+            s = x;
+            if (!(fabsf(x) < INFINITY)) s = static_cast<double>(attn_dot<T, HD>(c, job.q, row, job.hk, 0x1p-66f)) * 0x1p132;
         }
         s = see ? s * scale_log2 : -INFINITY;
-        float mx = s;
+        double mx = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const float t = __shfl_xor_sync(0xffffffffu, mx, o);
+            const double t = __shfl_xor_sync(0xffffffffu, mx, o);
             mx = mx > t || mx != mx ? mx : t;  // a NaN score stays
         }
-        const float mn = m > mx || m != m ? m : mx;
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float corr = exp2f(m - base), pr = see ? exp2f(s - base) : 0.0f;
+        const double mn = m > mx || m != m ? m : mx, base = mn == -INFINITY ? 0.0 : mn;
+        const float corr = exp2f(static_cast<float>(m - base)), pr = see ? exp2f(static_cast<float>(s - base)) : 0.0f;
         m = mn;
         float sum = pr;
 #pragma unroll

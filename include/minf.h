@@ -618,7 +618,8 @@ MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f1
  * must not.
  * Sums and softmax statistics are fp32; products run on the tensor cores with operands split into
  * halves whose sum carries 22 bits or more (softmax weights below 2^-15 of a row's largest: 2^-37 of it).
- * A row that sees an infinity or a NaN is computed again key by key: right, but slow.
+ * A row that sees an infinity or a NaN, or whose scores pass the range of fp32, is computed again key
+ * by key: right, but slow.
  * Device errors: MINF_ERRBIT_ATTN_POS (p < 0, or p >= cap: the window is clamped to cap), _BLOCK
  * (a visible row's block is missing: read as zeros), _CHUNK (nothing written), _TIMEOUT.
  * Errors: as minf_gqa_attn_decode; MINF_ERR_ARG for window < 0, n_sink < 0, max_chunk <= 0,

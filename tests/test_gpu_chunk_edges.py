@@ -104,3 +104,13 @@ def test_rows_of_minus_infinity_over_many_parts(m, kind):
     b = Batch((14, 2, 64, 64), kind, [20], [3000], paged=False, seed=106)
     minus_infinity(b, range(b.pool_rows))
     assert np.isnan(check(m, b)).all()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 2]])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_scores_past_the_range_of_fp32(m, new, sign):
+    # finite rows whose products are not: about 1e40, 1e38 and more apart, so that one key has all of the weight
+    b = Batch((14, 2, 64, 64), "f32", new, [70, 0], paged=True, block=16, seed=107)
+    b.q = (np.abs(b.q) + 0.1).astype(np.float32) * np.float32(1e19)
+    b.k = (sign * (np.abs(b.k) + 0.1) * 1e20).astype(np.float32)
+    check(m, b, scale=1.0)
