@@ -762,9 +762,10 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
 #pragma unroll
             for (int k = 1; k < PARTS; ++k) am = fmaxf(am, sm.sum[k][row]);
             const int sh = row_shift(am, 126);
-            const float f = p.scale_log2 < 0.0f ? -pow2i(sh) : pow2i(sh);
+            const float f = p.scale_log2 < 0.0f ? -pow2i(sh) : p.scale_log2 == 0.0f ? 0.0f : pow2i(sh);
             // S * c is the score in powers of two, c > 0: a row's largest S is its largest score (the sign of
-            // the caller's scale is Q's; a scale of zero is the smallest one, so that hidden keys' -infinity stays)
+            // the caller's scale is Q's, and so is a scale of zero: times an infinite key it is not a number; c is
+            // then the smallest one, so that hidden keys' -infinity stays)
             c = fabsf(p.scale_log2) * pow2i(-sh);
             if (c == 0.0f) c = __uint_as_float(1u);
             constexpr int QD = DIMS < 32 ? DIMS : 32;  // dims of a store: half as many columns

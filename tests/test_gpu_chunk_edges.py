@@ -114,3 +114,13 @@ def test_scores_past_the_range_of_fp32(m, new, sign):
     b.q = (np.abs(b.q) + 0.1).astype(np.float32) * np.float32(1e19)
     b.k = (sign * (np.abs(b.k) + 0.1) * 1e20).astype(np.float32)
     check(m, b, scale=1.0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new", [[1], [40]])
+def test_a_scale_of_zero_times_an_infinite_score(m, kind, new):
+    b = Batch((14, 2, 64, 64), kind, new, [70], paged=True, block=16, seed=108)
+    minus_infinity(b, [b.row(0, 70)])
+    with np.errstate(invalid="ignore"):
+        got = check(m, b, scale=0.0)
+    assert np.isnan(got).all()
