@@ -34,8 +34,8 @@ long long row_bytes_of(int kv, int W) { return kv == kKvQ8 ? q8_row_bytes(W) : (
 constexpr long long kMaxRowsKv = 0x7fffffffLL - 4096;
 
 int set_paged(ChunkKv *c, const void *k, const void *v, int kv, int64_t pool_rows, int W, const int32_t *table,
-              int max_blocks, int block_rows) {
-    if (!ok_f(k) || !ok_f(v) || !table || pool_rows <= 0 || max_blocks <= 0) return MINF_ERR_ARG;
+              int max_blocks, int block_rows, int n_seq) {
+    if (!ok_f(k) || !ok_f(v) || (!table && n_seq != 0) || pool_rows <= 0 || max_blocks <= 0) return MINF_ERR_ARG;
     if (block_rows < 16 || block_rows > 4096 || (block_rows & (block_rows - 1))) return MINF_ERR_UNSUPPORTED;
     if (pool_rows % block_rows || static_cast<long long>(max_blocks) * block_rows > kMaxRowsKv || pool_rows > kMaxRowsKv)
         return MINF_ERR_UNSUPPORTED;
@@ -61,8 +61,11 @@ bool overlap(const float *a, size_t na, const float *b, size_t nb) {
 }
 
 bool ok_seqs(const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq) {
-    return n_past && nt >= 0 && n_seq >= 0 && (chunk_off || nt == n_seq);
+    return (n_past || n_seq == 0) && nt >= 0 && n_seq >= 0 && (chunk_off || nt == n_seq);
 }
+
+// Arrays of nt rows: of no rows they may be null, as empty tensors are.
+bool ok_rows(const void *p, int nt) { return p ? aligned16(p) : nt == 0; }
 
 int rope_store(float *q_out, float *k_out, const float *q, const float *k, const float *v, const int32_t *rope_pos,
                int n_axis, const uint8_t *pair_axis, const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq,
@@ -73,9 +76,9 @@ int rope_store(float *q_out, float *k_out, const float *q, const float *k, const
     if (st != MINF_OK) return st;
     if (hd % 8) return MINF_ERR_UNSUPPORTED;
     ChunkStoreArgs a = {};
-    st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows);
+    st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows, n_seq);
     if (st != MINF_OK) return st;
-    if (!ok_f(q_out) || (k_out && !ok_f(k_out)) || !ok_f(q) || !ok_f(k) || !ok_f(v) || !err ||
+    if (!ok_rows(q_out, nt) || (k_out && !ok_f(k_out)) || !ok_rows(q, nt) || !ok_rows(k, nt) || !ok_rows(v, nt) || !err ||
         !ok_seqs(chunk_off, n_past, nt, n_seq) || (style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd))
         return MINF_ERR_ARG;
     a.q_out = q_out;
@@ -102,9 +105,9 @@ int read_rows(void *k_rows, void *v_rows, int rows_f16, const void *k_pool, cons
     if (row_width <= 0 || row_width > (1 << 20) || row_width % (kv == kKvQ8 ? 32 : kv == kKvF16 ? 8 : 4)) return MINF_ERR_ARG;
     if (rows_f16 && row_width % 8) return MINF_ERR_ARG;
     ChunkReadArgs a = {};
-    const int st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, row_width, table, max_blocks, block_rows);
+    const int st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, row_width, table, max_blocks, block_rows, n_seq);
     if (st != MINF_OK) return st;
-    if (!ok_f(k_rows) || !ok_f(v_rows) || !err || !ok_seqs(chunk_off, n_past, nt, n_seq)) return MINF_ERR_ARG;
+    if (!ok_rows(k_rows, nt) || !ok_rows(v_rows, nt) || !err || !ok_seqs(chunk_off, n_past, nt, n_seq)) return MINF_ERR_ARG;
     a.k_rows = k_rows;
     a.v_rows = v_rows;
     a.f16 = rows_f16 != 0;
@@ -117,7 +120,7 @@ int read_rows(void *k_rows, void *v_rows, int rows_f16, const void *k_pool, cons
 int attention(ChunkAttnArgs &a, float *out, const float *q, const int32_t *chunk_off, const int32_t *n_past, int nt,
               int n_seq, int max_chunk, int nh, int nk, int hd, int hd_kv, float scale, int window, int n_sink, void *ws,
               size_t ws_bytes, int32_t *err, minf_stream_t stream) {
-    if (!ok_f(out) || !ok_f(q) || !err || !ok_seqs(chunk_off, n_past, nt, n_seq) || max_chunk <= 0 || window < 0 ||
+    if (!ok_rows(out, nt) || !ok_rows(q, nt) || !err || !ok_seqs(chunk_off, n_past, nt, n_seq) || max_chunk <= 0 || window < 0 ||
         n_sink < 0)
         return MINF_ERR_ARG;
     if (nt == 0 || n_seq == 0) return MINF_OK;
@@ -148,7 +151,7 @@ int attn_paged(float *out, const float *q, const void *k_pool, const void *v_poo
     int st = check_geometry(nh, nk, hd, hd_kv);
     if (st != MINF_OK) return st;
     ChunkAttnArgs a = {};
-    st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows);
+    st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows, n_seq);
     if (st != MINF_OK) return st;
     return attention(a, out, q, chunk_off, n_past, nt, n_seq, max_chunk, nh, nk, hd, hd_kv, scale, window, n_sink, ws,
                      ws_bytes, err, stream);
@@ -188,10 +191,11 @@ int layer_step(float *xn, const float *h, const float *gain, float eps, int n_em
     if (st != MINF_OK) return st;
     // everything is checked before the first launch
     ChunkKv c;
-    st = set_paged(&c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows);
+    st = set_paged(&c, k_pool, v_pool, kv, pool_rows, nk * hd_kv, table, max_blocks, block_rows, n_seq);
     if (st != MINF_OK) return st;
     if (hd % 8) return MINF_ERR_UNSUPPORTED;
-    if (!xn || !h || n_embd <= 0 || !ok_f(q) || !ok_f(k) || !ok_f(v) || !ok_f(out) || !err ||
+    if (((!xn || !h) && nt != 0) || n_embd <= 0 || !ok_rows(q, nt) || !ok_rows(k, nt) || !ok_rows(v, nt) ||
+        !ok_rows(out, nt) || !err ||
         !ok_seqs(chunk_off, n_past, nt, n_seq) || max_chunk <= 0 || window < 0 || n_sink < 0 ||
         (style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd))
         return MINF_ERR_ARG;
@@ -215,7 +219,7 @@ extern "C" {
 
 int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt, int n_axis, const uint8_t *pair_axis,
                    int n_head, int hd, float theta, float freq_scale, int style, int32_t *err, minf_stream_t stream) {
-    if (!y || !x || !pos || !err || nt < 0 || n_head <= 0 || hd <= 0 || (hd & 1) || hd > 2 * kMaxHalf) return MINF_ERR_ARG;
+    if (((!y || !x || !pos) && nt != 0) || !err || nt < 0 || n_head <= 0 || hd <= 0 || (hd & 1) || hd > 2 * kMaxHalf) return MINF_ERR_ARG;
     if ((style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd)) return MINF_ERR_ARG;
     if (static_cast<long long>(n_head) * hd > (1 << 20)) return MINF_ERR_UNSUPPORTED;
     RopeAxesArgs a = {y, x, pos, err, nt, n_axis, n_head, hd, style};

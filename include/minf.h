@@ -540,7 +540,8 @@ MINF_API int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt
  * belong to sequence s, and its i-th new token is at cache position p = n_past[s] + i.
  * chunk_off: int32[n_seq + 1], nondecreasing within [0, nt]; n_past: int32[n_seq]; both on the
  * device, so a captured call replays with other lengths.  chunk_off NULL: one token a sequence
- * (nt == n_seq).  A sequence may have no token.  Rows outside every chunk (padding before the
+ * (nt == n_seq).  A sequence may have no token; a call without tokens (nt 0) or without sequences does
+ * nothing, and the arrays that have no elements then may be null.  Rows outside every chunk (padding before the
  * first or behind the last) are neither read into a result nor written.
  * Pools, block_table, max_blocks, block_rows and pool_rows are as for the paged forms above;
  * blocks that no token needs (behind the last token, or outside its window and sinks) may be

@@ -135,3 +135,33 @@ def test_workspace_of_geometries_that_no_call_takes(lib, nh, nk):
     for max_chunk in (1, 4, 1000):
         assert lib.minf_attn_chunk_workspace_bytes(4, 2, nh, nk, 64, max_chunk) == 0
     assert lib.minf_gqa_attn_chunk_paged(*attn_args(nh=nh, nk=nk)) == 3
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+def test_calls_without_tokens_take_null_arrays(lib, end):
+    # tensors of no elements have no address
+    none = dict(out=None, q=None, nt=0)
+    for f, args in (("minf_gqa_attn_chunk_paged", attn_args), ("minf_gqa_attn_window", window_args)):
+        assert getattr(lib, f + end)(*args(**none)) == 0
+        assert getattr(lib, f + end)(*args(**none, n_seq=0, past=None)) == 0
+        assert getattr(lib, f + end)(*args(**none, n_seq=0, past=None, off=None)) == 0
+        assert getattr(lib, f + end)(*args(**none, err=None)) == 1
+        assert getattr(lib, f + end)(*args(**none, past=None)) == 1
+        assert getattr(lib, f + end)(*args(**none, k=None)) == 1
+    assert getattr(lib, "minf_gqa_attn_chunk_paged" + end)(*attn_args(**none, n_seq=0, past=None, table=None)) == 0
+    assert getattr(lib, "minf_gqa_attn_chunk_paged" + end)(*attn_args(**none, table=None)) == 1
+    a = dict(q_out=None, k_out=None, q=None, k=None, v=None, pos=None, n_axis=1, pair_axis=None, off=FAKE, past=FAKE, nt=0,
+             n_seq=2, nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, kp=FAKE, vp=FAKE, rows=256, table=FAKE,
+             max_blocks=4, block_rows=16, err=FAKE, stream=None)
+    assert getattr(lib, "minf_rope_kv_append_chunk_paged" + end)(*a.values()) == 0
+    a.update(style=2)
+    assert getattr(lib, "minf_rope_kv_append_chunk_paged" + end)(*a.values()) == 1
+    a = dict(k_rows=None, v_rows=None, f16=0, kp=FAKE, vp=FAKE, rows=256, w=128, table=FAKE, max_blocks=4, block_rows=16,
+             off=FAKE, past=FAKE, nt=0, n_seq=2, err=FAKE, stream=None)
+    assert getattr(lib, "minf_kv_read_chunk_paged" + end)(*a.values()) == 0
+    a = dict(xn=None, h=None, gain=None, eps=1e-6, n_embd=896, q=None, k=None, v=None, pos=None, n_axis=1, pair_axis=None,
+             off=FAKE, past=FAKE, nt=0, n_seq=2, max_chunk=4, kp=FAKE, vp=FAKE, rows=256, table=FAKE, max_blocks=4,
+             block_rows=16, nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, window=0, n_sink=0, out=None,
+             ws=None, ws_bytes=0, err=FAKE, stream=None)
+    assert getattr(lib, "minf_layer_attn_step_chunk_paged" + end)(*a.values()) == 0
+    assert lib.minf_rope_axes(None, None, None, 0, 1, None, 2, 8, 1e4, 1.0, 0, FAKE, None) == 0

@@ -6,8 +6,9 @@ to 1e-5 of sum_j p_j |V_j|, the weighted sum of magnitudes: a score is off by le
 and the 22 bits of a value add less than 1e-6."""
 import numpy as np
 import pytest
+import torch
 
-from test_gpu_chunk import KINDS, Batch, check, m, rng  # noqa: F401
+from test_gpu_chunk import END, KINDS, Batch, check, i32, m, q8_row_bytes, rng  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +125,31 @@ def test_a_scale_of_zero_times_an_infinite_score(m, kind, new):
     with np.errstate(invalid="ignore"):
         got = check(m, b, scale=0.0)
     assert np.isnan(got).all()
+
+
+# ----------------------------------------------------------------------------- nothing to do
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n_seq", [0, 2])
+def test_calls_without_tokens(m, kind, n_seq):
+    # a step in which no sequence has a new token: tensors of no elements have no address
+    nh, nk, hd, hd_kv = 14, 2, 64, 64
+    w, end = nk * hd_kv, END[kind]
+    dt = {"f32": torch.float32, "f16": torch.float16, "q8": torch.uint8}[kind]
+    kp, vp = (torch.zeros(64, q8_row_bytes(w) if kind == "q8" else w, dtype=dt, device="cuda") for _ in range(2))
+    q, k, v, out, h, xn = (torch.empty(0, c, device="cuda") for c in (nh * hd, w, w, nh * hd_kv, 896, 896))
+    table, off = torch.zeros(n_seq, 2, dtype=torch.int32, device="cuda"), torch.zeros(n_seq + 1, dtype=torch.int32, device="cuda")
+    past, err = torch.zeros(n_seq, dtype=torch.int32, device="cuda"), i32([0])
+    ws, pos = m.kv.chunk_workspace(0, n_seq, nh, nk, hd_kv, 1), torch.empty(3, 0, dtype=torch.int32, device="cuda")
+    axis = [0] * 10 + [1] * 10 + [2] * 12
+    m.minf_rope_axes(q, q, pos, axis, nh, hd, 1e6, 1.0, 0, err)
+    for p, a in ((None, None), (pos, axis)):
+        getattr(m, "minf_rope_kv_append_chunk_paged" + end)(q, k, q, k, v, p, a, off, past, nh, nk, hd, hd_kv, 1e6, 1.0, 0, kp,
+                                                            vp, table, 16, err)
+    getattr(m, "minf_kv_read_chunk_paged" + end)(k, v, kp, vp, table, 16, off, past, err)
+    getattr(m, "minf_gqa_attn_chunk_paged" + end)(out, q, kp, vp, table, 16, off, past, 1, nh, nk, hd, hd_kv, 0.1, 0, 0, ws, err)
+    getattr(m, "minf_gqa_attn_window" + end)(out, q, kp, vp, torch.zeros(n_seq, dtype=torch.int64, device="cuda"), None, 32, off,
+                                             past, 1, nh, nk, hd, hd_kv, 0.1, 4, 1, ws, err)
+    getattr(m, "minf_layer_attn_step_chunk_paged" + end)(xn, h, None, 1e-6, q, k, v, None, None, off, past, 1, kp, vp, table, 16,
+                                                         nh, nk, hd, hd_kv, 1e6, 1.0, 0, 0, 0, out, ws, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and not kp.any() and not vp.any()
