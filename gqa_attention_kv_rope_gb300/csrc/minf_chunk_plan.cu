@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
             if (w < warp) here += y;
             before += y;
         }
-        if (s < a.sq.n_seq) seq_units[s] = here;
+        if (s < a.sq.n_seq) seq_units[s] = a.seq_units[s] = here;  // (the walks look it up there)
         __syncthreads();  // warp_sum is free for the next pass
     }
     if (reported) flag_error(a.err, MINF_ERRBIT_ATTN_POS);
@@ -120,15 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     long long in_tile = 0, item = 0;
     const long long *tu = nullptr;
     auto locate = [&]() {  // the item of unit x and its place there
-        int r = a.sq.n_seq;  // the last sequence that starts at or before x (it has units: x is below the total)
-        l = 0;
-        while (r - l > 1) {
-            const int mid = (l + r) >> 1;
-            if (seq_units[mid] <= x)
-                l = mid;
-            else
-                r = mid;
-        }
+        l = seq_of_unit(seq_units, a.sq.n_seq, x);
         int lo, hi;
         chunk_rows(a.sq.off, a.sq.nt, l, lo, hi);
         tu = tile_units + tile_base(lo, l, a.tt);

@@ -79,7 +79,7 @@ struct PlanArgs {
     PlanHead *head;
     PlanStart *starts;        // [max_ctas]
     int *tickets;             // [max_ctas]
-    long long *seq_units;     // [n_seq + 1] units of the sequences before s
+    long long *seq_units;     // [n_seq] units of the sequences before s
     long long *tile_units;    // units of a sequence's token tiles up to and with this one, one kv head
     int32_t *err;
 };
@@ -108,6 +108,20 @@ inline PlanLayout plan_layout(int nt, int n_seq, int tt, int max_ctas, size_t pa
     return l;
 }
 
+// The sequence of unit x (below the total): the last that starts at or before it (those that the plan does not take
+// have no units).
+__device__ __forceinline__ int seq_of_unit(const long long *seq_units, int n_seq, long long x) {
+    int l = 0, r = n_seq;
+    while (r - l > 1) {
+        const int mid = l + ((r - l) >> 1);
+        if (seq_units[mid] <= x)
+            l = mid;
+        else
+            r = mid;
+    }
+    return l;
+}
+
 // The plans of one call: that of the kernel for long chunks and that of the one for few rows, where it runs both.
 struct Plans {
     PlanArgs a[2];
@@ -120,6 +134,7 @@ struct AttnParams {
     const PlanHead *head;
     const PlanStart *starts;
     int *tickets;
+    const long long *seq_units;  // [n_seq] units of the sequences before s
     float *parts;
     float scale_log2;
     int tt, kt;       // tokens of an item, keys of a tile
@@ -152,6 +167,7 @@ inline void plan_args(PlanArgs &pl, AttnParams &p, const PlanLayout &lay, void *
     p.head = pl.head;
     p.starts = pl.starts;
     p.tickets = pl.tickets;
+    p.seq_units = pl.seq_units;
     p.parts = reinterpret_cast<float *>(ws + lay.parts);
 }
 
@@ -214,10 +230,13 @@ __device__ __forceinline__ bool walk_next(Walk &w, const AttnParams &p) {
         w.tile = 0;
         if (++w.head == p.a.nk) {
             w.head = 0;
-            do {
-                ++w.seq;
+            ++w.seq;
+            walk_seq(w, p);
+            if (w.n < p.least || w.n > p.most) {
+                // sequences that another launch takes, or without tokens: however many, they are passed at once
+                w.seq = seq_of_unit(p.seq_units, p.a.sq.n_seq, p.starts[blockIdx.x].end - w.left);
                 walk_seq(w, p);
-            } while (w.n < p.least || w.n > p.most);
+            }
         }
     }
     walk_item<KT>(w, p);

@@ -153,3 +153,17 @@ def test_calls_without_tokens(m, kind, n_seq):
                                                          nh, nk, hd, hd_kv, 1e6, 1.0, 0, 0, 0, out, ws, err)
     torch.cuda.synchronize()
     assert err.item() == 0 and not kp.any() and not vp.any()
+
+
+# ----------------------------------------------------------------------------- many sequences without tokens
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("new,count", [(1, 200), (500, 2), (1, 5)])
+def test_sequences_without_tokens_between_others(m, kind, paged, new, count):
+    # 30000 sequences, most of them without tokens: a stretch of work goes from the first ones to the last
+    r, n = rng(110), 30000
+    lens, past = np.zeros(n, int), np.zeros(n, int)
+    lens[:count] = lens[-count:] = new
+    lens[[4000, 12345, 20000]] = 1, new, 2 if new > 1 else 1
+    past[lens > 0] = r.integers(0, 300, (lens > 0).sum())
+    check(m, Batch((14, 2, 64, 64), kind, lens.tolist(), past.tolist(), paged=paged, block=16, seed=110))
