@@ -6,15 +6,13 @@ namespace minf {
 
 namespace {
 
-// Query rows (tokens x heads of a kv head) up to which the streaming kernel runs alone.  Measured on 16 query
-// heads over 8 kv heads of 128 dims, 64 sequences of 4096 rows, streaming kernel and tiles: binary16 16 rows
+// The limits of minf_chunk_tiles.h.  kStreamRows and kStreamRowsF16, query rows (tokens x heads of a kv head) up to
+// which the streaming kernel runs alone: measured on 16 query heads over 8 kv heads of 128 dims, 64 sequences of 4096 rows, streaming kernel and tiles: binary16 16 rows
 // 195 and 210 us, 32 rows 363 and 212; Q8_0 32 rows 627 and 725; fp32 (16 sequences) 238 and 267.  One sequence
 // of 8192 rows, binary16: 8 rows 25 and 56, 32 rows 49 and 54.
-constexpr int kStreamRows = 32, kStreamRowsF16 = 16;
-// And in a call that also has long chunks: there the streaming kernel takes the few tokens of the others.  31
+// kFewRows, in a call that also has long chunks: there the streaming kernel takes the few tokens of the others.  31
 // single tokens beside 3 chunks of 391, Q8_0: 267 us, all in tiles 575; with the streaming kernel laid out
 // for 32 rows 533 (it computes as many for every token).
-constexpr int kFewRows = 8;
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 

@@ -847,8 +847,12 @@ int launch(const AttnParams &p, int grid, cudaStream_t s) {
 
 template <int HD, int NT>
 int launch_kind(const AttnParams &p, int grid, cudaStream_t s) {
-    if constexpr (NT < 4)  // (more than 16 rows of binary16 go to the tiles)
-        if (p.a.c.kv == kKvF16) return launch<HD, __half, NT>(p, grid, s);
+    if (p.a.c.kv == kKvF16) {
+        if constexpr (NT <= 2)
+            return launch<HD, __half, NT>(p, grid, s);
+        else
+            return MINF_ERR_UNSUPPORTED;  // (such calls go to the tiles)
+    }
     return p.a.c.kv == kKvQ8 ? launch<HD, Q8, NT>(p, grid, s) : launch<HD, float, NT>(p, grid, s);
 }
 

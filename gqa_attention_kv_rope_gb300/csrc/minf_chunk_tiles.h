@@ -7,6 +7,12 @@
 
 namespace minf {
 
+// Query rows up to which the streaming kernel runs alone, over binary16 rows and over the others, and up to which it
+// takes sequences in a batch with longer chunks (minf_chunk_attn.cu says why).  It has instances for 8, 16 and 32
+// rows, over binary16 for 8 and 16.
+constexpr int kStreamRows = 32, kStreamRowsF16 = 16, kFewRows = 8;
+static_assert(kStreamRows <= 32 && kStreamRowsF16 <= 16 && kFewRows <= 16, "instances of the streaming kernel");
+
 // 128-row tiles on the tensor cores (minf_chunk_tiles.cu), for the sequences with at least `least`
 // new tokens.
 void plan_chunk_tiles(PlanArgs &plan, AttnParams &p, const ChunkAttnArgs &a, void *workspace, int least);
