@@ -54,10 +54,19 @@ int set_paged(ChunkKv *c, const void *k, const void *v, int kv, int64_t pool_row
     return MINF_OK;
 }
 
-// Two stretches of floats share some.  (A query row is read again after parts of out are written.)
-bool overlap(const float *a, size_t na, const float *b, size_t nb) {
+// Two stretches of `bytes`-byte values share some.  (A query row is read again after parts of out are written.)
+bool overlap(const void *a, size_t na, const void *b, size_t nb, size_t bytes = sizeof(float)) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb * sizeof(float) && y < x + na * sizeof(float);
+    return x < y + nb * bytes && y < x + na * bytes;
+}
+
+// Whether the rotated rows can be written while others are read: an output is its input or apart from it (a value
+// is turned with its partner half a head away), and apart from everything else.
+bool ok_in_place(const float *out, const float *in, size_t n) { return out == in || !overlap(out, n, in, n); }
+bool ok_rope_rows(const float *q_out, const float *k_out, const float *q, const float *k, const float *v, size_t nq, size_t nk) {
+    return ok_in_place(q_out, q, nq) && !overlap(q_out, nq, k, nk) && !overlap(q_out, nq, v, nk) &&
+           (!k_out || (ok_in_place(k_out, k, nk) && !overlap(k_out, nk, q, nq) && !overlap(k_out, nk, v, nk) &&
+                       !overlap(k_out, nk, q_out, nq)));
 }
 
 bool ok_seqs(const int32_t *chunk_off, const int32_t *n_past, int nt, int n_seq) {
@@ -81,6 +90,9 @@ int rope_store(float *q_out, float *k_out, const float *q, const float *k, const
     if (!ok_rows(q_out, nt) || (k_out && !ok_f(k_out)) || !ok_rows(q, nt) || !ok_rows(k, nt) || !ok_rows(v, nt) || !err ||
         !ok_seqs(chunk_off, n_past, nt, n_seq) || (style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd))
         return MINF_ERR_ARG;
+    if (nt == 0 || n_seq == 0) return MINF_OK;
+    if (!ok_rope_rows(q_out, k_out, q, k, v, static_cast<size_t>(nt) * nh * hd, static_cast<size_t>(nt) * nk * hd_kv))
+        return MINF_ERR_ARG;
     a.q_out = q_out;
     a.k_out = k_out;
     a.q = q;
@@ -95,7 +107,6 @@ int rope_store(float *q_out, float *k_out, const float *q, const float *k, const
     a.hd_kv = hd_kv;
     a.style = style;
     a.err = err;
-    if (nt == 0 || n_seq == 0) return MINF_OK;
     return launch_chunk_store(a, theta, freq_scale, pair_axis, cs(stream));
 }
 
@@ -108,12 +119,14 @@ int read_rows(void *k_rows, void *v_rows, int rows_f16, const void *k_pool, cons
     const int st = set_paged(&a.c, k_pool, v_pool, kv, pool_rows, row_width, table, max_blocks, block_rows, n_seq);
     if (st != MINF_OK) return st;
     if (!ok_rows(k_rows, nt) || !ok_rows(v_rows, nt) || !err || !ok_seqs(chunk_off, n_past, nt, n_seq)) return MINF_ERR_ARG;
+    if (nt == 0 || n_seq == 0) return MINF_OK;
+    const size_t n = static_cast<size_t>(nt) * row_width;
+    if (overlap(k_rows, n, v_rows, n, rows_f16 ? 2 : 4)) return MINF_ERR_ARG;
     a.k_rows = k_rows;
     a.v_rows = v_rows;
     a.f16 = rows_f16 != 0;
     a.sq = {chunk_off, n_past, nt, n_seq};
     a.err = err;
-    if (nt == 0 || n_seq == 0) return MINF_OK;
     return launch_chunk_read(a, cs(stream));
 }
 
@@ -202,7 +215,9 @@ int layer_step(float *xn, const float *h, const float *gain, float eps, int n_em
     if (nt == 0 || n_seq == 0) return MINF_OK;
     if (!ws || !aligned16(ws) || ws_bytes < chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk))
         return MINF_ERR_WORKSPACE;
-    if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd)) return MINF_ERR_ARG;
+    if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd) ||
+        !ok_rope_rows(q, k, q, k, v, static_cast<size_t>(nt) * nh * hd, static_cast<size_t>(nt) * nk * hd_kv))
+        return MINF_ERR_ARG;
     st = launch_rms_norm(xn, h, gain, nt, n_embd, eps, cs(stream));
     if (st != MINF_OK) return st;
     st = rope_store(q, k, q, k, v, rope_pos, n_axis, pair_axis, chunk_off, n_past, nt, n_seq, nh, nk, hd, hd_kv, theta,
@@ -222,6 +237,7 @@ int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt, int n_a
     if (((!y || !x || !pos) && nt != 0) || !err || nt < 0 || n_head <= 0 || hd <= 0 || (hd & 1) || hd > 2 * kMaxHalf) return MINF_ERR_ARG;
     if ((style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd)) return MINF_ERR_ARG;
     if (static_cast<long long>(n_head) * hd > (1 << 20)) return MINF_ERR_UNSUPPORTED;
+    if (nt > 0 && !ok_in_place(y, x, static_cast<size_t>(nt) * n_head * hd)) return MINF_ERR_ARG;
     RopeAxesArgs a = {y, x, pos, err, nt, n_axis, n_head, hd, style};
     return launch_rope_axes(a, theta, freq_scale, pair_axis, cs(stream));
 }

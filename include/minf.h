@@ -527,7 +527,7 @@ MINF_API int minf_layer_attn_step_qkv(float *xn, const float *h, const float *ga
  * that token copied unrotated.
  * Errors: MINF_ERR_ARG for null pointers, nt < 0, n_head <= 0, odd hd, hd > 256, a style
  * not in {0, 1}, n_axis outside [1, 255], pair_axis NULL with n_axis > 1 or naming an axis
- * that is not there; MINF_ERR_UNSUPPORTED for n_head * hd above 2^20.
+ * that is not there, y overlapping x without being it; MINF_ERR_UNSUPPORTED for n_head * hd above 2^20.
  */
 MINF_API int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt, int n_axis, const uint8_t *pair_axis,
                             int n_head, int hd, float theta, float freq_scale, int style, int32_t *err,
@@ -557,14 +557,14 @@ MINF_API int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt
  * Device errors: MINF_ERRBIT_ROPE_POS (token left unrotated, still stored), _STORE_POS (position
  * outside [0, max_blocks * block_rows): rotated, not stored), _BLOCK (not stored), _CHUNK.
  * Errors: as minf_rope_axes and minf_gqa_attn_decode_paged; MINF_ERR_UNSUPPORTED also for
- * hd not a multiple of 8.
+ * hd not a multiple of 8; MINF_ERR_ARG also for an output that overlaps anything but its own input.
  *
  * minf_kv_read_chunk_paged: the rows of the chunks back from the pools, as values: row t of
  * k_rows and v_rows [nt, row_width] is the cached row of token t, in fp32 or (rows_f16) rounded
  * to binary16.  Rows of missing blocks or past the capacity come back as zeros, with
  * MINF_ERRBIT_BLOCK or MINF_ERRBIT_STORE_POS.
  * Errors: as minf_kv_append_paged; MINF_ERR_ARG also for rows_f16 with row_width not a
- * multiple of 8.
+ * multiple of 8 and for k_rows overlapping v_rows.
  */
 MINF_API int minf_rope_kv_append_chunk_paged(float *q_out, float *k_out, const float *q, const float *k, const float *v,
                                              const int32_t *rope_pos, int n_axis, const uint8_t *pair_axis,

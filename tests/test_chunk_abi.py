@@ -165,3 +165,43 @@ def test_calls_without_tokens_take_null_arrays(lib, end):
              ws=None, ws_bytes=0, err=FAKE, stream=None)
     assert getattr(lib, "minf_layer_attn_step_chunk_paged" + end)(*a.values()) == 0
     assert lib.minf_rope_axes(None, None, None, 0, 1, None, 2, 8, 1e4, 1.0, 0, FAKE, None) == 0
+
+
+Q, K, V = 1 << 20, 1 << 21, 1 << 22  # 4 rows: of 14336 bytes (14 heads of 64), of 2048 (two)
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad", [dict(q_out=Q + 16), dict(q_out=Q - 14320), dict(q_out=K), dict(q_out=V + 2032),
+                                 dict(q_out=Q, k_out=Q + 14320), dict(k_out=K + 16), dict(k_out=K - 2032), dict(k_out=V),
+                                 dict(k_out=Q), dict(q_out=1 << 23, k_out=(1 << 23) + 32)])
+def test_store_refuses_outputs_that_overlap(lib, end, bad):
+    a = dict(q_out=Q, k_out=None, q=Q, k=K, v=V, pos=None, n_axis=1, pair_axis=None, off=FAKE, past=FAKE, nt=4, n_seq=2,
+             nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, kp=FAKE, vp=FAKE, rows=256, table=FAKE, max_blocks=4,
+             block_rows=16, err=FAKE, stream=None)
+    a.update(bad)
+    assert getattr(lib, "minf_rope_kv_append_chunk_paged" + end)(*[P(x) if isinstance(x, int) and x >= Q - 14336 else x
+                                                                   for x in a.values()]) == 1
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("f16,at", [(0, 0), (0, 2032), (0, -16), (1, 1008), (1, -1008)])
+def test_read_refuses_outputs_that_overlap(lib, end, f16, at):
+    a = dict(k_rows=P(K), v_rows=P(K + at), f16=f16, kp=FAKE, vp=FAKE, rows=256, w=128, table=FAKE, max_blocks=4,
+             block_rows=16, off=FAKE, past=FAKE, nt=4, n_seq=2, err=FAKE, stream=None)
+    assert getattr(lib, "minf_kv_read_chunk_paged" + end)(*a.values()) == 1
+
+
+@pytest.mark.parametrize("at", [4, -4, 4 * 2 * 8 * 4 - 4])
+def test_rope_axes_refuses_partly_in_place(lib, at):
+    assert lib.minf_rope_axes(P(Q + at), P(Q), FAKE, 4, 1, None, 2, 8, 1e4, 1.0, 0, FAKE, None) == 1
+
+
+@pytest.mark.parametrize("end", ["", "_f16", "_q8"])
+@pytest.mark.parametrize("bad", [dict(k=P(Q + 16)), dict(v=P(Q)), dict(v=P(K)), dict(v=P(K + 2032))])
+def test_layer_step_refuses_rows_that_overlap(lib, end, bad):
+    a = dict(xn=FAKE, h=FAKE, gain=None, eps=1e-6, n_embd=896, q=P(Q), k=P(K), v=P(V), pos=None, n_axis=1, pair_axis=None,
+             off=FAKE, past=FAKE, nt=4, n_seq=2, max_chunk=4, kp=FAKE, vp=FAKE, rows=256, table=FAKE, max_blocks=4,
+             block_rows=16, nh=14, nk=2, hd=64, hd_kv=64, theta=1e4, fs=1.0, style=0, window=0, n_sink=0, out=P(1 << 24),
+             ws=FAKE, ws_bytes=1 << 40, err=FAKE, stream=None)
+    a.update(bad)
+    assert getattr(lib, "minf_layer_attn_step_chunk_paged" + end)(*a.values()) == 1
