@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_chunk import END, KINDS, Batch, check, i32, m, q8_row_bytes, rng  # noqa: F401
+from test_gpu_chunk import END, KINDS, Batch, check, close, dev, i32, m, q8_row_bytes, rng  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,67 @@ def test_sequences_without_tokens_between_others(m, kind, paged, new, count):
     lens[[4000, 12345, 20000]] = 1, new, 2 if new > 1 else 1
     past[lens > 0] = r.integers(0, 300, (lens > 0).sum())
     check(m, Batch((14, 2, 64, 64), kind, lens.tolist(), past.tolist(), paged=paged, block=16, seed=110))
+
+
+# ----------------------------------------------------------------------------- missing blocks
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("new", [[1, 1], [3, 1], [40, 3]])
+@pytest.mark.parametrize("block", [16, 128])
+@pytest.mark.parametrize("missing", [-1, 1 << 20])
+def test_missing_blocks_are_read_as_zeros(m, kind, new, block, missing):
+    # their keys score 0 and count in the sum
+    def batch():
+        return Batch((16, 8, 128, 128), kind, new, [300, 200], paged=True, block=block, seed=109)
+
+    b, clean = batch(), batch()
+    rows = [clean.row(0, block + i) for i in range(block)]
+    clean.k[rows], clean.v[rows] = 0, 0
+    b.table[0, 1] = missing
+    got, err = b.run(m)
+    clean.scale = b.scale
+    close(got, clean.ref())
+    assert err == 0x10
+
+
+# ----------------------------------------------------------------------------- rotation and store
+@pytest.mark.parametrize("theta,freq_scale", [(1e4, 0.25), (1e4, 3.0), (5e5, 1 / 3)])
+@pytest.mark.parametrize("style", [0, 1])
+def test_other_angular_speeds(m, theta, freq_scale, style):
+    nt, heads, hd = 50, 3, 128
+    r, axis = rng(111), [0] * 16 + [1] * 24 + [2] * 24
+    x = r.standard_normal((nt, heads, hd)).astype(np.float32)
+    pos = r.integers(0, 1 << 17, (3, nt)).astype(np.int32)
+    want, size = np.array(x, np.float64), np.zeros(x.shape)
+    for i in range(hd // 2):
+        a, b = (i, i + hd // 2) if style == 0 else (2 * i, 2 * i + 1)
+        th = pos[axis[i]][:, None] * (float(np.float32(freq_scale)) * float(np.float32(theta)) ** (-2.0 * i / hd))
+        xa, xb = x[:, :, a].astype(np.float64), x[:, :, b].astype(np.float64)
+        want[:, :, a], want[:, :, b] = xa * np.cos(th) - xb * np.sin(th), xa * np.sin(th) + xb * np.cos(th)
+        size[:, :, a] = size[:, :, b] = np.abs(xa) + np.abs(xb)
+    y, err = torch.empty(nt, heads, hd, device="cuda"), i32([0])
+    m.minf_rope_axes(y, dev(x), i32(pos), axis, heads, hd, theta, freq_scale, style, err)
+    assert (np.abs(y.cpu().numpy() - want) <= 3.5e-7 * size).all()
+    # the store turns q and k alike
+    table, pool = i32([[0, 1, 2, 3]]), [torch.zeros(64, heads * hd, device="cuda") for _ in range(2)]
+    q_out, k_out = torch.empty_like(y), torch.empty_like(y)
+    m.minf_rope_kv_append_chunk_paged(q_out, k_out, dev(x), dev(x), dev(x), i32(pos), axis, i32([0, nt]), i32([7]), heads,
+                                      heads, hd, hd, theta, freq_scale, style, *pool, table, 16, err)
+    assert torch.equal(q_out, y) and torch.equal(k_out, y) and err.item() == 0
+    assert torch.equal(pool[0][7:57].view(nt, heads, hd), y)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("starts", [[0, 5, 3, 8], [-1, 2, 4, 8], [0, 3, 5, 9]])
+def test_store_and_read_back_report_offsets_out_of_order(m, kind, starts):
+    geom = (14, 2, 64, 64)
+    nh, nk, hd, hd_kv = geom
+    b = Batch(geom, kind, [3, 2, 3], [5, 9, 100], paged=True, seed=112)
+    q, k, v = (torch.randn(8, c, device="cuda") for c in (nh * hd, b.w, b.w))
+    kp, vp, off, err = dev(b.k), dev(b.v), i32(starts), i32([0])
+    getattr(m, "minf_rope_kv_append_chunk_paged" + END[kind])(q, k, q, k, v, None, None, off, i32(b.past), nh, nk, hd, hd_kv,
+                                                              1e6, 1.0, 0, kp, vp, i32(b.table), 16, err)
+    assert err.item() & 0x40
+    err.zero_()
+    getattr(m, "minf_kv_read_chunk_paged" + END[kind])(torch.empty_like(k), torch.empty_like(v), kp, vp, i32(b.table), 16, off,
+                                                       i32(b.past), err)
+    assert err.item() & 0x40
