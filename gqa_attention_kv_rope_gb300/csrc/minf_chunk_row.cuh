@@ -41,9 +41,9 @@ __device__ __forceinline__ float attn_dot(const ChunkKv &c, const float *q, long
     return s;
 }
 
-// Returns (in every lane) whether a block the row sees is missing; its rows count as zeros.
+// (The rows of a block that is missing count as zeros; the kernels' producers report it.)
 template <typename T, int HD>
-__device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float scale_log2, int window, int n_sink) {
+__device__ __forceinline__ void attn_row(const ChunkKv &c, const RowJob &job, float scale_log2, int window, int n_sink) {
     constexpr int D4 = HD / 4, PER = HD / 32;  // values a lane owns
     const int lane = threadIdx.x & 31;
     const long long last = job.p < job.rows.cap - 1 ? job.p : job.rows.cap - 1;  // last visible key
@@ -51,7 +51,6 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
     float l = 0.0f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
-    bool missing = false;
     // key groups: from 0 while sinks are left, then from the window's first key
     const long long first = window == 0 ? 0 : (job.p - window + 1 > 0 ? job.p - window + 1 : 0);
     for (long long j0 = n_sink > 0 ? 0 : (first & ~31LL); j0 <= last; j0 += 32) {
@@ -60,10 +59,7 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
         const int j = static_cast<int>(j0) + lane;
         const bool see = j <= last && chunk_sees(job.p, j, window, n_sink);
         long long row = -1;
-        if (see) {
-            row = seq_row(c, job.rows, j);
-            if (row < 0) missing = true;
-        }
+        if (see) row = seq_row(c, job.rows, j);
         double s = 0.0;
         if (row >= 0) {
             const float x = attn_dot<T, HD>(c, job.q, row, job.hk, 1.0f);
@@ -116,7 +112,27 @@ __device__ __noinline__ bool attn_row(const ChunkKv &c, const RowJob &job, float
     const float inv = 1.0f / (l * kValueScale);
 #pragma unroll
     for (int i = 0; i < PER; ++i) job.out[lane * PER + i] = none ? 0.0f : acc[i] * inv;
-    return __any_sync(0xffffffffu, missing);
+}
+
+// The rows of an item that are marked in `odd`, a row a warp: q and out are the item's first row's, p0 its position,
+// g the rows of a token.  (One call out of line, with the arithmetic of the rows inside: with the rows' loop in the
+// kernels, whatever changed in it moved their hot loops' registers and instructions; 1043 us against 1015 over
+// ragged binary16 prompts.)
+template <typename T, int HD>
+__device__ __noinline__ void attn_rows_again(const ChunkKv &c, const int *odd, int rows, int warp, int warps, const float *q,
+                                             float *out, int g, int nh, int hd, SeqRows sr, long long p0, int hk,
+                                             float scale_log2, int window, int n_sink) {
+    for (int r = warp; r < rows; r += warps) {
+        if (!odd[r]) continue;
+        RowJob job;
+        const long long at = static_cast<long long>(r / g) * nh + r % g;
+        job.q = q + at * hd;
+        job.out = out + at * HD;
+        job.rows = sr;
+        job.p = p0 + r / g;
+        job.hk = hk;
+        attn_row<T, HD>(c, job, scale_log2, window, n_sink);
+    }
 }
 
 }  // namespace minf

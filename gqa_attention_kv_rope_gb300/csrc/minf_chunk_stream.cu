@@ -745,13 +745,13 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
                 for (int e = 0; e < 2; ++e) {
                     const int r = t * 8 + 2 * c4 + e;
                     if (warp >= MT || r >= rows) continue;
-                    const bool empty = L[t][e] == 0.0f;  // it sees nothing, or nothing but scores of minus infinity
-                    const float inv = empty ? 0.0f : 1.0f / L[t][e];
+                    // (a sum of zero, where it sees nothing or nothing but scores of minus infinity, gives NaN here)
+                    const float inv = 1.0f / L[t][e];
                     float *out = p.a.out + (static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g) * HD;
-                    bool bad = empty && (mt.lim[r].y < mt.lim[r].x || mt.lim[r].z > 0);
+                    bool bad = false;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float y = empty ? 0.0f : res[t][2 * h + e] * inv;
+                        const float y = res[t][2 * h + e] * inv;
                         const int d = C::Q || C::F32 ? (warp >> 1) * 32 + 4 * n8 + 2 * (warp & 1) + h : warp * 16 + n8 + 8 * h;
                         out[d] = y;
                         bad |= !(fabsf(y) < INFINITY);
@@ -763,17 +763,9 @@ __device__ __forceinline__ void compute(unsigned char *smem, Meta &mt, const Att
             again = !named_all(1, C::kComputeThreads, !odd);
             if (again) {
                 if (tid == 0) rows_again(&mt.abort_flag, true);
-                for (int r = warp; r < rows; r += kWarps) {
-                    if (!mt.odd[r]) continue;
-                    RowJob job;
-                    const long long at = static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g;
-                    job.q = p.a.q + at * p.a.hd;
-                    job.out = p.a.out + at * HD;
-                    job.rows = w.rows;
-                    job.p = walk_pos(w, p) + r / g;
-                    job.hk = w.head;
-                    attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
-                }
+                const long long at = static_cast<long long>(walk_row(w, p)) * p.a.nh + w.head * g;
+                attn_rows_again<T, HD>(p.a.c, mt.odd, rows, warp, kWarps, p.a.q + at * p.a.hd, p.a.out + at * HD, g, p.a.nh,
+                                       p.a.hd, w.rows, walk_pos(w, p), w.head, p.scale_log2, p.a.window, p.a.n_sink);
             }
         }
         named_sync(1, C::kComputeThreads);  // Q, limits and the join buffer are free

@@ -792,7 +792,6 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             const long long first = walk_pos(w, p), last = first + w.cnt - 1;
             const long long lo = p.a.window && last - p.a.window + 1 > 0 ? last - p.a.window + 1 : 0;
             const long long hi = first + 1 < w.rows.cap ? first + 1 : w.rows.cap;
-            sm.span = make_int2(0x7fff, -0x7fff);
             sm.all = make_int2(lo < 0x7fffffff ? static_cast<int>(lo) : 0x7fffffff, hi > 0 ? static_cast<int>(hi) : 0);
             // the next segment
             Walk next = w;
@@ -801,6 +800,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
         }
         named_sync(1, C::kRowThreads);
         float m = -INFINITY, l = 0.0f, last_corr = 1.0f;
+        int span_lo = 0x7fff, span_hi = -0x7fff;  // of V's exponents
         float2 acc[DIMS / 2];
 #pragma unroll
         for (int d = 0; d < DIMS / 2; ++d) acc[d] = make_float2(0.0f, 0.0f);
@@ -831,7 +831,10 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     chunk_wait(&sm.k_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     chunk_wait(&sm.v_stat[q & 3], (q >> 2) & 1, abort_flag, err);
                     const auto fk = sm.k_tile[q & 3], fv = sm.v_tile[q & 3];
-                    if (F32 && tid == 0) sm.span = make_int2(min(sm.span.x, sm.v_span[q & 3].x), max(sm.span.y, sm.v_span[q & 3].y));
+                    if (F32) {
+                        const int2 o = sm.v_span[q & 3];
+                        span_lo = min(span_lo, o.x), span_hi = max(span_hi, o.y);
+                    }
                     k_rows = fk.by_row, v_rows = fv.by_row;
                     cc = c * fk.fac;  // (1, 0 and 1 where they are row by row)
                     ve = fv.exp;
@@ -955,6 +958,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             if (lane == 0) mbar_arrive(&sm.p_ready[q & 1]);
         }
         n += tiles;
+        if (F32 && tid == 0) sm.span = make_int2(span_lo, span_hi);
         if (warp_live) fold(n - 1);
         sm.sum[part][row] = l;
         named_sync(1, C::kRowThreads);
@@ -982,19 +986,16 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             named_sync(1, C::kRowThreads);
         };
         bool finish = whole, odd = false, again = false;
-        // a row whose sum is zero sees nothing, or nothing but scores of minus infinity
-        auto sees = [&]() { return live && chunk_sees_any(walk_pos(w, p) + sm.token[row], w.rows.cap, p.a.window, p.a.n_sink); };
         if (whole) {
             if (F32) odd = sm.span.y - sm.span.x > kSpan;
-            if (l == 0.0f) odd |= sees();
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            const float inv = 1.0f / l;  // (l zero, where a row sees nothing or nothing but scores of minus infinity: NaN)
 #pragma unroll
             for (int d = 0; d < DIMS; d += 16) {
                 float y[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float2 o = acc[(d + e) >> 1];
-                    y[e] = l == 0.0f ? 0.0f : (e & 1 ? o.y : o.x) * inv;
+                    y[e] = (e & 1 ? o.y : o.x) * inv;
                     odd |= !(fabsf(y[e]) < INFINITY);
                 }
 #pragma unroll
@@ -1029,15 +1030,7 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                 // join the parts in the order of their keys (dead rows read what is there and are not put); two
                 // parts' loads are in flight at a time
                 constexpr int JD = C::HL ? 32 : DIMS;  // dims of a pass
-                if (F32) {
-                    int2 span = sm.span;
-                    for (int b = b0; b <= b1; ++b) {
-                        const float *q = p.parts + (2 * static_cast<size_t>(b) + (b == b0 ? 1 : 0)) * kPart;
-                        const int2 o = __ldcg(reinterpret_cast<const int2 *>(q + BM * (HD + 2)));
-                        span = make_int2(min(span.x, o.x), max(span.y, o.y));
-                    }
-                    odd = span.y - span.x > kSpan;
-                }
+                int2 span = sm.span;
 #pragma unroll 1
                 for (int d0 = 0; d0 < DIMS; d0 += JD) {
                     float M = -INFINITY, L = 0.0f;
@@ -1051,6 +1044,10 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                         float4 x[JD / 4];
 #pragma unroll
                         for (int d = 0; d < JD / 4; ++d) x[d] = __ldcg(reinterpret_cast<const float4 *>(q) + ((part * DIMS + d0) / 4 + d) * BM + row);
+                        if (F32) {
+                            const int2 o = __ldcg(reinterpret_cast<const int2 *>(q + BM * (HD + 2)));
+                            span = make_int2(min(span.x, o.x), max(span.y, o.y));
+                        }
                         if (mb == -INFINITY && lb == 0.0f) continue;  // saw nothing, whatever it holds
                         const float mn = fmaxf(M, mb), fo = ex2_approx(M - mn), fn = ex2_approx(mb - mn);
                         M = mn;
@@ -1063,13 +1060,13 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                             y[4 * d + 3] = y[4 * d + 3] * fo + x[d].w * fn;
                         }
                     }
-                    if (L == 0.0f) odd |= sees();
-                    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+                    const float inv = 1.0f / L;
 #pragma unroll
                     for (int d = 0; d < JD; ++d) {
-                        y[d] = L == 0.0f ? 0.0f : y[d] * inv;
+                        y[d] *= inv;
                         odd |= !(fabsf(y[d]) < INFINITY);
                     }
+                    if (F32) odd |= span.y - span.x > kSpan;
 #pragma unroll
                     for (int d = 0; d < JD; d += OD) put(y + d, d0 + d);
                 }
@@ -1082,17 +1079,9 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
             again = !named_all(1, C::kRowThreads, !odd);
             if (again) {
                 if (tid == 0) rows_again(&sm.abort_flag, true);
-                for (int r = warp; r < rows; r += C::kRowWarps) {
-                    if (!sm.odd[r]) continue;
-                    RowJob job;
-                    const long long at = static_cast<long long>(walk_row(w, p) + r / g) * p.a.nh + w.head * g + r % g;
-                    job.q = p.a.q + at * p.a.hd;
-                    job.out = p.a.out + at * HD;
-                    job.rows = w.rows;
-                    job.p = walk_pos(w, p) + r / g;
-                    job.hk = w.head;
-                    attn_row<T, HD>(p.a.c, job, p.scale_log2, p.a.window, p.a.n_sink);
-                }
+                const long long at = static_cast<long long>(walk_row(w, p)) * p.a.nh + w.head * g;
+                attn_rows_again<T, HD>(p.a.c, sm.odd, rows, warp, C::kRowWarps, p.a.q + at * p.a.hd, p.a.out + at * HD, g,
+                                       p.a.nh, p.a.hd, w.rows, walk_pos(w, p), w.head, p.scale_log2, p.a.window, p.a.n_sink);
             }
         }
         tc_before();
