@@ -7,17 +7,19 @@ namespace minf {
 namespace {
 
 // The limits of minf_chunk_tiles.h.  kStreamRows and kStreamRowsF16, query rows (tokens x heads of a kv head) up to
-// which the streaming kernel runs alone: measured on 16 query heads over 8 kv heads of 128 dims, 64 sequences of 4096 rows, streaming kernel and tiles: binary16 16 rows
-// 195 and 210 us, 32 rows 363 and 212; Q8_0 32 rows 627 and 725; fp32 (16 sequences) 238 and 267.  One sequence
-// of 8192 rows, binary16: 8 rows 25 and 56, 32 rows 49 and 54.
-// kFewRows, in a call that also has long chunks: there the streaming kernel takes the few tokens of the others.  31
-// single tokens beside 3 chunks of 391, Q8_0: 267 us, all in tiles 575; with the streaming kernel laid out
-// for 32 rows 533 (it computes as many for every token).
+// which the streaming kernel runs alone: measured on 16 query heads over 8 kv heads of 128 dims, 64 sequences of
+// 4096 rows, streaming kernel and tiles: binary16 16 rows 195 and 210 us, 32 rows 363 and 212; Q8_0 32 rows 627 and
+// 725; fp32 (16 sequences) 238 and 267.  (The 32-row instances keep 128 sums a thread at 128 dims and spill 570 and
+// 760 bytes.)  One sequence of 8192 rows, binary16: 8 rows 25 and 56, 32 rows 49 and 54 (there the tiles are taken).
+// kFewRows, in a call that also has long chunks: there the streaming kernel takes the few tokens of the others, after
+// the tiles.  31 single tokens with 3 chunks of 391, Q8_0: 267 us, all in tiles 575; with the streaming kernel laid
+// out for 32 rows 533 (it computes as many for every token).  31 times 4 tokens of two heads with chunks of 391, 300
+// and 200 and 31 times 5, which go to the tiles: Q8_0 267 and 515 us, fp32 512 and 685, binary16 178 and 193.
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // A call whose chunks all fit the streaming kernel runs that alone; one sequence with a longer chunk
-// runs the tiles alone; a batch runs both, each over its own sequences.
+// runs the tiles alone; a batch runs both, each over its own sequences, one after the other.
 struct Choice {
     bool stream, tiles;
     int rows, most;  // of the streaming kernel

@@ -41,13 +41,16 @@
 // split and write K and V in turn.
 //
 // What bounds it, on a batch of six ragged prompts of up to 2048 tokens over up to 12000 cached binary16 rows
-// (16 query heads on 8 of 128 dims; 684 GFLOP): 1.13 ms, 607 TFLOP/s, twice that on the tensor cores, whose
-// measured rate of 1.88 PFLOP/s allows 0.73 ms.  A tile takes 2800 to 3100 clocks, of which S and P V take
-// 2600 (81 to 88 a 128x128x16 step) and the row threads 2500: both are nearly full.  S cut into two halves
-// of 64 keys, so that the first could start earlier, measured 1260 us.  Q8_0 and fp32 tiles take about
-// 10000 clocks, against 3900 of tensor work in three products: the splitting warps write 128 KB of halves
-// a tile, there is no room for a second stage of them at 128 dims, and the warps of a CTA wait on one another.
-// Tried there and not kept: K split a tile ahead of V (265 us against 264 on 34 sequences, 31 of them single
+// (16 query heads on 8 of 128 dims; 684 GFLOP): 1.12 ms, 612 TFLOP/s, twice that on the tensor cores, whose
+// measured rate of 1.88 PFLOP/s allows 0.73 ms.  A CTA takes 1.74 million clocks for its 552 tiles and 7 to 8
+// items (at 1.69 GHz, under the power limit): 3150 a tile with the items' edges.  Within a tile S and P V take
+// 2600 clocks, 81 to 88 a 128x128x16 step, where the tensor cores' rate is 64 and a library product of 8192^3 takes
+// 68, and the row threads 2500.  S cut into two halves of 64 keys, so that the first could start earlier,
+// measured 1260 us.  Under a window of 8 tiles (6000 tokens, 1024 rows: 163 us) a tile takes 5800 clocks with the
+// items' edges.  At 128 dims (2048 tokens over 8192 rows: 592 and 1007 us) Q8_0 tiles take 8700 clocks and fp32 ones
+// 13500, against 3100 of tensor work in three products: the splitting warps write 128 KB of halves a tile, there is
+// one stage of them beside the staged Q rows (66 KB, in use once an item), and the warps of a CTA wait on one
+// another; of fp32 rows V is read a second time for its maxima.  Tried there and not kept: K split a tile ahead of V (265 us against 264 on 34 sequences, 31 of them single
 // tokens), the tiles' factors found by the warp that resolves the rows (277 us).
 //
 // Values in rows that no token of the item sees are zeroed in V (P is zero there, but 0 * inf is
@@ -211,12 +214,11 @@ __device__ __forceinline__ uint32_t sw16(int row, int c) {
     return static_cast<uint32_t>(row) * 128u + ((static_cast<uint32_t>(c) ^ static_cast<uint32_t>(row & 7)) << 4);
 }
 
-// The power of two that brings a row's largest magnitude to [2^14, 2^15), as 2^sh; 1 for a row of
-// zeros.  Larger sh than `most` are cut to it.
+// The power of two that brings a row's largest magnitude to [2^14, 2^15), as 2^sh within -126 .. most; 1 for a
+// row of zeros.
 __device__ __forceinline__ int row_shift(float amax, int most) {
     const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff) - 127;
-    const int sh = amax > 0.0f ? 14 - ex : most < 0 ? 0 : (most < 126 ? most : 0);
-    return sh > most ? most : (sh < -126 ? -126 : sh);
+    return amax > 0.0f ? max(min(14 - ex, most), -126) : 0;
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
@@ -233,11 +235,22 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
 }
 
 // ----------------------------------------------------------------------------- producers
+// One warp: an item's Q rows into the stage.
+template <int HD, typename T>
+__device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w) {
+    using C = Cfg<HD, T>;
+    const int lane = threadIdx.x & 31, g = p.a.nh / p.a.nk, rows = w.cnt * g;
+    if (lane == 0) mbar_expect_tx(&sm.q_in, static_cast<uint32_t>(rows) * HD * 4);
+    __syncwarp();
+    for (int r = lane; r < rows; r += 32) {
+        const long long t = walk_row(w, p) + r / g;
+        bulk_load(sm.q + r * C::kQRow, p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd, HD * 4, &sm.q_in);
+    }
+    __syncwarp();
+}
+
 // One warp: TMA copies of the stretch's K (or V) tiles, a lane a copy.  A copy that no visible row
 // lies in, or whose block is missing, reads past the map's end: zeros.
-template <int HD, typename T>
-__device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w);
-
 template <int HD, typename T, bool kV>
 __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &map, const AttnParams &p, int ctas) {
     using C = Cfg<HD, T>;
@@ -278,20 +291,7 @@ __device__ __forceinline__ void copy_tiles(Smem<HD, T> &sm, const CUtensorMap &m
     }
 }
 
-// One warp: an item's Q rows into the stage.
-template <int HD, typename T>
-__device__ __forceinline__ void copy_q_rows(Smem<HD, T> &sm, const AttnParams &p, const Walk &w) {
-    using C = Cfg<HD, T>;
-    const int lane = threadIdx.x & 31, g = p.a.nh / p.a.nk, rows = w.cnt * g;
-    if (lane == 0) mbar_expect_tx(&sm.q_in, static_cast<uint32_t>(rows) * HD * 4);
-    __syncwarp();
-    for (int r = lane; r < rows; r += 32) {
-        const long long t = walk_row(w, p) + r / g;
-        bulk_load(sm.q + r * C::kQRow, p.a.q + (t * p.a.nh + w.head * g + r % g) * p.a.hd, HD * 4, &sm.q_in);
-    }
-    __syncwarp();
-}
-// The same for all items, as soon as the row threads have taken the last one's.
+// One warp: all items' Q rows, each as soon as the row threads have taken the last one's.
 template <int HD, typename T>
 __device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, int ctas) {
     volatile int *abort_flag = &sm.abort_flag;
@@ -303,14 +303,11 @@ __device__ __forceinline__ void copy_q(Smem<HD, T> &sm, const AttnParams &p, int
     }
 }
 
-// Four warps each: the stretch's K and V tiles as scaled hi + lo halves; a warp takes 32 of a tile's
-// rows.  V's exponents go out a tile ahead (the row threads need them with S, while the V stage may
-// still be in use); fp32 rows are prefetched into L2.  Eight lanes load, split and write a row, four
-// rows a step.  (The rows come resolved from warp 9: a walk of their own would take the registers
-// that the splitting warps hold rows in.)
-
-// Eight lanes a row: VPL consecutive values a lane, a warp's rows of a whole tile held as they
-// are stored, loaded as soon as the last tile's have been written.
+// What a splitting warp (split_tiles) holds of its 16 rows of a tile: eight lanes load, split and write a row, four
+// rows a step.
+//
+// Q8_0: VPL consecutive values a lane, all 16 rows held as they are stored, loaded as soon as the last tile's have
+// been written.
 template <int HD>
 struct SplitQ8 {
     static constexpr int VPL = HD / 8, CH = VPL / 8;  // values and 16-byte chunks of halves a lane
@@ -482,6 +479,9 @@ __device__ __forceinline__ void resolve_rows(Smem<HD, T> &sm, const AttnParams &
     }
 }
 
+// The stretch's K and V tiles as scaled hi + lo halves.  (The rows come resolved from warp 9: a walk of their own
+// would take the registers that the splitting warps hold rows in.)  V's exponents go out a tile ahead: the row
+// threads need them with S, while the V stage may still be in use.  fp32 rows are prefetched into L2.
 // The splitting warps take K and V of a tile in turn, 16 rows each: K of the next tile while P V runs, V while
 // S does.  (Four warps for K and four for V took twice as long over a product's operand, with the tensor cores
 // waiting for it.)  Lanes 0-15 hold what belongs to the warp's K rows, lanes 16-31 to its V rows.
@@ -841,8 +841,8 @@ __device__ __forceinline__ void do_rows(Smem<HD, T> &sm, const AttnParams &p, ui
                     vi = fv.fac;
                 }
                 const float tile_c = cc;
-                // key by key factors (rare): t = S c k + e as the scores are read, else one multiply-add below takes
-                // S to its exponential
+                // key by key factors (all fp32 tiles have them for K, Q8_0 tiles rarely): t = S c k + e as the scores are
+                // read, else one multiply-add below takes S to its exponential
                 const bool by_key = C::HL && (k_rows || v_rows);
                 if (by_key) cc = 1.0f;
                 const int2 all = sm.all;
