@@ -618,7 +618,8 @@ MINF_API int minf_kv_read_chunk_paged_q8(void *k_rows, void *v_rows, int rows_f1
  * next, so calls of any shape may share it one after the other; two calls that run concurrently
  * must not.
  * Sums and softmax statistics are fp32; products run on the tensor cores with operands split into
- * halves whose sum carries 22 bits or more (softmax weights below 2^-15 of a row's largest: 2^-37 of it).
+ * halves whose sum carries 22 bits or more of the largest value of a query's or a cached row's head
+ * (softmax weights below 2^-15 of a row's largest: 2^-37 of it).
  * A row that sees an infinity or a NaN, or whose scores pass the range of fp32, is computed again key
  * by key: right, but slow.
  * Device errors: MINF_ERRBIT_ATTN_POS (p < 0, or p >= cap: the window is clamped to cap), _BLOCK
