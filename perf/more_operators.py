@@ -312,8 +312,7 @@ def _plain_grow(s):
     b = torch.arange(s["table"].shape[1], device="cuda") - held[:, None]
     nth = (upto - take)[:, None] + b
     taken = (b >= 0) & (b < take[:, None])
-    # the last of the list, in its order
-    ids = s["free"][(s["n_free"].long() - upto[-1] + nth).clamp(min=0, max=s["free"].shape[0] - 1)]
+    ids = s["free"][(s["n_free"].long() - 1 - nth).clamp(min=0, max=s["free"].shape[0] - 1)]
     s["table"].copy_(torch.where(taken, ids, s["table"]))
     off = torch.cat([torch.zeros_like(new[:1]), new.cumsum(0)])
     t = torch.arange(s["nt"], device="cuda")
@@ -326,11 +325,11 @@ def _plain_grow(s):
 
 
 def _plain_release(s, n_free):
-    """Every block in the given rows back at the list's end, in order; a list with one more place, cut off again."""
+    """Every block in the given rows back on the list, the last one first; a list with one more place, cut off again."""
     b = torch.arange(s["table"].shape[1], device="cuda") * s["block"]
     out = (b >= s["row_lo"][:, None]) & (b + s["block"] <= s["row_hi"][:, None]) & (s["table"] >= 0)
     nth = out.view(-1).cumsum(0)
-    place = torch.where(out.view(-1), n_free.long() + nth - 1, s["free"].shape[0])
+    place = torch.where(out.view(-1), n_free.long() + nth[-1] - nth, s["free"].shape[0])
     s["free"].copy_(torch.cat([s["free"], s["free"][:1]]).scatter(0, place, s["table"].view(-1))[:-1])
     s["table"].masked_fill_(out, -1)
     return n_free + nth[-1:].int()
