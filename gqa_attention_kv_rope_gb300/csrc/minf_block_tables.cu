@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const BlockGrowArgs a) {
         take[a.n_seq] = static_cast<int>(blks);
     }
     __syncthreads();
-    const int32_t *ids = a.free_ids + (n_free - static_cast<int>(blks));  // the call's blocks, in order
+    const int32_t *ids = a.free_ids + n_free - 1;  // the call's blocks: ids[0], ids[-1], ids[-2] ..
     for (int s = at; s <= a.n_seq; s += step) a.chunk_off[s] = off[s];
     for (int i = at; i < blks; i += step) {
         const int s = last_not_above(take, a.n_seq, i);
-        a.table[static_cast<size_t>(s) * a.max_blocks + blocks_of(past[s], a.block_shift) + (i - take[s])] = __ldg(ids + i);
+        a.table[static_cast<size_t>(s) * a.max_blocks + blocks_of(past[s], a.block_shift) + (i - take[s])] = __ldg(ids - i);
     }
     // positions and pool rows: four tokens a thread
     int missing = 0;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const BlockGrowArgs a) {
             const int p = past[s] + (t - off[s]), b = p >> a.block_shift;
             if (b != have || s != have_s) {
                 const int held = blocks_of(past[s], a.block_shift);
-                id = b < held ? a.table[static_cast<size_t>(s) * a.max_blocks + b] : __ldg(ids + take[s] + (b - held));
+                id = b < held ? a.table[static_cast<size_t>(s) * a.max_blocks + b] : __ldg(ids - (take[s] + (b - held)));
                 have = b;
                 have_s = s;
                 missing |= id < 0 || id >= a.pool_blocks;
@@ -244,10 +244,11 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const BlockReleaseArg
         return;
     }
     int bad = 0;
-    auto give = [&](int32_t *e, int x, long long place) {
+    int32_t *ids = a.free_ids + n_free + all - 1;  // the last to go back is put on the list first
+    auto give = [&](int32_t *e, int x, long long nth) {
         *e = -1;
         bad |= x >= a.pool_blocks;
-        if (held(x)) a.free_ids[n_free + place] = x;
+        if (held(x)) ids[-nth] = x;
     };
     if (hi - lo <= kThreads) {
         if (mine) give(mine, id, base + nth[0]);

@@ -747,7 +747,7 @@ MINF_API int minf_layer_attn_step_chunk_paged_q4(float *xn, const float *h, cons
  *
  * minf_block_table_grow: n_new[s] tokens are to be appended to sequence s.  Writes
  *   block_table  the entries up to ceil((n_past[s] + n_new[s]) / B) that are not held yet: the call's T new
- *                blocks are the list's last T, in its order, given out by sequence and then by entry;
+ *                blocks are the list's last T, its last id first, given out by sequence and then by entry;
  *   chunk_off    [n_seq + 1] the sums of n_new, as the chunk operators take them;
  *   pos          [nt] the cache position of each packed token (also a pos of minf_rope and rope_pos);
  *   slot         [nt] its row of the pool (pos of minf_kv_append and its forms, with the pool as the regions);
@@ -761,12 +761,13 @@ MINF_API int minf_layer_attn_step_chunk_paged_q4(float *xn, const float *h, cons
  * held or from the list, is not in the pool gets the slot -1 and MINF_ERRBIT_BLOCK.
  *
  * minf_block_table_release: the blocks that lie wholly in rows [row_lo[s], row_hi[s]) of sequence s go
- * back to the list's end, by sequence and then by entry, and their entries become -1 (entries below
- * 0 are passed; bounds are clamped to the capacity).  Finished: [0, capacity); drafted tokens
- * rejected: [rows kept, capacity); behind a window: [rows of the sinks, position - window + 1).  A release of what a
- * grow took leaves the list as it was.  An id at or above the pool's blocks is cleared and dropped, with
- * MINF_ERRBIT_BLOCK.  Where the list would pass max_free, or n_free is outside [0, max_free]:
- * MINF_ERRBIT_BLOCK, and nothing changes.  An id must not stand in the tables twice.
+ * back to the list's end, the first of them (by sequence and then by entry) as its last id, the next
+ * ahead of that and so on, and their entries become -1 (entries below 0 are passed; bounds are clamped
+ * to the capacity).  Finished: [0, capacity); drafted tokens rejected: [rows kept, capacity); behind a
+ * window: [rows of the sinks, position - window + 1).  A release of what a grow took leaves the list as
+ * it was, and the next grow gives the same ids out again.  An id at or above the pool's blocks is cleared
+ * and dropped, with MINF_ERRBIT_BLOCK.  Where the list would pass max_free, or n_free is outside
+ * [0, max_free]: MINF_ERRBIT_BLOCK, and nothing changes.  An id must not stand in the tables twice.
  *
  * Calls over one list must follow one another.  Errors of both: MINF_ERR_ARG for null or unaligned (4 bytes)
  * pointers (an array without elements may be null), max_blocks <= 0, negative pool_rows, n_seq, nt or max_free, an array that
