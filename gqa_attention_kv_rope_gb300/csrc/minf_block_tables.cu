@@ -274,8 +274,10 @@ int ctas_for(long long turns) { return turns <= 4 * kThreads ? 1 : turns <= 16 *
 template <typename Args>
 int launch(void (*kernel)(Args), const Args &a, int arrays, long long turns, cudaStream_t s) {
     const size_t smem = static_cast<size_t>(arrays) * (a.n_seq + 1) * sizeof(int);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    // What a kernel is allowed is state of the whole context: always the same, so that no thread's call lowers it between
+    // another's setting and its launch.
+    const int most = arrays * (kMostSeqs + 1) * static_cast<int>(sizeof(int));
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
         return MINF_ERR_CUDA;
     int ctas = ctas_for(turns);
     cudaLaunchConfig_t cfg = {};
