@@ -24,7 +24,8 @@ def lib(tmp_path_factory):
     if not os.path.exists(obj):
         obj = build._compile("minf_block_tables.cu", False)
     so = tmp_path_factory.mktemp("fake") / "tables.so"
-    subprocess.run([build.nvcc(), "-shared", "-cudart", "none", "-Xcompiler", "-fPIC", "-o", str(so),
+    # (-Bsymbolic: its own stand-ins, not the runtime that torch has loaded)
+    subprocess.run([build.nvcc(), "-shared", "-cudart", "none", "-Xcompiler", "-fPIC", "-Xlinker", "-Bsymbolic", "-o", str(so),
                     os.path.join(HERE, "fake_cuda_runtime.cpp"), obj], check=True, capture_output=True)
     lib = ctypes.CDLL(str(so))
     i, i64 = ctypes.c_int, ctypes.c_int64
