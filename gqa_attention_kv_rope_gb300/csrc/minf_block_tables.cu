@@ -277,7 +277,11 @@ int launch(void (*kernel)(Args), const Args &a, int arrays, long long turns, cud
     // What a kernel is allowed is state of the whole context: always the same, so that no thread's call lowers it between
     // another's setting and its launch.
     const int most = arrays * (kMostSeqs + 1) * static_cast<int>(sizeof(int));
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    // (48 KB without the setting, a kernel's own arrays included)
+    constexpr size_t kOwn = 1024;
+    static_assert(sizeof(WarpSums<2>) + 64 <= kOwn && 2 * sizeof(WarpSums<1>) + 64 <= kOwn, "the kernels' own arrays");
+    if (smem + kOwn > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
         return MINF_ERR_CUDA;
     int ctas = ctas_for(turns);
     cudaLaunchConfig_t cfg = {};

@@ -54,3 +54,15 @@ def test_no_call_lowers_what_another_is_allowed(lib, call, mine, other):
     lib.fake_meanwhile(hook)
     assert call(lib, mine) == 0 and theirs == [0]
     assert lib.fake_launches() == 2 and lib.fake_last_error() == 0
+
+
+@pytest.mark.parametrize("call,bytes_a_seq", [(grow, 12), (release, 8)])
+def test_a_kernels_own_arrays_count(lib, call, bytes_a_seq):
+    """Sums that fit 48 KB by themselves, but not with the kernel's own arrays, as the first call and after larger ones."""
+    near = 48 * 1024 // bytes_a_seq - 1
+    for first in (None, 16384):
+        for n in [*range(near - 200, near + 3, 7), near - 1, near, near + 1]:
+            lib.fake_reset(OWN)
+            assert first is None or call(lib, first) == 0
+            assert call(lib, n) == 0 and lib.fake_last_error() == 0, n
+            assert lib.fake_dynamic() == bytes_a_seq * (n + 1)
