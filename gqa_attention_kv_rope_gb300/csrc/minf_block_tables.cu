@@ -299,7 +299,9 @@ int launch(void (*kernel)(Args), const Args &a, int arrays, long long turns, cud
         int clusters = 0;
         if (ctas <= 8 || (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
                           cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0))
-            break;  // (else no part of this GPU has 16 SMs side by side)
+            break;
+        // (no part of this GPU has 16 SMs side by side: no error, and none for those who ask for the last one)
+        (void)cudaGetLastError();
     }
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MINF_OK : MINF_ERR_CUDA;
 }

@@ -66,3 +66,19 @@ def test_a_kernels_own_arrays_count(lib, call, bytes_a_seq):
             assert first is None or call(lib, first) == 0
             assert call(lib, n) == 0 and lib.fake_last_error() == 0, n
             assert lib.fake_dynamic() == bytes_a_seq * (n + 1)
+
+
+@pytest.mark.parametrize("clusters", [0, -1, None])
+def test_without_large_clusters(lib, clusters):
+    """Where no cluster of 16 can be had -- the query says none, or fails, or the attribute is refused -- the largest calls
+    run in eight CTAs, and nothing is left behind that the next operator would take for its own error."""
+    for call in (lambda: grow(lib, 1024, nt=121000), lambda: release(lib, 3000, max_blocks=40)):
+        lib.fake_reset(OWN)
+        assert call() == 0 and lib.fake_cluster() == 16
+        lib.fake_reset(OWN)
+        if clusters is None:
+            lib.fake_refuse_large_clusters()
+        else:
+            lib.fake_clusters_of_16(clusters)
+        assert call() == 0 and lib.fake_cluster() == 8
+        assert lib.fake_last_error() == 0
