@@ -133,13 +133,20 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const BlockGrowArgs a) {
     __syncthreads();
     const int32_t *ids = a.free_ids + n_free - 1;  // the call's blocks: ids[0], ids[-1], ids[-2] ..
     for (int s = at; s <= a.n_seq; s += step) a.chunk_off[s] = off[s];
+    int missing = 0;
+    auto outside = [&](int id) { return id < 0 || id >= a.pool_blocks; };
     for (int i = at; i < blks; i += step) {
-        const int s = last_not_above(take, a.n_seq, i);
-        a.table[static_cast<size_t>(s) * a.max_blocks + blocks_of(past[s], a.block_shift) + (i - take[s])] = __ldg(ids - i);
+        const int s = last_not_above(take, a.n_seq, i), id = __ldg(ids - i);
+        a.table[static_cast<size_t>(s) * a.max_blocks + blocks_of(past[s], a.block_shift) + (i - take[s])] = id;
+        missing |= outside(id);
+    }
+    const int mask = (1 << a.block_shift) - 1;
+    if (!a.pos && !a.slot) {  // (else the tokens look their blocks up)
+        for (int s = at; s < a.n_seq; s += step)
+            if (off[s + 1] > off[s] && (past[s] & mask))
+                missing |= outside(a.table[static_cast<size_t>(s) * a.max_blocks + (past[s] >> a.block_shift)]);
     }
     // positions and pool rows: four tokens a thread
-    int missing = 0;
-    const int mask = (1 << a.block_shift) - 1;
     for (int t0 = 4 * at; t0 < (a.pos || a.slot ? a.nt : 0); t0 += 4 * step) {
         int pos[4], slot[4];
         int s = t0 < toks ? last_not_above(off, a.n_seq, t0) : 0, have = -1, have_s = -1, id = 0;
@@ -155,10 +162,10 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const BlockGrowArgs a) {
                 id = b < held ? a.table[static_cast<size_t>(s) * a.max_blocks + b] : __ldg(ids - (take[s] + (b - held)));
                 have = b;
                 have_s = s;
-                missing |= id < 0 || id >= a.pool_blocks;
+                missing |= outside(id);
             }
             pos[e] = p;
-            if (id >= 0 && id < a.pool_blocks) slot[e] = (id << a.block_shift) | (p & mask);
+            if (!outside(id)) slot[e] = (id << a.block_shift) | (p & mask);
         }
         const bool whole = t0 + 4 <= a.nt;
 #pragma unroll

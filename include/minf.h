@@ -758,7 +758,8 @@ MINF_API int minf_layer_attn_step_chunk_paged_q4(float *xn, const float *h, cons
  * MINF_ERRBIT_STORE_POS: n_past + n_new above max_blocks * B; MINF_ERRBIT_BLOCK: n_free outside
  * [0, max_free] or below T -- the table stays as it is, n_free_out is n_free, chunk_off is all
  * zeros (what follows on the stream then has no tokens), pos and slot are -1.  A token whose block's id,
- * held or from the list, is not in the pool gets the slot -1 and MINF_ERRBIT_BLOCK.
+ * held or from the list, is not in the pool gets the slot -1 and MINF_ERRBIT_BLOCK (with pos and slot both
+ * NULL too).
  *
  * minf_block_table_release: the blocks that lie wholly in rows [row_lo[s], row_hi[s]) of sequence s go
  * back to the list's end, the first of them (by sequence and then by entry) as its last id, the next

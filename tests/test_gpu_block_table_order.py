@@ -66,3 +66,38 @@ def test_a_release_is_undone_by_the_next_grow(m, n, mb):
     d.grow(m, new, sum(new))
     assert int(d.err) == 0
     assert all(bool((a == b).all()) for a, b in zip(first, (d.table, d.slot, d.n_free)))
+
+
+@pytest.mark.parametrize("pos", [False, True])
+@pytest.mark.parametrize("slot", [False, True])
+def test_ids_are_checked_whatever_arrays_are_wanted(m, pos, slot):
+    """An id of the list, or the held one of a partly filled block that gets tokens, outside the pool: an error bit."""
+    def grow(held=2, new=(4, 0), listed=1):
+        d = tables.Device(Stack([20, 16], 16, 4, 6, seed=1))
+        d.table[0, 1] = held        # rows 16 .. 19 of the first sequence
+        d.free[5] = listed          # the id that is taken first
+        d.table[0, 0] = d.table[1, 0] = -9  # full blocks: nobody's new rows
+        d.grow(m, list(new), sum(new), pos=pos, slot=slot)
+        return int(d.err)
+
+    ok = [dict(), dict(new=(12, 0)), dict(new=(13, 0)), dict(new=(0, 3)), dict(new=(0, 3), held=-1), dict(new=(4, 0), listed=-1),
+          dict(new=(0, 0), held=99, listed=99)]
+    bad = [dict(held=-1), dict(held=9), dict(held=1 << 30), dict(new=(13, 0), listed=-1), dict(new=(0, 1), listed=9),
+           dict(new=(0, 1), listed=-(1 << 31)), dict(new=(1, 40), held=-1)]
+    assert [grow(**a) for a in ok] == [0] * len(ok)
+    assert [grow(**a) for a in bad] == [m.ERRBIT_BLOCK] * len(bad)
+
+
+@pytest.mark.parametrize("n", [1, 1023, 1025, 16384])
+def test_the_last_sequences_held_id_is_checked(m, n):
+    d = tables.Device(Stack([3] * n, 16, 1, 2, seed=n))
+    for at in {0, n // 2, n - 1}:
+        d.err.zero_()
+        first = int(d.table[at, 0])
+        d.table[at, 0] = -1
+        d.grow(m, [1] * n, n, pos=False, slot=False)
+        assert int(d.err) == m.ERRBIT_BLOCK
+        d.table[at, 0] = first
+    d.err.zero_()
+    d.grow(m, [1] * n, n, pos=False, slot=False)
+    assert int(d.err) == 0
