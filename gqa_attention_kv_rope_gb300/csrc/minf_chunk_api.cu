@@ -139,7 +139,7 @@ int attention(ChunkAttnArgs &a, float *out, const float *q, const int32_t *chunk
         n_sink < 0)
         return MINF_ERR_ARG;
     if (nt == 0 || n_seq == 0) return MINF_OK;
-    const size_t need = chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk);
+    const size_t need = chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk, a.c.kv == kKvQ4);
     if (!ws || !aligned16(ws) || ws_bytes < need) return MINF_ERR_WORKSPACE;
     if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd)) return MINF_ERR_ARG;
     a.out = out;
@@ -215,7 +215,7 @@ int layer_step(float *xn, const float *h, const float *gain, float eps, int n_em
         (style != 0 && style != 1) || !ok_axes(n_axis, pair_axis, hd))
         return MINF_ERR_ARG;
     if (nt == 0 || n_seq == 0) return MINF_OK;
-    if (!ws || !aligned16(ws) || ws_bytes < chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk))
+    if (!ws || !aligned16(ws) || ws_bytes < chunk_attn_workspace_bytes(nt, n_seq, nh, nk, hd_kv, max_chunk, kv == kKvQ4))
         return MINF_ERR_WORKSPACE;
     if (overlap(out, static_cast<size_t>(nt) * nh * hd_kv, q, static_cast<size_t>(nt) * nh * hd) ||
         !ok_rope_rows(q, k, q, k, v, static_cast<size_t>(nt) * nh * hd, static_cast<size_t>(nt) * nk * hd_kv))

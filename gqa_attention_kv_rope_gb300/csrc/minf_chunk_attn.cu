@@ -35,11 +35,12 @@ Choice choose(int kv, int n_seq, int g, int max_chunk) {
 
 }  // namespace
 
-size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk) {
+size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk, bool q4) {
     if (nt <= 0 || n_seq <= 0 || nh <= 0 || nk <= 0 || nh % nk || !decode_supported(nh, nk, hd_kv, hd_kv) || max_chunk <= 0)
         return 0;  // (at most 8 heads a kv head: the layouts divide by them)
     size_t most = 0;  // of the types
     for (const int kv : {kKvF32, kKvF16, kKvQ8, kKvQ4}) {
+        if (kv == kKvQ4 && !q4) continue;
         const Choice c = choose(kv, n_seq, nh / nk, max_chunk);
         const size_t need = (c.tiles ? up256(chunk_tiles_workspace(nt, n_seq, nh, nk, hd_kv)) : 0) +
                             (!c.stream        ? 0

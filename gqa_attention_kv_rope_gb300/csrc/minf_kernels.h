@@ -261,7 +261,9 @@ struct BlockReleaseArgs {
     int32_t *err;
 };
 
-size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk);
+// The most that a call takes over rows of any type, or (q4 false) of any but Q4: the parts of all kv heads at once make that
+// one's eight times as large (64 single tokens of 16 heads on 8 of 128 dims: 10.1 MB, 1.3 without).
+size_t chunk_attn_workspace_bytes(int nt, int n_seq, int nh, int nk, int hd_kv, int max_chunk, bool q4 = true);
 int launch_chunk_attn(const ChunkAttnArgs &a, cudaStream_t s);
 
 }  // namespace minf

@@ -645,7 +645,8 @@ MINF_API int minf_kv_read_chunk_paged_q4(void *k_rows, void *v_rows, int rows_f1
  * ws: minf_attn_chunk_workspace_bytes(nt, n_seq, n_head, n_kv_head, hd_kv, max_chunk) bytes,
  * 16-byte aligned.  Its contents need no preparation and no call leaves anything in it for the
  * next, so calls of any shape may share it one after the other; two calls that run concurrently
- * must not.
+ * must not.  (The bytes are for rows of any type; calls over other rows than Q4, whose parts take the
+ * most, are content with less.)
  * Sums and softmax statistics are fp32; products run on the tensor cores with operands split into
  * halves whose sum carries 22 bits or more of the largest value of a query's or a cached row's head
  * (softmax weights below 2^-15 of a row's largest: 2^-37 of it).  Binary16 and Q4 values are operands as
