@@ -12,11 +12,12 @@
 // takes a few tokens: it resolves their rows and the sines and cosines of their angles once into
 // shared memory (every head of a token shares them), then sweeps the tokens' heads.
 //
-// Over Q4 rows a thread packs whole words of eight codes, of V from eight values of its own (59 us for 10,051 tokens of
-// 16 query heads on 8 of 128 dims, 300 MB: 5.0 TB/s; 64.5 with four values and a neighbour's half of the word), of K
-// with one exchange between neighbours, and reads back a word a thread, whose values are binary16 numbers as they are (14.2
-// us for 53 MB, most of it in L2; 22.9 with four values).  The store is bound by its instructions: a rounding, a clamp
-// and a shift a value beside the rotation.
+// Over Q4 rows a thread packs whole words of eight codes, of V from eight values of its own (four values and a neighbour's
+// half of the word took 64.5 us where this took 59), of K with one exchange between neighbours, and reads back a word a
+// thread, whose values are binary16 numbers as they are (14.2 us for 53 MB, most of it in L2; 22.9 with four values).  K
+// turns in pairs of floats (turn_sincos2, below).  10,051 tokens of 16 query heads on 8 of 128 dims, 300 MB, back to back
+// in a graph: 60.3 us, 5.0 TB/s; 56.7 where K turned in single floats.  The store is bound by its instructions: a rounding,
+// a clamp and a shift a value beside the rotation.
 #include <cmath>
 
 #include "minf_chunk.cuh"
@@ -58,13 +59,85 @@ __device__ __forceinline__ void turn_pair(float &a, float &b, float2 cs) {
     b = x * cs.y + y * cs.x;
 }
 
+// The same in pairs of floats, hi + lo: within 2^-36 of the cosine and the sine.  Rows that are quantized turn so: a value
+// next to a border between two codes, or a block's largest next to one between two scales, goes where the exact rotation,
+// rounded to fp32, goes (turned in fp32, about one value in two million got a neighbour's code, half a step off).
+// The angle is the nearest 256th of a turn, whose cosine and sine are tabled for a quarter, and a rest of pi/256 at most.
+struct Sines {
+    float cs[64][4];  // cosine hi, lo, sine hi, lo
+};
+constexpr double series(double x, int n0) {  // of the cosine (n0 0) or the sine (n0 1), up to pi/2
+    double term = n0 ? x : 1.0, sum = term;
+    for (int n = n0 + 2; n < 30; n += 2) {
+        term *= -x * x / (n * (n - 1));
+        sum += term;
+    }
+    return sum;
+}
+constexpr Sines quarter_turn() {
+    Sines t = {};
+    for (int i = 0; i < 64; ++i) {
+        const double x = 6.283185307179586476925286766559 * i / 256, c = series(x, 0), s = series(x, 1);
+        t.cs[i][0] = static_cast<float>(c);
+        t.cs[i][1] = static_cast<float>(c - t.cs[i][0]);
+        t.cs[i][2] = static_cast<float>(s);
+        t.cs[i][3] = static_cast<float>(s - t.cs[i][2]);
+    }
+    return t;
+}
+__device__ const Sines kSines alignas(16) = quarter_turn();
+
+__device__ __forceinline__ float4 turn_sincos2(int pos, unsigned long long F) {  // cosine hi, lo, sine hi, lo
+    const unsigned long long ph = static_cast<unsigned long long>(static_cast<unsigned>(pos)) * F;
+    const unsigned i = static_cast<unsigned>((ph + (1ull << 55)) >> 56);
+    const long long rest = static_cast<long long>(ph - (static_cast<unsigned long long>(i) << 56));  // 2^-64 turns
+    constexpr double kTurn = 6.283185307179586476925286766559 / 18446744073709551616.0;
+    constexpr float k0 = static_cast<float>(kTurn), k1 = static_cast<float>(kTurn - k0);
+    const float r0 = __ll2float_rn(rest), r1 = __ll2float_rn(rest - __float2ll_rn(r0));
+    const float x = __fmul_rn(r0, k0), xl = __fmaf_rn(r0, k0, -x) + (r0 * k1 + r1 * k0);
+    const float xx = x * x;
+    const float sl = xl + x * xx * (-1.0f / 6 + xx * (1.0f / 120));   // sin = x + sl
+    const float cl = xx * (-0.5f + xx * (1.0f / 24)) - x * xl;        // cos = 1 + cl
+    const float4 t = __ldg(reinterpret_cast<const float4 *>(kSines.cs[i & 63]));
+    // a + (b x) + small: the two that are not small without a rounding
+    auto sum = [&](float a, float al, float b, float bl) {
+        const float p = __fmul_rn(b, x), e = __fmaf_rn(b, x, -p);
+        const float h = __fadd_rn(a, p), back = __fsub_rn(h, a);
+        const float lost = __fadd_rn(__fsub_rn(a, __fsub_rn(h, back)), __fsub_rn(p, back));
+        const float l = lost + (e + (al + (a * cl + (b * sl + bl * x))));
+        const float y = __fadd_rn(h, l);
+        return make_float2(y, __fadd_rn(__fsub_rn(h, y), l));
+    };
+    const float2 c = sum(t.x, t.y, -t.z, -t.w), s = sum(t.z, t.w, t.x, t.y);
+    switch (i >> 6 & 3) {
+        case 0: return make_float4(c.x, c.y, s.x, s.y);
+        case 1: return make_float4(-s.x, -s.y, c.x, c.y);
+        case 2: return make_float4(-c.x, -c.y, -s.x, -s.y);
+        default: return make_float4(s.x, s.y, -c.x, -c.y);
+    }
+}
+// a c + b s, c and s as hi + lo: products and their sum with what they lose, rounded once more at the end.
+__device__ __forceinline__ float dot2(float a, float c, float cl, float b, float s, float sl) {
+    const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p), q = __fmul_rn(b, s), qe = __fmaf_rn(b, s, -q);
+    const float h = __fadd_rn(p, q), back = __fsub_rn(h, p);
+    const float lost = __fadd_rn(__fsub_rn(p, __fsub_rn(h, back)), __fsub_rn(q, back));
+    const float y = __fadd_rn(h, lost + ((pe + qe) + (a * cl + b * sl)));
+    return fabsf(h) < INFINITY ? y : h;  // (what an infinity loses is not a number)
+}
+__device__ __forceinline__ void turn_pair(float &a, float &b, float4 cs) {
+    const float x = a, y = b;
+    a = dot2(x, cs.x, cs.y, y, -cs.z, -cs.w);
+    b = dot2(x, cs.z, cs.w, y, cs.x, cs.y);
+}
+
 // Unit u of a head row (8 values): four pairs, as two float4.  style 0: values 4u.. and
 // 4u + hd/2..; style 1: values 8u.. and 8u + 4...
 __device__ __forceinline__ void unit_at(int u, int hd, int style, int &i0, int &i1) {
     i0 = style == 0 ? u : 2 * u;
     i1 = style == 0 ? u + (hd >> 3) : 2 * u + 1;
 }
-__device__ __forceinline__ void turn_unit(float4 &a, float4 &b, int style, const float2 *cs) {
+template <typename CS>
+__device__ __forceinline__ void turn_unit(float4 &a, float4 &b, int style, const CS *cs) {
     if (style == 0) {
         turn_pair(a.x, b.x, cs[0]);
         turn_pair(a.y, b.y, cs[1]);
@@ -77,7 +150,6 @@ __device__ __forceinline__ void turn_unit(float4 &a, float4 &b, int style, const
         turn_pair(b.z, b.w, cs[3]);
     }
 }
-
 // kVec: hd a multiple of 8 (rows of float4 units); otherwise pair by pair.
 template <bool kVec>
 __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs a, const __grid_constant__ AxisTable tab,
@@ -184,11 +256,15 @@ __device__ __forceinline__ void q8_pad(unsigned char *row, int W, long long rb) 
 // of a token, in order: q heads, k heads (8 values a unit) and v (4 values a unit, 8 over Q4).  Each count
 // is a multiple of 8 units (hd_kv 64 or 128; q's is rounded up), so the eight (or four) lanes that
 // share a Q8_0 or Q4 block are always active together.
+// (Eight blocks an SM: the Q4 store's registers stop at 32, where it would take 40: 60.3 us against 62.0.  Two pairs at a
+// time in packed instructions want more of them: 66.9, or 68.3 with 48.)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) chunk_store_kernel(const ChunkStoreArgs a,
+__global__ void __launch_bounds__(kThreads, 8) chunk_store_kernel(const ChunkStoreArgs a,
                                                                const __grid_constant__ AxisTable tq,
                                                                const __grid_constant__ AxisTable tk, int tok) {
-    __shared__ float2 cq[kMaxTok][kMaxHalf], ck[kMaxTok][kMaxHalf];
+    constexpr bool kExact = std::is_same<T, Q4>::value;
+    __shared__ float2 cq[kMaxTok][kMaxHalf];
+    __shared__ std::conditional_t<kExact, float4, float2> ck[kMaxTok][kMaxHalf];
     __shared__ long long dst[kMaxTok];  // pool row of the token, -1: not stored
     __shared__ int pos0[kMaxTok];       // cache position
     __shared__ int state[kMaxTok];      // 0 a token, 1 left unrotated, 2 padding: nothing is written
@@ -227,7 +303,13 @@ __global__ void __launch_bounds__(kThreads) chunk_store_kernel(const ChunkStoreA
         const int pos = a.rope_pos ? __ldg(a.rope_pos + static_cast<size_t>(tq.axis[p]) * a.sq.nt + t0 + t) : pos0[t];
         if (pos < 0 && state[t] == 0) state[t] = 1;
         cq[t][p] = turn_sincos(pos, tq.turn[p]);
-        if (p < hk) ck[t][p] = a.hd == a.hd_kv ? cq[t][p] : turn_sincos(pos, tk.turn[p]);
+        if (p < hk) {
+            if constexpr (kExact) {
+                ck[t][p] = turn_sincos2(pos, a.hd == a.hd_kv ? tq.turn[p] : tk.turn[p]);
+            } else {
+                ck[t][p] = a.hd == a.hd_kv ? cq[t][p] : turn_sincos(pos, tk.turn[p]);
+            }
+        }
     }
     __syncthreads();
     if (threadIdx.x < n && state[threadIdx.x] == 1 && first) flag_error(a.err, MINF_ERRBIT_ROPE_POS);

@@ -571,6 +571,8 @@ MINF_API int minf_rope_axes(float *y, const float *x, const int32_t *pos, int nt
  * with rope_pos [n_axis, nt] (NULL: the cache position on every axis), and writes the rotated k
  * rows and the v rows to the pool rows of their positions: a copy, rounded to binary16 (_f16) or
  * quantized (_q8, _q4) exactly as minf_kv_append_f16, minf_kv_append_q8 and minf_kv_append_q4 do.
+ * (_q4: k turns within 2^-36 of the exact rotation and is rounded to fp32 once, so that its codes and
+ * scales are those of the exact one's.)
  * Two tokens at one position of one sequence cannot be: each row has one writer, as long as no
  * block id is used twice.
  * Device errors: MINF_ERRBIT_ROPE_POS (token left unrotated, still stored), _STORE_POS (position
