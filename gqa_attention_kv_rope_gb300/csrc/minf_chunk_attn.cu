@@ -11,9 +11,11 @@ namespace {
 // 4096 rows, streaming kernel and tiles: binary16 16 rows 195 and 210 us, 32 rows 363 and 212; Q8_0 32 rows 627 and
 // 725; fp32 (16 sequences) 238 and 267.  (The 32-row instances keep 128 sums a thread at 128 dims and spill 570 and
 // 760 bytes.)  One sequence of 8192 rows, binary16: 8 rows 25 and 56, 32 rows 49 and 54 (there the tiles are taken).
-// kStreamRowsQ4 (minf_chunk_q4.cu, whose items are 8 rows: every 8 more are another pass): the same 64 sequences 8 rows 104
-// us and 263, 16 rows 186 and 263, 24 rows 268 and 265; 8 sequences 16 rows 46 and 53, 24 rows 55 and 53.  14 heads
-// on 2 of 64 dims, 64 sequences: 14 rows 47 and 61, 21 rows 63 and 62; 8 sequences: 14 rows 22 and 31, 28 rows 28 and 31.
+// kStreamRowsQ4 (minf_chunk_q4.cu, whose items are 8 rows of whole tokens: what does not fit one is another pass): the same
+// 64 sequences 8 rows 109 us and 256, 16 rows 196 and 256 (24 rows 268 and 265 once); 8 sequences 16 rows 46 and 52, 24
+// rows 55 and 53.  14 heads on 2 of 64 dims, 64 sequences: 14 rows 48 and 61, 21 rows 63 and 62; 8 sequences: 14 rows 22 and
+// 31, 28 rows 28 and 31.  With 3 or 5 heads a kv head 15 rows are three passes: 24 heads on 8 of 128 dims, 64 sequences 283
+// and 257, 8 sequences 56 and 52, one 38 and 42; 12 heads on 4, 64 sequences 158 and 143, one 29 and 52.
 // kFewRows, in a call that also has long chunks: there the streaming kernel takes the few tokens of the others, after
 // the tiles.  31 single tokens with 3 chunks of 391, Q8_0: 267 us, all in tiles 575; with the streaming kernel laid
 // out for 32 rows 533 (it computes as many for every token).  31 times 4 tokens of two heads with chunks of 391, 300

@@ -15,23 +15,26 @@
 //                   a mask a pair of codes and a shift a word, where u - 8 as a binary16 number would take another
 //                   instruction a pair.  The tensor cores line a product up by the exponents of its operands, 2^-14 for
 //                   every subnormal one, and cut off what is below some 24 bits; codes left in bits 0 to 3 lose two bits
-//                   more there (outputs of 2 queries a key: 9.7e-7 off relative to their norm, not 3.1e-7; of more
-//                   1.7e-6, not 5.6e-7; 112 us for 64 sequences of up to 8192 rows instead of 114), codes all brought to
-//                   bits 4 to 7 gain a little over this (3.0e-7, 4.3e-7) for 116 us.
+//                   more there (outputs of 2 queries a key: 9.7e-7 off relative to their norm, not 3.1e-7; 112 us for 64
+//                   sequences of up to 8192 rows instead of 114), codes all brought to bits 4 to 7 gain little over
+//                   this (3.0e-7) for 116 us.
 //   O^T += V^T P^T  the values d (u - 8), exact binary16 numbers.  (An offset taken out of the sums afterwards would not
 //                   do here: over n keys the sums shrink by sqrt(n) against it.)
 // Q and P are split into binary16 halves hi + lo.  Where an item has at most four query rows the halves stand side by
 // side in the eight columns (PACK): one product does both, and the columns are added at the end; with more rows
-// the halves take a product each: 64 sequences of 4096 rows with two query rows a key 92 us, 107 in the variant of 8.
+// the halves take a product each: 64 sequences of 4096 rows with two query rows a key 95 us, 109 in the variant of 8.  The
+// sums over Q's halves are kept apart there too: in one sum the offset of the codes pushes lo's bits out where queries have
+// a large common part (of ten times their spread: outputs 1.6e-5 off, not 7e-7; 107 us, not 109).
 //
 // What bounds it, on 64 sequences of up to 8192 rows (16 query heads on 8 of 128 dims, 382 MB of rows, once from memory):
 // 114 us, 3.35 TB/s.  The producers alone would need 66 us, the computing warps 112 with the rows already there: some 650
-// instructions a warp for 32 keys of a head (a tile takes 2460 clocks: scores 950, softmax 420, values 1020), for every
-// half of codes a mask and a share of a shift, for every pair of values a mask, an exponent and two half2 steps.  Issue
-// slots are half full, the pipes 39 (integer), 36 (fp32 and half) and 18 per cent (tensor): eight warps of 208 registers, two
-// a scheduler, do not cover each other's latencies, and more do not fit (twelve 147 us, sixteen with half the keys
-// each 200 with spills; as pairs, one warp for scores and one for values, 115; scores of the next tile under the values of this
-// one 121).  Short calls are latency: one token over 128 rows 9.5 us in a graph with the plan's launch.
+// instructions a warp for 32 keys of a head (a tile takes 2210 clocks; 2460, of which scores 950, softmax 420 and values
+// 1020, before the offset moved into the products), for every half of codes a mask and a share of a shift, for every pair
+// of values a mask, an exponent and two half2 steps.  Issue slots are half full, the pipes 39 (integer), 36 (fp32 and half)
+// and 18 per cent (tensor): eight warps of 208 registers, two a scheduler, do not cover each other's latencies, and more do
+// not fit (twelve 147 us, sixteen with half the keys each 200 with spills; as pairs, one warp for scores and one for
+// values, 115; scores of the next tile under the values of this one 121).  Short calls are latency: one token over 128
+// rows 9.5 us in a graph with the plan's launch.
 #include <cmath>
 
 #include "minf_chunk_plan.cuh"
@@ -50,7 +53,7 @@ constexpr int kSteps = 2, kKeys = 16 * kSteps;       // of a tile, a warp
 // P is at most 2^(shift + slack) = 2^15, as in minf_chunk_stream.cu.
 constexpr float kShift = 12.0f, kSlack = 3.0f;
 constexpr int kMostStages = 8;
-// The join of a part takes a warp 740 clocks, a tile 2400.  One sequence of 40,000 rows, 8 heads of 128 dims: 100 us in
+// The join of a part takes a warp 740 clocks, a tile 2210.  One sequence of 40,000 rows, 8 heads of 128 dims: 100 us in
 // 152 stretches, 76 in the 64 that follow from this (79 with half of it, 72 with twice; 71 now, the plan being shorter); of 16,000 rows 93 and 50 (58,
 // 52); of 4096 rows 46 and 34.  (The parts' loads two and three at a time, without more of them in a lane: 99 and 98; a
 // row after the other, its values across the lanes: 71, but 75 us against 66 for 32 drafts, whose joins are short.)
@@ -224,7 +227,7 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
         // Q: the lane's dims 32 b + 8 c4 .. + 7 of query n8 (of query n8 & 3, PACK), hi and lo
         constexpr int TERMS = PACK ? 1 : 2;
         uint32_t q[TERMS][NB][4];
-        float2 off[NB];  // - 8 sum q 2^-22 of a block, of queries 2 c4, 2 c4 + 1: what its products start from
+        float2 off[TERMS][NB];  // - 8 sum q 2^-22 of a block, of queries 2 c4, 2 c4 + 1: what its products start from
         float cf[2];
         const long long at = static_cast<long long>(walk_row(w, p)) * p.a.nh + head * g;  // row of token 0, query head 0
         {
@@ -244,25 +247,33 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
             am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
             const int sh = row_shift(am);
             const float f = pow2i(sh);
-            float sum[NB];
+            float sum[TERMS][NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                sum[b] = 0.0f;
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) sum[t][b] = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float4 y = x[b][k >> 1];
                     uint32_t hi, lo;
                     split2(((k & 1) ? y.z : y.x) * f, ((k & 1) ? y.w : y.y) * f, hi, lo);
                     if (PACK && n8 >= 4) hi = lo;
-                    const float2 a = h2f(hi), e = h2f(lo);
-                    sum[b] += PACK ? a.x + a.y : (a.x + e.x) + (a.y + e.y);
+                    const float2 a = h2f(hi);
+                    sum[0][b] += a.x + a.y;
+                    if constexpr (!PACK) {
+                        const float2 e = h2f(lo);
+                        sum[1][b] += e.x + e.y;
+                    }
                     // codes four bits up count sixteen times
                     const uint32_t sixteenth = 0x2c002c00u;
                     q[0][b][k] = (k & 1) ? h2mul(hi, sixteenth) : hi;
                     if constexpr (!PACK) q[1][b][k] = (k & 1) ? h2mul(lo, sixteenth) : lo;
                 }
-                sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 1);
-                sum[b] += __shfl_xor_sync(0xffffffffu, sum[b], 2);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) {
+                    sum[t][b] += __shfl_xor_sync(0xffffffffu, sum[t][b], 1);
+                    sum[t][b] += __shfl_xor_sync(0xffffffffu, sum[t][b], 2);
+                }
             }
             const float back = p.scale_log2 * pow2i(-sh);
 #pragma unroll
@@ -270,7 +281,9 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
                 const int from = (2 * c4 + e) * 4;
                 cf[e] = __shfl_sync(0xffffffffu, back, from) * 0x1p22f;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) (e ? off[b].y : off[b].x) = __shfl_sync(0xffffffffu, sum[b], from) * -0x1p-19f;
+                for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) (e ? off[t][b].y : off[t][b].x) = __shfl_sync(0xffffffffu, sum[t][b], from) * -0x1p-19f;
             }
         }
         float m[2] = {-INFINITY, -INFINITY};
@@ -321,7 +334,7 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
                 }
                 // ---- scores
                 // (in this order: every load, then every first product, every second one and the sums, so that each has
-                // the others' time to arrive)
+                // the others' time to arrive; lo's before hi's, in sums of their own)
                 Frag x[kSteps], d[kSteps][NB];
                 uint32_t y[kSteps][NB][2];
 #pragma unroll
@@ -331,7 +344,7 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
 #pragma unroll
                         for (int b = 0; b < NB; ++b) y[s][b][h] = ld32(krow + (16 * s + 8 * h) * G.pitch + b * 16 + c4 * 4);
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t)
+                for (int t = TERMS - 1; t >= 0; --t) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -340,21 +353,24 @@ __device__ __forceinline__ void compute(const unsigned char *ring, float *join, 
                             for (int b = 0; b < NB; ++b) {
                                 const uint32_t y0 = h ? y[s][b][0] >> 6 : y[s][b][0] << 2, y1 = h ? y[s][b][1] >> 6 : y[s][b][1] << 2;
                                 const uint32_t a[4] = {y0 & 0x003c003cu, y1 & 0x003c003cu, y0 & 0x03c003c0u, y1 & 0x03c003c0u};
-                                const uint32_t(&qq)[4] = q[TERMS - 1 - t][b];
-                                if (t == 0 && h == 0)
-                                    mma_from(d[s][b], off[b], a, qq[0], qq[1]);
+                                if (h == 0)
+                                    mma_from(d[s][b], off[t][b], a, q[t][b][0], q[t][b][1]);
                                 else
-                                    mma(d[s][b], a, qq[2 * h], qq[2 * h + 1]);
+                                    mma(d[s][b], a, q[t][b][2], q[t][b][3]);
                             }
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
+                    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const float2 f0 = h2f(ks[s][0][b >> 1]), f1 = h2f(ks[s][1][b >> 1]);
-                        const float s0 = (b & 1) ? f0.y : f0.x, s1 = (b & 1) ? f1.y : f1.x;
-                        x[s].lo = b == 0 ? mul2(d[s][b].lo, both(s0)) : make_float2(fmaf(d[s][b].lo.x, s0, x[s].lo.x), fmaf(d[s][b].lo.y, s0, x[s].lo.y));
-                        x[s].hi = b == 0 ? mul2(d[s][b].hi, both(s1)) : make_float2(fmaf(d[s][b].hi.x, s1, x[s].hi.x), fmaf(d[s][b].hi.y, s1, x[s].hi.y));
-                    }
+                        for (int b = 0; b < NB; ++b) {
+                            const float2 f0 = h2f(ks[s][0][b >> 1]), f1 = h2f(ks[s][1][b >> 1]);
+                            const float s0 = (b & 1) ? f0.y : f0.x, s1 = (b & 1) ? f1.y : f1.x;
+                            const bool first = t == TERMS - 1 && b == 0;
+                            x[s].lo = first ? mul2(d[s][b].lo, both(s0)) : make_float2(fmaf(d[s][b].lo.x, s0, x[s].lo.x), fmaf(d[s][b].lo.y, s0, x[s].lo.y));
+                            x[s].hi = first ? mul2(d[s][b].hi, both(s1)) : make_float2(fmaf(d[s][b].hi.x, s1, x[s].hi.x), fmaf(d[s][b].hi.y, s1, x[s].hi.y));
+                        }
+                }
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
                     if constexpr (PACK) {
                         x[s].lo = add2(x[s].lo, make_float2(__shfl_xor_sync(0xffffffffu, x[s].lo.x, 2), __shfl_xor_sync(0xffffffffu, x[s].lo.y, 2)));
                         x[s].hi = add2(x[s].hi, make_float2(__shfl_xor_sync(0xffffffffu, x[s].hi.x, 2), __shfl_xor_sync(0xffffffffu, x[s].hi.y, 2)));
