@@ -183,6 +183,16 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _q8_rows(w, k_reg, v_reg):
+    """Q8_0 and Q4 rows are both held as bytes, so the type does not tell them apart: regions that are too small for rows of
+    w Q8_0 values are refused."""
+    need = k_reg.shape[0] * (w + ((w // 32) * 2 + 15) // 16 * 16)
+    for name, t in (("K", k_reg), ("V", v_reg)):
+        if isinstance(t, torch.Tensor) and t.numel() < need:
+            raise ValueError(f"the {name} regions (pools) must hold {k_reg.shape[0]} Q8_0 rows of {w} values, {need} bytes, "
+                             f"they are {tuple(t.shape)}")
+
+
 # The current stream's handle without a Stream object around it (which takes 3 us of a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -285,6 +295,8 @@ def _layer_step(name, reg_dtype, xn, h, gain, eps, q, k, v, pos, k_reg, v_reg, n
                 theta, freq_scale, style, out, ws, err, stream):
     nt, n_embd = h.shape
     cap = k_reg.shape[0]
+    if reg_dtype is torch.uint8:
+        _q8_rows(n_kv_head * hd_kv, k_reg, v_reg)
     _check(getattr(lib(), name)(
         _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd,
         _dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"), _dev(pos, torch.int32, "pos"), nt,
@@ -436,6 +448,8 @@ def _decode_paged(name, out, q, k_pool, v_pool, block_table, block_rows, pos, n_
                   ws, err, stream):
     dt = _pool_dtype(name)
     n_seq, max_blocks = block_table.shape
+    if dt is torch.uint8:
+        _q8_rows(n_kv_head * hd_kv, k_pool, v_pool)
     _check(getattr(lib(), name)(
         _dev(out, name="out"), _dev(q, name="q"), _dev(k_pool, dt, "k_pool"), _dev(v_pool, dt, "v_pool"),
         k_pool.shape[0], _dev(block_table, torch.int32, "block_table"), max_blocks, block_rows,
@@ -460,6 +474,8 @@ def _step_paged(name, xn, h, gain, eps, q, k, v, pos, k_pool, v_pool, block_tabl
     dt = _pool_dtype(name)
     n_seq, n_embd = h.shape
     max_blocks = block_table.shape[1]
+    if dt is torch.uint8:
+        _q8_rows(n_kv_head * hd_kv, k_pool, v_pool)
     _check(getattr(lib(), name)(
         _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd,
         _dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"), _dev(pos, torch.int32, "pos"), n_seq,
@@ -484,6 +500,7 @@ def minf_layer_attn_step_paged_f16(xn, h, gain, eps, q, k, v, pos, k_pool, v_poo
 def minf_kv_append_paged_q8(k_pool, v_pool, block_table, block_rows, k_rows, v_rows, pos, err, stream=None):
     """Pools [pool_rows, minf_q8_row_bytes(W)] uint8; W is taken from k_rows."""
     n_seq, max_blocks = block_table.shape
+    _q8_rows(k_rows.shape[-1], k_pool, v_pool)
     _check(lib().minf_kv_append_paged_q8(
         _dev(k_pool, torch.uint8, "k_pool"), _dev(v_pool, torch.uint8, "v_pool"), k_pool.shape[0], k_rows.shape[-1],
         _dev(block_table, torch.int32, "block_table"), max_blocks, block_rows, _dev(k_rows, name="k_rows"),
@@ -514,6 +531,7 @@ def minf_q8_row_bytes(row_width: int) -> int:
 
 
 def minf_kv_append_q8(k_reg, v_reg, k_rows, v_rows, pos, err, stream=None):
+    _q8_rows(k_rows.shape[-1], k_reg, v_reg)
     _check(lib().minf_kv_append_q8(_dev(k_reg, _U8, "k_reg"), _dev(v_reg, _U8, "v_reg"), k_reg.shape[0],
                                    k_rows.shape[-1], _dev(k_rows, name="k_rows"), _dev(v_rows, name="v_rows"),
                                    _dev(pos, torch.int32, "pos"), pos.numel(), _dev(err, torch.int32, "err"),
@@ -522,6 +540,7 @@ def minf_kv_append_q8(k_reg, v_reg, k_rows, v_rows, pos, err, stream=None):
 
 def minf_rope_kv_append_q8(q, k, v, pos, n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style, k_reg, v_reg, err,
                            stream=None):
+    _q8_rows(n_kv_head * hd_kv, k_reg, v_reg)
     _check(lib().minf_rope_kv_append_q8(_dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"),
                                         _dev(pos, torch.int32, "pos"), pos.numel(), n_head, n_kv_head, hd, hd_kv,
                                         theta, freq_scale, style, _dev(k_reg, _U8, "k_reg"), _dev(v_reg, _U8, "v_reg"),
@@ -531,6 +550,7 @@ def minf_rope_kv_append_q8(q, k, v, pos, n_head, n_kv_head, hd, hd_kv, theta, fr
 
 def minf_gqa_attn_decode_q8(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap, pos, n_head, n_kv_head, hd, hd_kv,
                             scale, ws, err, stream=None):
+    _q8_rows(n_kv_head * hd_kv, k_reg, v_reg)
     _check(lib().minf_gqa_attn_decode_q8(
         _dev(out, name="out"), _dev(q, name="q"), _dev(k_reg, _U8, "k_reg"), _dev(v_reg, _U8, "v_reg"),
         _dev(seq_row_off, torch.int64, "seq_row_off"), _dev(seq_cap, torch.int32, "seq_cap"), max_cap,
@@ -540,6 +560,7 @@ def minf_gqa_attn_decode_q8(out, q, k_reg, v_reg, seq_row_off, seq_cap, max_cap,
 
 
 def minf_gqa_attn_prefill_q8(out, q, k_reg, v_reg, pos, n_head, n_kv_head, hd, hd_kv, scale, ws, err, stream=None):
+    _q8_rows(n_kv_head * hd_kv, k_reg, v_reg)
     _check(lib().minf_gqa_attn_prefill_q8(
         _dev(out, name="out"), _dev(q, name="q"), _dev(k_reg, _U8, "k_reg"), _dev(v_reg, _U8, "v_reg"),
         k_reg.shape[0], _dev(pos, torch.int32, "pos"), pos.numel(), n_head, n_kv_head, hd, hd_kv, scale,
@@ -549,6 +570,7 @@ def minf_gqa_attn_prefill_q8(out, q, k_reg, v_reg, pos, n_head, n_kv_head, hd, h
 
 def minf_layer_attn_step_q8(xn, h, gain, eps, q, k, v, pos, k_reg, v_reg, n_head, n_kv_head, hd, hd_kv, theta,
                             freq_scale, style, out, ws, err, stream=None):
+    _q8_rows(n_kv_head * hd_kv, k_reg, v_reg)
     nt, n_embd = h.shape
     _check(lib().minf_layer_attn_step_q8(
         _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd,
@@ -561,6 +583,7 @@ def minf_layer_attn_step_q8(xn, h, gain, eps, q, k, v, pos, k_reg, v_reg, n_head
 def minf_layer_attn_step_batched_q8(xn, h, gain, eps, q, k, v, pos, k_arena, v_arena, seq_row_off, seq_cap, max_cap,
                                     n_head, n_kv_head, hd, hd_kv, theta, freq_scale, style, out, ws, err,
                                     stream=None):
+    _q8_rows(n_kv_head * hd_kv, k_arena, v_arena)
     n_seq, n_embd = h.shape
     _check(lib().minf_layer_attn_step_batched_q8(
         _dev(xn, name="xn"), _dev(h, name="h"), _dev(gain, name="gain"), eps, n_embd,
