@@ -602,7 +602,8 @@ def minf_q4_row_bytes(row_width: int) -> int:
 
 
 def minf_kv_append_q4(k_reg, v_reg, k_rows, v_rows, pos, err, stream=None):
-    """Row t of k_rows, v_rows [nt, W] to row pos[t] of the regions (or of the pools, with a slot map as pos)."""
+    """Row t of k_rows, v_rows [nt, W] to row pos[t] of the regions (or of the pools, with a slot map as pos; in an arena
+    of a sequence's own rows, KvArena.seq_view, whose capacity the positions are checked against)."""
     w, here = k_rows.shape[-1], _here()
     _chunk_pool("_q4", k_reg, v_reg, None, 0, w)
     for name, t in (("k_rows", k_rows), ("v_rows", v_rows)):

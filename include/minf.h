@@ -425,6 +425,9 @@ MINF_API int minf_layer_attn_step_batched_q8(float *xn, const float *h, const fl
  * store never writes, are not supported.  The attention is the fp32 attention over the values.
  * minf_kv_append_q4: as minf_kv_append_q8; no two tokens at one position.  With a pool as the
  * regions (cap = pool_rows) and a slot map as pos (minf_block_table_grow) it writes paged rows.
+ * Positions are checked against cap and nothing else: in an arena, append to one sequence a call,
+ * with its first row as the regions and its own capacity (a position past it is then reported and not
+ * stored; as a row of the whole arena it would be the next sequence's).
  */
 MINF_API size_t minf_q4_row_bytes(int row_width); /* 0 when row_width is not a positive multiple of 32 */
 MINF_API int minf_kv_append_q4(uint8_t *k_reg, uint8_t *v_reg, int cap, int row_width, const float *k_rows,
