@@ -256,12 +256,8 @@ __device__ __forceinline__ void q8_pad(unsigned char *row, int W, long long rb) 
 // of a token, in order: q heads, k heads (8 values a unit) and v (4 values a unit, 8 over Q4).  Each count
 // is a multiple of 8 units (hd_kv 64 or 128; q's is rounded up), so the eight (or four) lanes that
 // share a Q8_0 or Q4 block are always active together.
-// (Eight blocks an SM: the Q4 store's registers stop at 32, where it would take 40: 60.3 us against 62.0.  Two pairs at a
-// time in packed instructions want more of them: 66.9, or 68.3 with 48.)
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 8) chunk_store_kernel(const ChunkStoreArgs a,
-                                                               const __grid_constant__ AxisTable tq,
-                                                               const __grid_constant__ AxisTable tk, int tok) {
+__device__ __forceinline__ void chunk_store(const ChunkStoreArgs &a, const AxisTable &tq, const AxisTable &tk, int tok) {
     constexpr bool kExact = std::is_same<T, Q4>::value;
     __shared__ float2 cq[kMaxTok][kMaxHalf];
     __shared__ std::conditional_t<kExact, float4, float2> ck[kMaxTok][kMaxHalf];
@@ -447,6 +443,20 @@ __global__ void __launch_bounds__(kThreads, 8) chunk_store_kernel(const ChunkSto
     }
 }
 
+template <typename T>
+__global__ void __launch_bounds__(kThreads) chunk_store_kernel(const ChunkStoreArgs a,
+                                                               const __grid_constant__ AxisTable tq,
+                                                               const __grid_constant__ AxisTable tk, int tok) {
+    chunk_store<T>(a, tq, tk, tok);
+}
+// (Eight blocks an SM: the Q4 store's registers stop at 32, where it would take 40: 60.3 us against 62.0.  Two pairs at a
+// time in packed instructions want more of them: 66.9, or 68.3 with 48.  The other types stay below 32 unasked.)
+__global__ void __launch_bounds__(kThreads, 8) chunk_store_q4_kernel(const ChunkStoreArgs a,
+                                                                     const __grid_constant__ AxisTable tq,
+                                                                     const __grid_constant__ AxisTable tk, int tok) {
+    chunk_store<Q4>(a, tq, tk, tok);
+}
+
 // ----------------------------------------------------------------------------- read back
 // Row t of the outputs is the cached row of the chunk's token t, converted to fp32 or binary16.
 template <typename T, bool kF16>
@@ -535,7 +545,7 @@ int launch_chunk_store(const ChunkStoreArgs &a, float theta, float freq_scale, c
     dim3 grid;
     row_grid(a.sq.nt, static_cast<long long>(a.nh) * (a.hd / 8) + a.nk * (a.hd_kv / 8) + a.c.W / 4, tok, grid);
     if (a.c.kv == kKvQ4)
-        chunk_store_kernel<Q4><<<grid, kThreads, 0, s>>>(a, tq, tk, tok);
+        chunk_store_q4_kernel<<<grid, kThreads, 0, s>>>(a, tq, tk, tok);
     else if (a.c.kv == kKvQ8)
         chunk_store_kernel<Q8><<<grid, kThreads, 0, s>>>(a, tq, tk, tok);
     else if (a.c.kv == kKvF16)
