@@ -2,6 +2,7 @@
 // attention (offsets, positions, pool rows, blocks from the free list) from the sequences' lengths, and blocks given
 // back.
 //
+// The list of free blocks is a stack: its last id goes out first, and of what comes back the first is its last again.
 // With B rows a block, sequence s holds held_s = ceil(past_s / B) blocks and needs ceil((past_s + new_s) / B); the sums
 // over the sequences before it say where its tokens (chunk_off) and its new blocks on the list begin.  A few thousand
 // sums and 8 bytes a token are latency, not bandwidth: so one launch, and nothing that goes through memory between its

@@ -149,7 +149,7 @@ __device__ __forceinline__ void mma0(Frag &d, uint32_t a0, uint32_t a1, uint32_t
         : "=f"(d.lo.x), "=f"(d.lo.y), "=f"(d.hi.x), "=f"(d.hi.y)
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {  // (transpose8 of minf_warp_mma.cuh, free to move)
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;

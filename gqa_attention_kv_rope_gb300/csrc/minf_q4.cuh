@@ -84,7 +84,9 @@ __device__ __forceinline__ float4 ld4_q4(const unsigned char *row, int W, int i4
 }
 
 // The eight values of a word as half2 pairs, in order; d2: the scale in both halves.  A nibble under 0x6400 is 1024 + u
-// (or 1024 + 16 u where it stands four bits higher), u - 8 is exact, and so is its product with d.
+// (or 1024 + 16 u where it stands four bits higher), u - 8 is exact, and so is its product with d.  (Codes put under a
+// binary16 number's exponent, the bias taken off in arithmetic: Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't
+// Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022.)
 __device__ __forceinline__ uint32_t q4_lop(uint32_t w, uint32_t mask) {  // (w & mask) | 0x64006400
     uint32_t y;
     asm("lop3.b32 %0, %1, %2, 0x64006400, 0xea;" : "=r"(y) : "r"(w), "r"(mask));
